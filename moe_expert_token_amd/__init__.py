@@ -1,6 +1,8 @@
-"""MoE token shuffle for AMD MI355X (gfx950): plan, dispatch, combine.
+"""MoE token shuffle for AMD MI355X (gfx950): plan, dispatch, combine, and the
+experts' gated feed-forward block in between.
 
-A thin Python face of the C ABI in include/moe_shuffle.h; every step runs in
+A thin Python face of the C ABI in include/moe_shuffle.h and
+include/moe_experts.h; every step runs in
 the HIP kernels of libmoe_shuffle.so.  Tensors are torch tensors on the GPU;
 bf16 activations may be torch.bfloat16 or any 16-bit view of the same bits.
 """
@@ -14,4 +16,9 @@ from ._lib import (  # noqa: F401
     moe_shuffle_combine_rank_partial, moe_shuffle_combine_backward, moe_shuffle_dispatch_range,
     moe_shuffle_combine_range, moe_shuffle_combine_rank_partial_f32, moe_shuffle_copy_reference,
     moe_shuffle_plan_static, PlanStorage, STATIC_WORKSPACE_BYTES,
+)
+from .experts import (  # noqa: F401
+    ACT_GELU_TANH, ACT_SILU, EXPERTS_EXPORTS, GROUP8, moe_experts_ffn_backward, moe_experts_ffn_forward,
+    moe_experts_ffn_w4_forward, moe_experts_ffn_workspace_size, moe_experts_pack8, moe_experts_unpack8,
+    moe_experts_w4_quantize,
 )

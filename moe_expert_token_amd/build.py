@@ -14,7 +14,9 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libmoe_shuffle.so")
-SOURCES = [os.path.join(CSRC, f) for f in ("abi.hip", "plan.hip", "rows.hip", "reduce.hip", "combine_bwd.hip", "copy_ref.hip")]
+SOURCES = [os.path.join(CSRC, f) for f in ("abi.hip", "plan.hip", "rows.hip", "reduce.hip", "combine_bwd.hip", "copy_ref.hip",
+                                               "experts_abi.hip", "experts_ffn.hip", "experts_w4.hip",
+                                               "experts_pack.hip")]
 ARCH = os.environ.get("MOE_SHUFFLE_ARCH", "gfx950")
 
 HIPCC_FLAGS = [

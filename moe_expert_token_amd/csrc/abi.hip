@@ -13,14 +13,6 @@
 #include "internal.h"
 #include "moe_shuffle.h"
 
-struct moe_shuffle_plan_s {
-    moe_shuffle_dims dims;
-    ms::Layout L;
-    char* ws;
-    int64_t n_known;  // N after moe_shuffle_plan_query, else -1
-    int owned;        // 1: allocated by moe_shuffle_plan (destroy frees it); 0: in caller storage
-};
-
 static_assert(sizeof(moe_shuffle_plan_s) <= sizeof(moe_shuffle_plan_storage),
               "the plan handle must fit the caller's storage");
 static_assert(alignof(moe_shuffle_plan_s) <= alignof(moe_shuffle_plan_storage),
@@ -36,29 +28,11 @@ namespace {
 
 thread_local int g_last_hip_error = 0;
 
-int hip_fail(hipError_t e)
-{
-    g_last_hip_error = (int)e;
-    return MOE_SHUFFLE_E_HIP;
-}
+using ms::hip_fail;
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-int check_dims(const moe_shuffle_dims* d)
-{
-    if (!d) return MOE_SHUFFLE_E_INVALID_ARG;
-    if (d->num_tokens < 0 || d->hidden <= 0 || d->num_experts <= 0 || d->top_k <= 0 || d->num_ranks <= 0)
-        return MOE_SHUFFLE_E_INVALID_ARG;
-    if (d->top_k > d->num_experts || d->num_experts % d->num_ranks != 0) return MOE_SHUFFLE_E_INVALID_ARG;
-    if (d->hidden % 8 != 0) return MOE_SHUFFLE_E_ALIGN;
-    if ((int64_t)d->num_tokens * d->top_k >= ((int64_t)1 << 31)) return MOE_SHUFFLE_E_OVERFLOW;
-    if (d->top_k > ms::kMaxTopK || d->num_experts + d->num_ranks > ms::kMaxCols) return MOE_SHUFFLE_E_OVERFLOW;
-    // kernels index 512-element pieces of rows with int: every row count
-    // (at most T*k) times the pieces per row must stay below 2^31
-    const int64_t pieces = ((int64_t)d->hidden / 8 + ms::kWave - 1) / ms::kWave;
-    if ((int64_t)d->num_tokens * d->top_k * pieces + 64 >= ((int64_t)1 << 31)) return MOE_SHUFFLE_E_OVERFLOW;
-    return MOE_SHUFFLE_OK;
-}
+using ms::check_dims;
 
 bool misaligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) != 0; }
 
@@ -85,6 +59,28 @@ int64_t rank_rows_needed(const moe_shuffle_plan_s* p)
 }  // namespace
 
 namespace ms {
+
+int hip_fail(hipError_t e)
+{
+    g_last_hip_error = (int)e;
+    return MOE_SHUFFLE_E_HIP;
+}
+
+int check_dims(const moe_shuffle_dims* d)
+{
+    if (!d) return MOE_SHUFFLE_E_INVALID_ARG;
+    if (d->num_tokens < 0 || d->hidden <= 0 || d->num_experts <= 0 || d->top_k <= 0 || d->num_ranks <= 0)
+        return MOE_SHUFFLE_E_INVALID_ARG;
+    if (d->top_k > d->num_experts || d->num_experts % d->num_ranks != 0) return MOE_SHUFFLE_E_INVALID_ARG;
+    if (d->hidden % 8 != 0) return MOE_SHUFFLE_E_ALIGN;
+    if ((int64_t)d->num_tokens * d->top_k >= ((int64_t)1 << 31)) return MOE_SHUFFLE_E_OVERFLOW;
+    if (d->top_k > ms::kMaxTopK || d->num_experts + d->num_ranks > ms::kMaxCols) return MOE_SHUFFLE_E_OVERFLOW;
+    // kernels index 512-element pieces of rows with int: every row count
+    // (at most T*k) times the pieces per row must stay below 2^31
+    const int64_t pieces = ((int64_t)d->hidden / 8 + ms::kWave - 1) / ms::kWave;
+    if ((int64_t)d->num_tokens * d->top_k * pieces + 64 >= ((int64_t)1 << 31)) return MOE_SHUFFLE_E_OVERFLOW;
+    return MOE_SHUFFLE_OK;
+}
 
 void make_layout(const moe_shuffle_dims& d, Layout& L)
 {

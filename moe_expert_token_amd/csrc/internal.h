@@ -31,8 +31,14 @@ struct Layout {
     size_t total;
 };
 
+// MOE_SHUFFLE_OK, or the status code that these dims are refused with.
+int check_dims(const moe_shuffle_dims* d);
+
 // Fills `L` from validated dims.
 void make_layout(const moe_shuffle_dims& d, Layout& L);
+
+// Notes the calling thread's HIP error; returns MOE_SHUFFLE_E_HIP.
+int hip_fail(hipError_t e);
 
 struct PlanPtrs {
     const int32_t* idx;
@@ -86,3 +92,11 @@ hipError_t launch_combine_backward(const void* grad_out, const void* ye, const f
 hipError_t launch_copy_reference(const void* src, void* dst, int64_t n_vectors, hipStream_t s);
 
 }  // namespace ms
+
+struct moe_shuffle_plan_s {
+    moe_shuffle_dims dims;
+    ms::Layout L;
+    char* ws;
+    int64_t n_known;  // N after moe_shuffle_plan_query, else -1
+    int owned;        // 1: allocated by moe_shuffle_plan (destroy frees it); 0: in caller storage
+};

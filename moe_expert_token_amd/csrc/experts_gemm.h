@@ -84,6 +84,7 @@ __device__ __forceinline__ void wait_loads() { __builtin_amdgcn_s_waitcnt(0x0f70
 //   LDS: [256][64] bf16; the 16-byte piece c of row r lies at piece c ^ (r & 7), so that the eight lanes of a
 //   fragment read that are served together fall on all banks.
 struct KContiguous {
+    static constexpr int kReads = 1;  // LDS instructions a fragment
     const char* p;     // (row 0, k 0)
     unsigned ld;       // bytes from row to row
     unsigned bytes;    // from p to the end of the last valid row
@@ -135,6 +136,7 @@ struct KContiguous {
 //   LDS: [64][256] bf16; the 32-byte piece c of row k lies at piece c ^ (k & 3 | (k >> 3 & 3) << 2): the sixteen
 //   rows of a transposing read (four of every eight) fall on different banks.
 struct KStrided {
+    static constexpr int kReads = 2;
     const char* p;     // (k 0, feature 0 of the tile)
     unsigned ld;       // bytes from k to k + 1
     int K;
@@ -181,6 +183,17 @@ struct KStrided {
     }
 };
 
+// Asks for `Reads` LDS reads spread among `Products` matrix instructions, so that both proceed.
+template <int Reads, int Products, int I = 0>
+__device__ __forceinline__ void interleave()
+{
+    if constexpr (I < Reads) {
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, (I + 1) * Products / Reads - I * Products / Reads, 0);
+        interleave<Reads, Products, I + 1>();
+    }
+}
+
 template <int MF>
 using Acc = f32x4[MF][4];
 
@@ -200,23 +213,36 @@ __device__ __forceinline__ void tile_product(const R& r, const F& f, int K, char
         r.template load<(MF + 1) / 2>(kt, at);
         f.template load<4>(kt, at + kOperandBytes);
     };
-    start(0);
-    wait_loads();
-    __syncthreads();
-    for (int kt = 0; kt < nk; ++kt) {
-        start(kt + 1);
+    bf16x8 ra[2][MF], fa[2][4];
+    const auto fragments = [&](int kt, int half) {
         const char* const at = lds + (kt & 1) * 2 * kOperandBytes;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            bf16x8 ra[MF], fa[4];
+        for (int n = 0; n < 4; ++n) fa[half][n] = F::fragment(at + kOperandBytes, wf * 64 + n * 16, half);
 #pragma unroll
-            for (int n = 0; n < 4; ++n) fa[n] = F::fragment(at + kOperandBytes, wf * 64 + n * 16, half);
+        for (int m = 0; m < MF; ++m) ra[half][m] = R::fragment(at, (wr * MF + m) * 16, half);
+    };
+    const auto multiply = [&](int half) {
 #pragma unroll
-            for (int m = 0; m < MF; ++m) ra[m] = R::fragment(at, (wr * MF + m) * 16, half);
+        for (int m = 0; m < MF; ++m)
 #pragma unroll
-            for (int m = 0; m < MF; ++m)
-#pragma unroll
-                for (int n = 0; n < 4; ++n) acc[m][n] = mfma_16x16x32(fa[n], ra[m], acc[m][n]);
+            for (int n = 0; n < 4; ++n) acc[m][n] = mfma_16x16x32(fa[half][n], ra[half][m], acc[m][n]);
+    };
+    if (nk > 0) {
+        start(0);
+        start(1);
+        wait_loads();
+        __syncthreads();
+        fragments(0, 0);
+        for (int kt = 0; kt < nk; ++kt) {
+            fragments(kt, 1);
+            multiply(0);
+            interleave<MF * R::kReads + 4 * F::kReads, 4 * MF>();
+            wait_loads();
+            __syncthreads();
+            start(kt + 2);
+            fragments(kt + 1, 0);
+            multiply(1);
+            interleave<MF * R::kReads + 4 * F::kReads, 4 * MF>();
         }
         wait_loads();
         __syncthreads();

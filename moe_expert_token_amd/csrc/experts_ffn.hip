@@ -10,12 +10,6 @@ namespace {
 
 __device__ __forceinline__ u32x2 pack4(f32x4 v) { return u32x2{bf16_pack2(v[0], v[1]), bf16_pack2(v[2], v[3])}; }
 
-__device__ __forceinline__ f32x4 load4(const void* p, int64_t at)
-{
-    const u32x2 u = *(const u32x2*)((const unsigned short*)p + at);
-    return f32x4{bf16_lo(u[0]), bf16_hi(u[0]), bf16_lo(u[1]), bf16_hi(u[1])};
-}
-
 // A staged output tile: rows of `Bytes` bytes in LDS, their 16-byte pieces permuted by the row so that the sixteen
 // rows a wave writes at once spread over the banks; from there rows go out whole.
 template <int Bytes>
@@ -25,15 +19,27 @@ struct Stage {
         return lds + row * Bytes + (((byte >> 4) ^ (row & 7)) << 4) + (byte & 15);
     }
 
-    // Rows [0, nr) and bytes [0, valid) of the tile to out + row * ld; Vec divides valid and the rows' alignment.
-    template <class Vec>
+    // Rows [0, nr) of at most 32 MF and bytes [0, valid) of the tile to out + row * ld; Vec divides valid and the
+    // rows' alignment.
+    template <class Vec, int MF>
     static __device__ __forceinline__ void store(const char* lds, int nr, int valid, char* out, int64_t ld)
     {
         constexpr int kLanes = Bytes / (int)sizeof(Vec), kRows = kGemmThreads / kLanes;
-        const int b = (int)(threadIdx.x % kLanes) * (int)sizeof(Vec);
+        constexpr int kTurns = (32 * MF + kRows - 1) / kRows, kBatch = kTurns < 4 ? kTurns : 4;
+        const int b = (int)(threadIdx.x % kLanes) * (int)sizeof(Vec), r0 = threadIdx.x / kLanes;
         if (b >= valid) return;
-        for (int r = threadIdx.x / kLanes; r < nr; r += kRows)
-            *(Vec*)(out + r * ld + b) = *(const Vec*)at((char*)lds, r, b);
+#pragma unroll
+        for (int t = 0; t < kTurns; t += kBatch) {
+            Vec v[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i)
+                v[i] = *(const Vec*)at((char*)lds, min(r0 + (t + i) * kRows, 32 * MF - 1), b);
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int r = r0 + (t + i) * kRows;
+                if (r < nr) *(Vec*)(out + r * ld + b) = v[i];
+            }
+        }
     }
 };
 
@@ -69,6 +75,15 @@ __device__ __forceinline__ void with_rows(int nr, F&& f)
     }
 }
 
+// The slots of nr rows of `width` elements from `first`.
+template <int MF>
+__device__ __forceinline__ void row_slots(KContiguous& r, const char* first, int width, int nr)
+{
+    constexpr int kFirst = 32 * ((MF + 1) / 2);
+    r.slot(0, first, min(nr, kFirst));
+    r.slot(1, first + (int64_t)kFirst * width * 2, nr - kFirst);
+}
+
 // ---- the kernels ----
 
 // Largest magnitude over the 32 features that the four lanes of a row hold in a and b; infinity if any is not
@@ -94,28 +109,30 @@ __global__ __launch_bounds__(kGemmThreads, 2) void ffn_up_kernel(ExpertShape S, 
                                                                  char* h, SavedActs saved, int across, GridSpan span)
 {
     __shared__ __align__(1024) char lds[kGemmLds];
-    if (*S.status) return;
     const Place at = place_of(span, across);
     int row0, nr;
-    const int e = segment_tile(S.offset, S.E, kTileRows, 32, at.tile, &row0, &nr);
-    if (e < 0) return;
+    const int bad = *S.status, e = segment_tile(S.offset, S.E, kTileRows, 32, at.tile, &row0, &nr);
+    if (bad || e < 0) return;
     const int c0 = at.across * kUpFeatures, H = S.H, I = S.I;
-    KContiguous r, f;
-    r.init(xe + (int64_t)row0 * H * 2, H, nr, H);
-    // 64 LDS rows are 32 gate rows (loaded by waves 0 .. 3) and the 32 up rows of the same features: one wave's
     const int valid = min(kUpFeatures, I - c0);
-    f.init(w + ((int64_t)e * 2 * I + c0 + (wave_id() >= 4 ? I : 0)) * H * 2, H, valid, H, 32, (threadIdx.x >> 3) & 31);
-    const int lane = lane_id(), wr = wave_id() >> 2, wf = wave_id() & 3, groups = (I + kGroup8 - 1) / kGroup8;
+    KContiguous r, f;
+    r.init(H, H);
+    f.init(H, H);
+    // F0 is the gate's rows, F1 the up projection's: a wave gets both of the same features
+    f.slot(0, w + ((int64_t)e * 2 * I + c0) * H * 2, valid);
+    f.slot(1, w + ((int64_t)e * 2 * I + I + c0) * H * 2, valid);
+    const int lane = lane_id(), wf = wave_id() & 3, groups = (I + kGroup8 - 1) / kGroup8;
     with_rows(nr, [&](auto mf) {
         constexpr int MF = decltype(mf)::value;
         Acc<MF> acc;
+        row_slots<MF>(r, xe + (int64_t)row0 * H * 2, H, nr);
         tile_product<MF>(r, f, H, lds, acc);
         typedef Stage<kUpFeatures * 2> Wide;
         typedef Stage<kUpFeatures> Narrow;
         char* const second = lds + 256 * kUpFeatures * 2;
 #pragma unroll
         for (int m = 0; m < MF; ++m) {
-            const int row = 16 * (MF * wr + m) + (lane & 15);
+            const int row = row_of<MF>(m) + (lane & 15);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int c = 32 * wf + 16 * i + 4 * (lane >> 4);
@@ -143,43 +160,43 @@ __global__ __launch_bounds__(kGemmThreads, 2) void ffn_up_kernel(ExpertShape S, 
             }
         }
         __syncthreads();
-        Wide::store<u32x4>(lds, nr, 2 * valid, h + ((int64_t)row0 * I + c0) * 2, (int64_t)I * 2);
+        Wide::store<u32x4, MF>(lds, nr, 2 * valid, h + ((int64_t)row0 * I + c0) * 2, (int64_t)I * 2);
         if (!saved.data) return;
         char* const out = (char*)saved.data + ((int64_t)row0 * 2 * I + c0) * (saved.scale ? 1 : 2);
         if (saved.scale) {
-            Narrow::store<u32x2>(second, nr, valid, out, (int64_t)2 * I);
-            Narrow::store<u32x2>(second + 256 * kUpFeatures, nr, valid, out + I, (int64_t)2 * I);
+            Narrow::store<u32x2, MF>(second, nr, valid, out, (int64_t)2 * I);
+            Narrow::store<u32x2, MF>(second + 256 * kUpFeatures, nr, valid, out + I, (int64_t)2 * I);
             return;
         }
-        Wide::store<u32x4>(second, nr, 2 * valid, out, (int64_t)4 * I);
+        Wide::store<u32x4, MF>(second, nr, 2 * valid, out, (int64_t)4 * I);
         __syncthreads();
 #pragma unroll
         for (int m = 0; m < MF; ++m)
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-                *(u32x2*)Wide::at(lds, 16 * (MF * wr + m) + (lane & 15), 2 * (32 * wf + 16 * i + 4 * (lane >> 4))) =
+                *(u32x2*)Wide::at(lds, row_of<MF>(m) + (lane & 15), 2 * (32 * wf + 16 * i + 4 * (lane >> 4))) =
                     pack4(acc[m][2 + i]);
         __syncthreads();
-        Wide::store<u32x4>(lds, nr, 2 * valid, out + (int64_t)2 * I, (int64_t)4 * I);
+        Wide::store<u32x4, MF>(lds, nr, 2 * valid, out + (int64_t)2 * I, (int64_t)4 * I);
     });
 }
 
 typedef Stage<kTileFeatures * 2> WideStage;
 
-// The accumulators, put through `value` (m, n, row, feature, acc) -> packed bf16, to rows of `out`.
+// The packed values of each (m, n) to rows of `out`.
 template <int MF, class Value>
 __device__ __forceinline__ void write_tile(char* lds, int nr, int valid, char* out, int64_t ld, Value value)
 {
-    const int lane = lane_id(), wr = wave_id() >> 2, wf = wave_id() & 3;
+    const int lane = lane_id();
 #pragma unroll
     for (int m = 0; m < MF; ++m)
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
-            const int row = 16 * (MF * wr + m) + (lane & 15), c = 64 * wf + 16 * n + 4 * (lane >> 4);
-            *(u32x2*)WideStage::at(lds, row, 2 * c) = value(m, n, row, c);
+            const int row = row_of<MF>(m) + (lane & 15), c = feature_of(n) + 4 * (lane >> 4);
+            *(u32x2*)WideStage::at(lds, row, 2 * c) = value(m, n);
         }
     __syncthreads();
-    WideStage::store<u32x4>(lds, nr, 2 * valid, out, ld);
+    WideStage::store<u32x4, MF>(lds, nr, 2 * valid, out, ld);
 }
 
 // out[row] = in[row] F^T for the rows of every expert; in [P, K], out [P, N], F of an expert [N][K] (or, Strided,
@@ -190,24 +207,107 @@ __global__ __launch_bounds__(kGemmThreads, 2) void ffn_rows_kernel(ExpertShape S
                                                                    GridSpan span)
 {
     __shared__ __align__(1024) char lds[kGemmLds];
-    if (*S.status) return;
     const Place at = place_of(span, across);
     int row0, nr;
-    const int e = segment_tile(S.offset, S.E, kTileRows, 32, at.tile, &row0, &nr);
-    if (e < 0) return;
+    const int bad = *S.status, e = segment_tile(S.offset, S.E, kTileRows, 32, at.tile, &row0, &nr);
+    if (bad || e < 0) return;
     const int n0 = at.across * kTileFeatures;
     KContiguous r;
-    r.init(in + (int64_t)row0 * K * 2, K, nr, K);
+    r.init(K, K);
     typename std::conditional<Strided, KStrided, KContiguous>::type f;
-    if constexpr (Strided) f.init(w + ((int64_t)e * K * N + n0) * 2, N, N - n0, K);
-    else f.init(w + ((int64_t)e * N + n0) * K * 2, K, min(N - n0, kTileFeatures), K);
+    f.init(Strided ? N : K, K);
+    for (int i = 0; i < 2; ++i) {
+        const int n = n0 + 128 * i;
+        f.slot(i, w + (Strided ? (int64_t)e * K * N + n : ((int64_t)e * N + n) * K) * 2, N - n);
+    }
     with_rows(nr, [&](auto mf) {
         constexpr int MF = decltype(mf)::value;
         Acc<MF> acc;
+        row_slots<MF>(r, in + (int64_t)row0 * K * 2, K, nr);
         tile_product<MF>(r, f, K, lds, acc);
         write_tile<MF>(lds, nr, min(N - n0, kTileFeatures), out + ((int64_t)row0 * N + n0) * 2, (int64_t)N * 2,
-                       [&](int m, int n, int, int) { return pack4(acc[m][n]); });
+                       [&](int m, int n) { return pack4(acc[m][n]); });
     });
+}
+
+// Fragment rows [M0, M0 + MC) of dh, a slot's, with the saved pre-activations to dg, du and h.
+template <int M0, int MC, int MF>
+__device__ __forceinline__ void dh_rows(const ExpertShape& S, char* lds, const Acc<MF>& acc, const SavedActs& saved,
+                                        int row0, int nr, int n0, int valid, char* h, char* dgu)
+{
+    constexpr int kHalf = 128 * kTileFeatures * 2, kFirst = M0 ? 32 * ((MF + 1) / 2) : 0;
+    const int lane = lane_id(), I = S.I, groups = (I + kGroup8 - 1) / kGroup8;
+    struct Held {
+        u32x2 g, u;
+        unsigned sg, su;
+    };
+    // rows and features outside the tile read their nearest neighbours: their results go nowhere
+    const auto fetch = [&](int i, Held (&to)[4]) {
+        const int64_t row = row0 + min(row_of<MF>(M0 + i) + (lane & 15), nr - 1);
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            const int c = min(n0 + feature_of(n) + 4 * (lane >> 4), I - 4);
+            const char* const from = (const char*)saved.data + (row * 2 * I + c) * (saved.scale ? 1 : 2);
+            if (saved.scale) {
+                to[n].g[0] = *(const unsigned*)from;
+                to[n].u[0] = *(const unsigned*)(from + I);
+                const unsigned short* const sc = (const unsigned short*)saved.scale + row * 2 * groups + c / kGroup8;
+                to[n].sg = sc[0];
+                to[n].su = sc[groups];
+            } else {
+                to[n].g = *(const u32x2*)from;
+                to[n].u = *(const u32x2*)(from + 2 * I);
+            }
+        }
+    };
+    Held held[2][4];
+    u32x2 hv[MC][4];
+    fetch(0, held[0]);
+#pragma unroll
+    for (int i = 0; i < MC; ++i) {
+        if (i + 1 < MC) fetch(i + 1, held[(i + 1) & 1]);
+        const int row = row_of<MF>(M0 + i) - kFirst + (lane & 15);
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            const Held& q = held[i & 1][n];
+            f32x4 g, u, vg, vu, vh;
+            if (saved.scale) {
+                const float sg = __uint_as_float(q.sg << 16), su = __uint_as_float(q.su << 16);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) { g[j] = int8_of(q.g[0], j) * sg; u[j] = int8_of(q.u[0], j) * su; }
+            } else {
+                g = f32x4{bf16_lo(q.g[0]), bf16_hi(q.g[0]), bf16_lo(q.g[1]), bf16_hi(q.g[1])};
+                u = f32x4{bf16_lo(q.u[0]), bf16_hi(q.u[0]), bf16_lo(q.u[1]), bf16_hi(q.u[1])};
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float slope;
+                const float d = acc[M0 + i][n][j], s = gate_sigmoid(g[j], S.c0, S.c1, &slope), a = g[j] * s;
+                vh[j] = a * u[j];
+                vu[j] = d * a;
+                vg[j] = d * u[j] * fmaf(a * (1.0f - s), slope, s);
+            }
+            const int c = feature_of(n) + 4 * (lane >> 4);
+            *(u32x2*)WideStage::at(lds, row, 2 * c) = pack4(vg);
+            *(u32x2*)WideStage::at(lds + kHalf, row, 2 * c) = pack4(vu);
+            hv[i][n] = pack4(vh);
+        }
+    }
+    __syncthreads();
+    const int64_t first = row0 + kFirst;
+    char* const out = dgu + (first * 2 * I + n0) * 2;
+    WideStage::store<u32x4, MC>(lds, nr - kFirst, 2 * valid, out, (int64_t)I * 4);
+    WideStage::store<u32x4, MC>(lds + kHalf, nr - kFirst, 2 * valid, out + 2 * I, (int64_t)I * 4);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < MC; ++i)
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+            *(u32x2*)WideStage::at(lds, row_of<MF>(M0 + i) - kFirst + (lane & 15), 2 * (feature_of(n) + 4 * (lane >> 4))) =
+                hv[i][n];
+    __syncthreads();
+    WideStage::store<u32x4, MC>(lds, nr - kFirst, 2 * valid, h + (first * I + n0) * 2, (int64_t)I * 2);
+    __syncthreads();
 }
 
 __global__ __launch_bounds__(kGemmThreads, 2) void ffn_dh_kernel(ExpertShape S, const char* gy, const char* w,
@@ -215,55 +315,26 @@ __global__ __launch_bounds__(kGemmThreads, 2) void ffn_dh_kernel(ExpertShape S, 
                                                                  GridSpan span)
 {
     __shared__ __align__(1024) char lds[kGemmLds];
-    if (*S.status) return;
     const Place at = place_of(span, across);
     int row0, nr;
-    const int e = segment_tile(S.offset, S.E, kTileRows, 32, at.tile, &row0, &nr);
-    if (e < 0) return;
-    const int n0 = at.across * kTileFeatures, H = S.H, I = S.I, groups = (I + kGroup8 - 1) / kGroup8;
+    const int bad = *S.status, e = segment_tile(S.offset, S.E, kTileRows, 32, at.tile, &row0, &nr);
+    if (bad || e < 0) return;
+    const int n0 = at.across * kTileFeatures, H = S.H, I = S.I;
     KContiguous r;
     KStrided f;
-    r.init(gy + (int64_t)row0 * H * 2, H, nr, H);
-    f.init(w + ((int64_t)e * H * I + n0) * 2, I, I - n0, H);
+    r.init(H, H);
+    f.init(I, H);
+    for (int i = 0; i < 2; ++i) f.slot(i, w + ((int64_t)e * H * I + n0 + 128 * i) * 2, I - n0 - 128 * i);
     const int valid = min(I - n0, kTileFeatures);
     with_rows(nr, [&](auto mf) {
         constexpr int MF = decltype(mf)::value;
         Acc<MF> acc;
+        row_slots<MF>(r, gy + (int64_t)row0 * H * 2, H, nr);
         tile_product<MF>(r, f, H, lds, acc);
-        // each pass reads the saved pre-activations again (from the caches) rather than hold three tiles
-#pragma unroll 1
-        for (int pass = 0; pass < 3; ++pass) {
-            char* const out = pass == 0 ? h + ((int64_t)row0 * I + n0) * 2
-                                        : dgu + ((int64_t)row0 * 2 * I + (pass == 1 ? 0 : I) + n0) * 2;
-            write_tile<MF>(lds, nr, valid, out, (int64_t)I * (pass == 0 ? 2 : 4), [&](int m, int n, int row, int c) {
-                f32x4 g = {0, 0, 0, 0}, u = {0, 0, 0, 0};
-                if (row < nr && c < valid) {
-                    const int64_t at = (int64_t)(row0 + row) * 2 * I + n0 + c;
-                    if (saved.scale) {
-                        const unsigned short* sc =
-                            (const unsigned short*)saved.scale + (int64_t)(row0 + row) * 2 * groups + (n0 + c) / kGroup8;
-                        const float sg = __uint_as_float((unsigned)sc[0] << 16);
-                        const float su = __uint_as_float((unsigned)sc[groups] << 16);
-                        const unsigned qg = *(const unsigned*)((const char*)saved.data + at);
-                        const unsigned qu = *(const unsigned*)((const char*)saved.data + at + I);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) { g[j] = int8_of(qg, j) * sg; u[j] = int8_of(qu, j) * su; }
-                    } else {
-                        g = load4(saved.data, at);
-                        u = load4(saved.data, at + I);
-                    }
-                }
-                f32x4 v;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    float slope;
-                    const float s = gate_sigmoid(g[j], S.c0, S.c1, &slope), a = g[j] * s, d = acc[m][n][j];
-                    v[j] = pass == 0 ? a * u[j] : pass == 1 ? d * u[j] * fmaf(a * (1.0f - s), slope, s) : d * a;
-                }
-                return pack4(v);
-            });
-            __syncthreads();
-        }
+        // a slot's rows at a time: dg and du go through LDS side by side, then h
+        constexpr int A = (MF + 1) / 2;
+        dh_rows<0, A>(S, lds, acc, saved, row0, nr, n0, valid, h, dgu);
+        if constexpr (MF > A) dh_rows<A, MF - A>(S, lds, acc, saved, row0, nr, n0, valid, h, dgu);
     });
 }
 
@@ -279,13 +350,17 @@ __global__ __launch_bounds__(kGemmThreads, 2) void ffn_wgrad_kernel(ExpertShape 
     if (e >= S.E) return;
     const int q0 = S.offset[e], rows = S.offset[e + 1] - q0;
     KStrided r, f;
-    r.init(a + ((int64_t)q0 * na + m0) * 2, na, na - m0, rows);
-    f.init(b + ((int64_t)q0 * nb + n0) * 2, nb, nb - n0, rows);
+    r.init(na, rows);
+    f.init(nb, rows);
+    for (int i = 0; i < 2; ++i) {
+        r.slot(i, a + ((int64_t)q0 * na + m0 + 128 * i) * 2, na - m0 - 128 * i);
+        f.slot(i, b + ((int64_t)q0 * nb + n0 + 128 * i) * 2, nb - n0 - 128 * i);
+    }
     Acc<8> acc;
     tile_product<8>(r, f, rows, lds, acc);
     write_tile<8>(lds, min(na - m0, kTileRows), min(nb - n0, kTileFeatures),
                   out + (((int64_t)e * na + m0) * nb + n0) * 2, (int64_t)nb * 2,
-                  [&](int m, int n, int, int) { return pack4(acc[m][n]); });
+                  [&](int m, int n) { return pack4(acc[m][n]); });
 }
 
 int64_t row_tiles(const ExpertShape& S) { return (int64_t)S.P / kTileRows + (S.P < S.E ? S.P : S.E); }

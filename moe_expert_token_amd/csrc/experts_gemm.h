@@ -4,17 +4,30 @@
 //   D[row][feature] = sum over k of R[row][k] * F[feature][k]
 //
 // One block of eight waves makes a tile of 32 MF rows by 256 features (MF up
-// to 8: 256 x 256), each wave half of the rows by 64 features, from
-// v_mfma_f32_16x16x32_bf16 with the features as its rows, so that a lane ends
-// with four neighbouring features of one row.  An operand comes in one of two
-// orders: k-contiguous (rows of a matrix), or k-strided (its columns), where
-// the transposing LDS read turns [k][16] blocks into fragments on the way.
+// to 8: 256 x 256) from v_mfma_f32_16x16x32_bf16, with the features as its
+// rows, so that a lane ends with four neighbouring features of one row.  An
+// operand comes in one of two orders: k-contiguous (rows of a matrix), or
+// k-strided (its columns), where the transposing LDS read turns [k][16] blocks
+// into fragments on the way.
 //
-// The tile of 64 k is loaded straight into LDS (16 bytes a lane, no
-// registers), two tiles deep (128 KiB).  Rows, features and k past the
-// operand's end are loads out of the buffer descriptor's range: they read as
-// zero and touch no memory.
+// A tile of 64 k is four slots of LDS, the halves R0, R1 of the rows and F0, F1
+// of the features, 16 KiB each, loaded straight into LDS (16 bytes a lane, no
+// registers); two tiles fit (128 KiB).  A step over tile t has four phases,
+// one barrier each:
+//
+//   product   R0 F0       R0 F1       R1 F1       R1 F0
+//   reads     F1 (t)      R1 (t)      R0 (t+1)    F0 (t+1)    fragments for the next phase
+//   loads     F0 (t+2)    F1 (t+2)    R1 (t+2)    R0 (t+3)    into the slot read a phase ago
+//
+// A slot is free as soon as its fragments are in registers, so its next load
+// starts seven phases before it is read: that is what hides the memory's
+// latency.
+//
+// Rows, features and k past the operand's end are loads out of the buffer
+// descriptor's range: they read as zero and touch no memory.
 #pragma once
+
+#include <type_traits>
 
 #include "experts.h"
 
@@ -24,107 +37,84 @@ constexpr int kGemmThreads = 512;
 constexpr int kTileK = 64;
 constexpr int kTileFeatures = 256;
 constexpr int kTileRows = 256;
-constexpr int kOperandBytes = 256 * kTileK * 2;  // 32 KiB of LDS an operand and stage
-constexpr int kGemmLds = 4 * kOperandBytes;
+constexpr int kSlot = 128 * kTileK * 2;  // 16 KiB
+constexpr int kGemmLds = 8 * kSlot;
 
 typedef __attribute__((address_space(3))) void lds_void;
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
 constexpr unsigned kOutside = 0x80000000u;  // an offset that no descriptor here reaches
 
-// N loads of 16 bytes a lane from `rsrc`, at voff[i], into LDS at `lds` + 8192 i (the wave's first byte; lane l's
-// land 16 l further).  In assembly so that the compiler does not take each later LDS read for one of this tile and
-// wait for it: the loads of a tile are waited for once, by wait_loads() and the barrier in front of its first read.
-// It has no register output, and nothing else in the kernels that use it goes by m0.  The waits inside are those
-// the hardware asks for: five states after a descriptor's word came from a vector instruction, one after m0 changed.
-template <int N>
-__device__ __forceinline__ void load_to_lds(u32x4 rsrc, unsigned lds, const unsigned (&voff)[N])
+// A load of 16 bytes a lane from `rsrc` at voff into LDS at `lds` (the wave's first byte; lane l's land 16 l
+// further).  In assembly so that the compiler does not take each later LDS read for one of this slot and wait for
+// it: a slot is waited for once, by wait_loads() and the barrier in front of the phase that reads it.  It has no
+// register output, and nothing else in the kernels that use it goes by m0.  The wait inside is the one the
+// hardware asks for: five states after a descriptor's word came from a vector instruction (one after m0 changed).
+__device__ __forceinline__ void load_to_lds(u32x4 rsrc, unsigned lds, unsigned voff)
 {
-    static_assert(N >= 1 && N <= 4, "tiles of at most 256 rows");
-    if constexpr (N == 1)
-        asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %2, %1, 0 offen lds"
-                     :
-                     : "s"(lds), "s"(rsrc), "v"(voff[0])
-                     : "memory", "scc");
-    else if constexpr (N == 2)
-        asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %2, %1, 0 offen lds\n\t"
-                     "s_add_u32 m0, %0, 0x2000\n\ts_nop 0\n\tbuffer_load_dwordx4 %3, %1, 0 offen lds"
-                     :
-                     : "s"(lds), "s"(rsrc), "v"(voff[0]), "v"(voff[1])
-                     : "memory", "scc");
-    else if constexpr (N == 3)
-        asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %2, %1, 0 offen lds\n\t"
-                     "s_add_u32 m0, %0, 0x2000\n\ts_nop 0\n\tbuffer_load_dwordx4 %3, %1, 0 offen lds\n\t"
-                     "s_add_u32 m0, %0, 0x4000\n\ts_nop 0\n\tbuffer_load_dwordx4 %4, %1, 0 offen lds"
-                     :
-                     : "s"(lds), "s"(rsrc), "v"(voff[0]), "v"(voff[1]), "v"(voff[2])
-                     : "memory", "scc");
-    else
-        asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %2, %1, 0 offen lds\n\t"
-                     "s_add_u32 m0, %0, 0x2000\n\ts_nop 0\n\tbuffer_load_dwordx4 %3, %1, 0 offen lds\n\t"
-                     "s_add_u32 m0, %0, 0x4000\n\ts_nop 0\n\tbuffer_load_dwordx4 %4, %1, 0 offen lds\n\t"
-                     "s_add_u32 m0, %0, 0x6000\n\ts_nop 0\n\tbuffer_load_dwordx4 %5, %1, 0 offen lds"
-                     :
-                     : "s"(lds), "s"(rsrc), "v"(voff[0]), "v"(voff[1]), "v"(voff[2]), "v"(voff[3])
-                     : "memory", "scc");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %2, %1, 0 offen lds"
+                 :
+                 : "s"(lds), "s"(rsrc), "v"(voff));
 }
 
 __device__ __forceinline__ u32x4 buffer_of(const char* p, unsigned bytes)
 {
     const uint64_t a = (uint64_t)p;
-    return u32x4{(unsigned)a, (unsigned)(a >> 32) & 0xffffu, bytes, 0x00020000u};
+    // the same in every lane; the reads put into scalar registers what the compiler computed in vector ones
+    return u32x4{(unsigned)__builtin_amdgcn_readfirstlane((int)a),
+                 (unsigned)__builtin_amdgcn_readfirstlane((int)(a >> 32)) & 0xffffu,
+                 (unsigned)__builtin_amdgcn_readfirstlane((int)bytes), 0x00020000u};
 }
 
 __device__ __forceinline__ unsigned lds_offset(const void* p) { return (unsigned)(uintptr_t)(lds_void*)p; }
 
-// s_waitcnt vmcnt(0): everything this wave has loaded (into LDS too) is there.
-__device__ __forceinline__ void wait_loads() { __builtin_amdgcn_s_waitcnt(0x0f70); }
+// Waits until all but this wave's last N loads have landed (those into LDS too).
+template <int N>
+__device__ __forceinline__ void wait_loads()
+{
+    static_assert(N < 64, "six bits");
+    __builtin_amdgcn_s_waitcnt((N & 15) | (N >> 4 << 14) | 0x0f70);
+}
 
 // An operand whose rows (or features) run along memory rows of k.
-//   LDS: [256][64] bf16; the 16-byte piece c of row r lies at piece c ^ (r & 7), so that the eight lanes of a
-//   fragment read that are served together fall on all banks.
+//   LDS: [128][64] bf16 a slot; the 16-byte piece c of row r lies at piece c ^ (r & 7), so that the eight lanes of
+//   a fragment read that are served together fall on all banks.
 struct KContiguous {
-    static constexpr int kReads = 1;  // LDS instructions a fragment
-    const char* p;     // (row 0, k 0)
-    unsigned ld;       // bytes from row to row
-    unsigned bytes;    // from p to the end of the last valid row
+    static constexpr bool kTransposed = false;
+    const char* p[2];   // of each slot: (row 0, k 0)
+    unsigned bytes[2];  // from p to the end of the slot's last valid row
+    unsigned ld;        // bytes from row to row
     int K;
-    unsigned voff;     // this thread's first piece
-    unsigned next;     // bytes to the same piece of the next instruction's rows
-    int piece8;        // its k within the tile
+    unsigned voff;      // this thread's first piece
+    int piece8;         // its k within the tile
 
-    // LDS rows 64 i + r hold the operand's rows `stride` * i + row: in order for stride 64 and row = r.
-    __device__ __forceinline__ void init(const void* base, int ld_elems, int valid_rows, int k_len, int stride, int row)
+    __device__ __forceinline__ void init(int ld_elems, int k_len)
     {
-        p = (const char*)base;
         ld = (unsigned)ld_elems * 2;
-        bytes = (unsigned)valid_rows * ld;
         K = k_len;
         const int t = threadIdx.x, r = t >> 3, c = (t & 7) ^ (r & 7);
         piece8 = c * 8;
-        voff = (unsigned)row * ld + (unsigned)c * 16;
-        next = (unsigned)stride * ld;
+        voff = (unsigned)r * ld + (unsigned)c * 16;
     }
-    __device__ __forceinline__ void init(const void* base, int ld_elems, int valid_rows, int k_len)
+    // The first of slot s's rows, and how many there are (none or fewer: the slot is zero).
+    __device__ __forceinline__ void slot(int s, const char* first, int valid)
     {
-        init(base, ld_elems, valid_rows, k_len, 64, threadIdx.x >> 3);
+        p[s] = first;
+        bytes[s] = (unsigned)max(0, min(valid, 128)) * ld;
     }
 
-    // Starts the loads of tile kt into LDS at `lds`: N instructions of 64 rows.
+    // Starts the loads of slot s of tile kt: N of 64 rows.
     template <int N>
-    __device__ __forceinline__ void load(int kt, unsigned lds) const
+    __device__ __forceinline__ void load(int s, int kt, unsigned lds) const
     {
-        const int k0 = kt * kTileK;
-        const bool any = k0 < K;
-        const unsigned skip = any ? (unsigned)k0 * 2 : 0;
-        unsigned v[N];
-        v[0] = k0 + piece8 < K ? voff : kOutside;
+        const int k0 = kt * kTileK, skip = k0 < K ? k0 * 2 : 0x7fffffff;
+        const u32x4 rsrc = buffer_of(p[s] + (unsigned)k0 * 2u, (unsigned)max((int)bytes[s] - skip, 0));
+        const unsigned v = k0 + piece8 < K ? voff : kOutside;
 #pragma unroll
-        for (int i = 1; i < N; ++i) v[i] = v[i - 1] + next;
-        load_to_lds<N>(buffer_of(p + skip, any ? bytes - skip : 0), lds + wave_id() * 1024, v);
+        for (int i = 0; i < N; ++i) load_to_lds(rsrc, lds + wave_id() * 1024 + i * 8192, v + i * 64 * ld);
     }
 
-    // The fragment of rows `row0` .. + 16 and k half `half`: lane & 15 the row, 8 (lane >> 4) the k.
+    // The fragment of the slot's rows `row0` .. + 16 and k half `half`: lane & 15 the row, 8 (lane >> 4) the k.
     static __device__ __forceinline__ bf16x8 fragment(const char* lds, int row0, int half)
     {
         const int lane = lane_id(), r = lane & 15, c = (half * 4 + (lane >> 4)) ^ (r & 7);
@@ -133,37 +123,36 @@ struct KContiguous {
 };
 
 // An operand whose k runs along memory rows of features.
-//   LDS: [64][256] bf16; the 32-byte piece c of row k lies at piece c ^ (k & 3 | (k >> 3 & 3) << 2): the sixteen
-//   rows of a transposing read (four of every eight) fall on different banks.
+//   LDS: [64][128] bf16 a slot; the 32-byte piece c of row k lies at piece c ^ (k & 3 | (k >> 3 & 1) << 2): the
+//   eight rows that a transposing read is served at once fall on different banks.
 struct KStrided {
-    static constexpr int kReads = 2;
-    const char* p;     // (k 0, feature 0 of the tile)
+    static constexpr bool kTransposed = true;
+    const char* p[2];  // of each slot: (k 0, feature 0)
+    unsigned voff[2];  // of this thread's piece; kOutside past the slot's features
     unsigned ld;       // bytes from k to k + 1
     int K;
-    unsigned voff[2];  // of even and odd instructions
 
-    __device__ __forceinline__ void init(const void* base, int ld_elems, int valid_features, int k_len)
+    __device__ __forceinline__ void init(int ld_elems, int k_len)
     {
-        p = (const char*)base;
         ld = (unsigned)ld_elems * 2;
         K = k_len;
-        const int t = threadIdx.x, r = t >> 5;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int c = (t & 31) ^ ((r & 3) << 1) ^ ((r >> 3) << 3) ^ (i << 4);
-            voff[i] = c * 8 < valid_features ? (unsigned)r * ld + (unsigned)c * 16 : kOutside;
-        }
+    }
+    __device__ __forceinline__ void slot(int s, const char* first, int valid)
+    {
+        p[s] = first;
+        const int t = threadIdx.x, r = t >> 4, c = (t & 15) ^ ((r & 3) << 1) ^ (((r >> 3) & 1) << 3);
+        voff[s] = c * 8 < valid ? (unsigned)r * ld + (unsigned)c * 16 : kOutside;
     }
 
-    // 16 rows of k an instruction; all 256 features whatever N.
+    // Starts the loads of slot s of tile kt: two of 32 rows of k.
     template <int N>
-    __device__ __forceinline__ void load(int kt, unsigned lds) const
+    __device__ __forceinline__ void load(int s, int kt, unsigned lds) const
     {
-        const int left = K - kt * kTileK;
-        const bool any = left > 0;
-        const unsigned v[4] = {voff[0], voff[1] + 16 * ld, voff[0] + 32 * ld, voff[1] + 48 * ld};
-        load_to_lds<4>(buffer_of(p + (any ? (int64_t)kt * kTileK * ld : 0), any ? (unsigned)min(left, kTileK) * ld : 0),
-                       lds + wave_id() * 1024, v);
+        static_assert(N == 2, "64 rows of k");
+        const int rows = min(max(K - kt * kTileK, 0), kTileK);
+        const u32x4 rsrc = buffer_of(p[s] + (int64_t)kt * kTileK * ld, (unsigned)rows * ld);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) load_to_lds(rsrc, lds + wave_id() * 1024 + i * 8192, voff[s] + i * 32 * ld);
     }
 
     static __device__ __forceinline__ bf16x8 fragment(const char* lds, int f0, int half)
@@ -171,82 +160,122 @@ struct KStrided {
         // lanes 4 r .. 4 r + 3 of each sixteen name row r of a [4][16] block; the block comes back by columns
         const int lane = lane_id(), b = lane >> 4, r = (lane >> 2) & 3, j = lane & 3;
         const int k = half * 32 + b * 8 + r;
-        const int piece = (f0 >> 4) ^ (r | (b << 2));
-        const char* at = lds + k * 512 + piece * 32 + j * 8;
+        const int piece = (f0 >> 4) ^ (r | ((b & 1) << 2));
+        const char* at = lds + k * 256 + piece * 32 + j * 8;
         union {
             s16x4 h[2];
             bf16x8 v;
         } u;
         u.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)at);
-        u.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(at + 4 * 512));
+        u.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(at + 4 * 256));
         return u.v;
     }
 };
 
-// Asks for `Reads` LDS reads spread among `Products` matrix instructions, so that both proceed.
-template <int Reads, int Products, int I = 0>
-__device__ __forceinline__ void interleave()
-{
-    if constexpr (I < Reads) {
-        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x008, (I + 1) * Products / Reads - I * Products / Reads, 0);
-        interleave<Reads, Products, I + 1>();
-    }
-}
-
 template <int MF>
 using Acc = f32x4[MF][4];
 
-// acc[m][f]: rows 16 (MF wr + m) + (lane & 15), features 64 wf + 16 f + 4 (lane >> 4) .. + 4 of the tile, with
-// wr = wave >> 2, wf = wave & 3.  `lds`: kGemmLds bytes.  Ends with a barrier: LDS is free.
+// Where acc[m][n] of this wave lies in the tile: rows row_of<MF>(m) + (lane & 15), features feature_of(n) +
+// 4 (lane >> 4) .. + 4.  Slot R0 holds the first 32 ceil(MF / 2) rows, R1 the rest.
+template <int MF>
+__device__ __forceinline__ int row_of(int m)
+{
+    constexpr int A = (MF + 1) / 2, B = MF / 2;
+    const int wr = wave_id() >> 2;
+    return m < A ? 16 * (A * wr + m) : 32 * A + 16 * (B * wr + m - A);
+}
+__device__ __forceinline__ int feature_of(int n) { return (n >> 1) * 128 + 32 * (wave_id() & 3) + 16 * (n & 1); }
+
+// The tile's product.  `lds`: kGemmLds bytes.  Ends with a barrier: LDS is free.
 template <int MF, class R, class F>
 __device__ __forceinline__ void tile_product(const R& r, const F& f, int K, char* lds, Acc<MF>& acc)
 {
+    constexpr int A = (MF + 1) / 2, B = MF / 2;  // row fragments of a wave in R0 and R1
+    constexpr int a = R::kTransposed ? 2 : (A + 1) / 2, b = R::kTransposed ? 2 : (B + 1) / 2;  // loads of R0 and R1
     const int wr = wave_id() >> 2, wf = wave_id() & 3, nk = (K + kTileK - 1) / kTileK;
 #pragma unroll
     for (int m = 0; m < MF; ++m)
 #pragma unroll
         for (int n = 0; n < 4; ++n) acc[m][n] = f32x4{0, 0, 0, 0};
+    if (nk == 0) return;
     const unsigned base = __builtin_amdgcn_readfirstlane(lds_offset(lds));
-    const auto start = [&](int kt) {
-        const unsigned at = base + (kt & 1) * 2 * kOperandBytes;
-        r.template load<(MF + 1) / 2>(kt, at);
-        f.template load<4>(kt, at + kOperandBytes);
+    // slots of a tile: R0, R1, F0, F1
+    const auto load_r = [&](int s, int kt) {
+        const unsigned at = base + (kt & 1) * 4 * kSlot + s * kSlot;
+        if (s == 0) r.template load<a>(0, kt, at);
+        else r.template load<b>(1, kt, at);
     };
-    bf16x8 ra[2][MF], fa[2][4];
-    const auto fragments = [&](int kt, int half) {
-        const char* const at = lds + (kt & 1) * 2 * kOperandBytes;
-#pragma unroll
-        for (int n = 0; n < 4; ++n) fa[half][n] = F::fragment(at + kOperandBytes, wf * 64 + n * 16, half);
-#pragma unroll
-        for (int m = 0; m < MF; ++m) ra[half][m] = R::fragment(at, (wr * MF + m) * 16, half);
+    const auto load_f = [&](int s, int kt) { f.template load<2>(s, kt, base + (kt & 1) * 4 * kSlot + (2 + s) * kSlot); };
+    bf16x8 r0[A][2], r1[B ? B : 1][2], fx[2][2], fy[2][2];
+    const auto read_r0 = [&](int kt, int i) {
+        r0[i >> 1][i & 1] = R::fragment(lds + (kt & 1) * 4 * kSlot, 16 * (A * wr + (i >> 1)), i & 1);
     };
-    const auto multiply = [&](int half) {
-#pragma unroll
-        for (int m = 0; m < MF; ++m)
-#pragma unroll
-            for (int n = 0; n < 4; ++n) acc[m][n] = mfma_16x16x32(fa[half][n], ra[half][m], acc[m][n]);
+    const auto read_r1 = [&](int kt, int i) {
+        r1[i >> 1][i & 1] = R::fragment(lds + (kt & 1) * 4 * kSlot + kSlot, 16 * (B * wr + (i >> 1)), i & 1);
     };
-    if (nk > 0) {
-        start(0);
-        start(1);
-        wait_loads();
-        __syncthreads();
-        fragments(0, 0);
-        for (int kt = 0; kt < nk; ++kt) {
-            fragments(kt, 1);
-            multiply(0);
-            interleave<MF * R::kReads + 4 * F::kReads, 4 * MF>();
-            wait_loads();
-            __syncthreads();
-            start(kt + 2);
-            fragments(kt + 1, 0);
-            multiply(1);
-            interleave<MF * R::kReads + 4 * F::kReads, 4 * MF>();
+    const auto read_f = [&](bf16x8 (&to)[2][2], int s, int kt, int i) {
+        to[i >> 1][i & 1] = F::fragment(lds + (kt & 1) * 4 * kSlot + (2 + s) * kSlot, 32 * wf + 16 * (i >> 1), i & 1);
+    };
+    // One phase: products of `count` row fragments with two feature fragments; the `reads` LDS reads of the next
+    // phase go out in the first half of the products, the loads in their middle.
+    const auto phase = [&](auto count, auto first, auto side, const bf16x8 (*rows)[2], const bf16x8 (&feat)[2][2],
+                           auto reads, auto read, auto load, auto newer) {
+        constexpr int C = decltype(count)::value, M0 = decltype(first)::value, N0 = decltype(side)::value * 2;
+        constexpr int kReads = decltype(reads)::value, kChunks = C > 0 ? C : 1, kOver = (kChunks + 1) / 2;
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+#pragma unroll
+            for (int i = 0; i < kReads; ++i)
+                if (i * kOver / (kReads ? kReads : 1) == c) read(i);
+            if (c == kChunks / 2) load();
+            if constexpr (C > 0) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int n = 0; n < 2; ++n)
+                        acc[M0 + c][N0 + n] = mfma_16x16x32(feat[n][h], rows[c][h], acc[M0 + c][N0 + n]);
+            }
+            __builtin_amdgcn_sched_barrier(0);
         }
-        wait_loads();
+        wait_loads<decltype(newer)::value>();
         __syncthreads();
+    };
+#define MS_INT(x) std::integral_constant<int, (x)>()
+    const auto step = [&](int kt, bf16x8 (&f0)[2][2], bf16x8 (&f1)[2][2]) {
+        phase(MS_INT(A), MS_INT(0), MS_INT(0), r0, f0, MS_INT(4), [&](int i) { read_f(f1, 1, kt, i); },
+              [&] { load_f(0, kt + 2); }, MS_INT(2 * a + b + 6));
+        phase(MS_INT(A), MS_INT(0), MS_INT(1), r0, f1, MS_INT(2 * B), [&](int i) { read_r1(kt, i); },
+              [&] { load_f(1, kt + 2); }, MS_INT(a + b + 8));
+        phase(MS_INT(B), MS_INT(A), MS_INT(1), r1, f1, MS_INT(2 * A), [&](int i) { read_r0(kt + 1, i); },
+              [&] { load_r(1, kt + 2); }, MS_INT(a + 2 * b + 6));
+        phase(MS_INT(B), MS_INT(A), MS_INT(0), r1, f0, MS_INT(4), [&](int i) { read_f(f1, 0, kt + 1, i); },
+              [&] { load_r(0, kt + 3); }, MS_INT(2 * a + 2 * b + 4));
+    };
+#undef MS_INT
+    // in the steps' order, so that what a wait counts as newer is the same from the first phase on
+    for (int kt = 0; kt < 2; ++kt) {
+        load_r(0, kt);
+        load_f(0, kt);
+        load_f(1, kt);
+        load_r(1, kt);
     }
+    wait_loads<a + 2 * b + 6>();  // R0 and F0
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 2 * A; ++i) read_r0(0, i);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) read_f(fx, 0, 0, i);
+    wait_loads<a + 2 * b + 4>();  // F1
+    __syncthreads();
+    load_r(0, 2);
+    for (int kt = 0;;) {
+        step(kt, fx, fy);
+        if (++kt >= nk) break;
+        step(kt, fy, fx);
+        if (++kt >= nk) break;
+    }
+    wait_loads<0>();
+    __syncthreads();
 }
 
 }  // namespace ms

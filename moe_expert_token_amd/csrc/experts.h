@@ -38,6 +38,12 @@ hipError_t launch_ffn_dx(const ExpertShape& S, const void* dgu, const void* w_ga
 hipError_t launch_ffn_wgrad(const ExpertShape& S, const void* a, int na, const void* b, int nb, void* out,
                             hipStream_t s);
 
+// The forward pass where the experts have few rows each (ffn_is_few says when it is the faster one).
+bool ffn_is_few(const ExpertShape& S);
+hipError_t launch_few_up(const ExpertShape& S, const void* xe, const void* w_gate_up, void* h, SavedActs saved,
+                         hipStream_t s);
+hipError_t launch_few_down(const ExpertShape& S, const void* h, const void* w_down, void* ye, hipStream_t s);
+
 hipError_t launch_w4_up(const ExpertShape& S, const void* xe, const void* q, const void* scale, int group, void* h,
                         hipStream_t s);
 hipError_t launch_w4_down(const ExpertShape& S, const void* h, const void* q, const void* scale, int group, void* ye,

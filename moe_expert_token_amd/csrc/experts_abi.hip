@@ -128,8 +128,13 @@ int moe_experts_ffn_forward(moe_shuffle_plan_t plan, const void* xe, const void*
                   {workspace, workspace_bytes_of(S, false)}},
                  {{xe, rows}, {w_gate_up, 2 * proj}, {w_down, proj}}))
         return MOE_SHUFFLE_E_INVALID_ARG;
-    hipError_t e = ms::launch_ffn_up(S, xe, w_gate_up, workspace, ms::SavedActs{saved, saved_scale}, (hipStream_t)stream);
-    if (e == hipSuccess) e = ms::launch_ffn_down(S, workspace, w_down, ye, (hipStream_t)stream);
+    hipStream_t s = (hipStream_t)stream;
+    const bool few = ms::ffn_is_few(S);
+    const ms::SavedActs held{saved, saved_scale};
+    hipError_t e = few ? ms::launch_few_up(S, xe, w_gate_up, workspace, held, s)
+                       : ms::launch_ffn_up(S, xe, w_gate_up, workspace, held, s);
+    if (e == hipSuccess)
+        e = few ? ms::launch_few_down(S, workspace, w_down, ye, s) : ms::launch_ffn_down(S, workspace, w_down, ye, s);
     return status_of(e);
 }
 

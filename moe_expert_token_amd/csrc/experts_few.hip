@@ -1,0 +1,393 @@
+// experts_few.hip -- the experts' block where an expert has few rows: the
+// weights' bytes are the cost, so every wave streams weights from memory
+// straight into registers.  Weights are bf16, or 4-bit with group scales.
+//
+//   D[row][feature] = sum over k of X[row][k] * W[feature][k]
+//
+// v_mfma_f32_16x16x32_bf16 takes 16 rows and 16 features; a lane holds one
+// feature (lane & 15) of four rows.  A wave works on four such feature groups
+// at once (for the projections two of the gate and the same two of the up
+// projection), which share the rows' fragments, and on the chunks of 128 k that
+// are its own: the block's waves split k and add their sums through LDS in a
+// fixed tree.
+//
+// A 4-bit value q enters the product as the bf16 number 128 + q, whose low
+// mantissa bits are q: one shift and one v_and_or_b32 make two of them.  What
+// that adds to a sum, 136 x over q - 8, is taken off by adding the product of
+// the rows with -136, which the feature groups share.  A group's sum is exact
+// up to fp32 rounding and is scaled in fp32 as it is added.  (An infinite x
+// therefore gives NaN.)  The 16 bytes that a lane loads of a weight
+// row are 32 neighbouring k; a transpose over the four quarters of the wave
+// (two v_permlane32_swap, two v_permlane16_swap) deals them out so that each
+// matrix instruction covers 32 neighbouring k, and so one group.
+#include <type_traits>
+
+#include "experts.h"
+
+namespace ms {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kWaves = kThreads / kWave;
+constexpr int kChunk = 128;
+constexpr int kGroupsOf16 = 4;  // feature groups of a wave
+constexpr unsigned kOutside = 0x80000000u;
+
+// A buffer whose reads past `bytes` are zero.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* p, int64_t bytes)
+{
+    const uint64_t a = (uint64_t)p;
+    const uint64_t u = (unsigned)__builtin_amdgcn_readfirstlane((int)a) |
+                       (uint64_t)(unsigned)__builtin_amdgcn_readfirstlane((int)(a >> 32)) << 32;
+    const int n = bytes > 0 ? (int)bytes : 0;
+    return __builtin_amdgcn_make_buffer_rsrc((void*)u, 0, __builtin_amdgcn_readfirstlane(n), 0x00020000);
+}
+
+__device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t r, unsigned at)
+{
+    return __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0);
+}
+
+// The weights of a wave's feature groups: rows of `ld` bytes; group s lies in buffer s >> 1, 16 (s & 1) rows in.
+// Group is 0 for bf16 weights, else the 4-bit weights' group size.
+template <int Group>
+struct Weights {
+    __amdgpu_buffer_rsrc_t w[2], sc[2];
+    unsigned ld, sld;
+
+    __device__ __forceinline__ void side(int i, const char* rows, const char* scales, int valid, int K)
+    {
+        ld = Group ? K / 2 : K * 2;
+        w[i] = buffer(rows, (int64_t)min(valid, 32) * ld);
+        if (Group) {
+            sld = K / (Group ? Group : 1) * 2;
+            sc[i] = buffer(scales, (int64_t)min(valid, 32) * sld);
+        }
+    }
+};
+
+// What a wave has in hand of one chunk: weights, their scales (bf16 pairs) and the rows' fragments.  As soon as a
+// part is in use, the next chunk's is loaded in its place.  Whole: K is a multiple of the chunk.
+template <int Group, int RT, bool Whole>
+struct Chunk {
+    u32x4 w[kGroupsOf16][Group ? 1 : 4];
+    unsigned sc[Group ? kGroupsOf16 : 1][2];
+    u32x4 x[RT][4];
+
+    // 4-bit weights and scales of chunk c
+    __device__ __forceinline__ void load_packed(const Weights<Group>& W, int c, int K)
+    {
+        constexpr int G = Group ? Group : 1;
+        const int lane = lane_id(), r = lane & 15, q = lane >> 4, k0 = c * kChunk;
+        const unsigned at = k0 + q * 32 < K ? r * W.ld + q * 16 + c * 64 : kOutside;
+#pragma unroll
+        for (int s = 0; s < kGroupsOf16; ++s) w[s][0] = load16(W.w[s >> 1], at + (s & 1) * 16 * W.ld);
+        const unsigned sat = k0 < K ? r * W.sld + c * (kChunk / G) * 2 : kOutside;
+#pragma unroll
+        for (int s = 0; s < kGroupsOf16; ++s) {
+            const unsigned f = sat + (s & 1) * 16 * W.sld;
+            if constexpr (Group == 128) {
+                sc[s][0] = __builtin_amdgcn_raw_buffer_load_b16(W.sc[s >> 1], f, 0, 0);
+            } else if constexpr (!Whole) {  // a row's scales need not be aligned, and the last chunk has fewer of them
+#pragma unroll
+                for (int i = 0; i < kChunk / G; i += 2) {
+                    const unsigned lo = k0 + i * G < K ? f + 2 * i : kOutside;
+                    const unsigned hi = k0 + (i + 1) * G < K ? f + 2 * i + 2 : kOutside;
+                    sc[s][i >> 1] = (unsigned)__builtin_amdgcn_raw_buffer_load_b16(W.sc[s >> 1], lo, 0, 0) |
+                                    (unsigned)__builtin_amdgcn_raw_buffer_load_b16(W.sc[s >> 1], hi, 0, 0) << 16;
+                }
+            } else if constexpr (Group == 64) {
+                sc[s][0] = __builtin_amdgcn_raw_buffer_load_b32(W.sc[s >> 1], f, 0, 0);
+            } else {
+                const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(W.sc[s >> 1], f, 0, 0);
+                sc[s][0] = v[0];
+                sc[s][1] = v[1];
+            }
+        }
+    }
+
+    // the 32 k at j of chunk c: fragments, and weights where they are bf16
+    __device__ __forceinline__ void load_part(const Weights<Group>& W, const __amdgpu_buffer_rsrc_t& rows, int c, int j, int K)
+    {
+        const int lane = lane_id(), r = lane & 15, k = c * kChunk + j * 32 + (lane >> 4) * 8;
+        if constexpr (Group == 0) {
+            const unsigned at = k < K ? r * W.ld + k * 2 : kOutside;
+#pragma unroll
+            for (int s = 0; s < kGroupsOf16; ++s) w[s][j] = load16(W.w[s >> 1], at + (s & 1) * 16 * W.ld);
+        }
+        const unsigned at = k < K ? (unsigned)r * (unsigned)(K * 2) + k * 2 : kOutside;
+#pragma unroll
+        for (int t = 0; t < RT; ++t) x[t][j] = load16(rows, at + t * 16 * (unsigned)(K * 2));
+    }
+
+    __device__ __forceinline__ void load(const Weights<Group>& W, const __amdgpu_buffer_rsrc_t& rows, int c, int K)
+    {
+        if constexpr (Group != 0) load_packed(W, c, K);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) load_part(W, rows, c, j, K);
+    }
+
+    // Adds this chunk's products to acc, and leaves chunk `next` in its place.
+    __device__ __forceinline__ void add_to(f32x4 (&acc)[kGroupsOf16][RT], const Weights<Group>& W,
+                                           const __amdgpu_buffer_rsrc_t& rows, int next, int K)
+    {
+        if constexpr (Group == 0) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+#pragma unroll
+                for (int s = 0; s < kGroupsOf16; ++s)
+#pragma unroll
+                    for (int t = 0; t < RT; ++t)
+                        acc[s][t] = mfma_16x16x32(__builtin_bit_cast(bf16x8, x[t][j]),
+                                                  __builtin_bit_cast(bf16x8, w[s][j]), acc[s][t]);
+                load_part(W, rows, next, j, K);
+            }
+        } else {
+            constexpr int kPer = Group / 32;  // matrix instructions a group
+            const u32x4 minus136 = {0xc308c308u, 0xc308c308u, 0xc308c308u, 0xc308c308u};
+            u32x4 d[kGroupsOf16];
+            unsigned now[kGroupsOf16][2];
+#pragma unroll
+            for (int s = 0; s < kGroupsOf16; ++s) {
+                // register j of quarter q <-> register q of quarter j
+                const auto a = __builtin_amdgcn_permlane32_swap(w[s][0][0], w[s][0][2], false, false);
+                const auto b = __builtin_amdgcn_permlane32_swap(w[s][0][1], w[s][0][3], false, false);
+                const auto e = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
+                const auto f = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
+                d[s] = u32x4{e[0], e[1], f[0], f[1]};
+                now[s][0] = sc[s][0];
+                now[s][1] = sc[s][1];
+            }
+            load_packed(W, next, K);
+            f32x4 sum[kGroupsOf16][RT], base[RT];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                bf16x8 xs[RT];
+#pragma unroll
+                for (int t = 0; t < RT; ++t) {
+                    // k in the order (0, 4), (1, 5), (2, 6), (3, 7) in which the weights' nibbles come apart
+                    const u32x4 v = x[t][j];
+                    const u32x4 p = {__builtin_amdgcn_perm(v[2], v[0], 0x05040100),
+                                     __builtin_amdgcn_perm(v[2], v[0], 0x07060302),
+                                     __builtin_amdgcn_perm(v[3], v[1], 0x05040100),
+                                     __builtin_amdgcn_perm(v[3], v[1], 0x07060302)};
+                    xs[t] = __builtin_bit_cast(bf16x8, p);
+                    if (j % kPer == 0) base[t] = f32x4{0, 0, 0, 0};
+                    base[t] = mfma_16x16x32(xs[t], __builtin_bit_cast(bf16x8, minus136), base[t]);
+                }
+                load_part(W, rows, next, j, K);
+#pragma unroll
+                for (int s = 0; s < kGroupsOf16; ++s) {
+                    const unsigned v = d[s][j];
+                    const u32x4 p = {(v & 0x000f000fu) | 0x43004300u, ((v >> 4) & 0x000f000fu) | 0x43004300u,
+                                     ((v >> 8) & 0x000f000fu) | 0x43004300u, ((v >> 12) & 0x000f000fu) | 0x43004300u};
+#pragma unroll
+                    for (int t = 0; t < RT; ++t) {
+                        if (j % kPer == 0) sum[s][t] = f32x4{0, 0, 0, 0};
+                        sum[s][t] = mfma_16x16x32(xs[t], __builtin_bit_cast(bf16x8, p), sum[s][t]);
+                    }
+                    if (j % kPer == kPer - 1) {
+                        const int g = j / kPer;
+                        const float f = g & 1 ? bf16_hi(now[s][g >> 1]) : bf16_lo(now[s][g >> 1]);
+#pragma unroll
+                        for (int t = 0; t < RT; ++t)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) acc[s][t][i] = fmaf(sum[s][t][i] + base[t][i], f, acc[s][t][i]);
+                    }
+                }
+            }
+        }
+    }
+};
+
+// How a block's eight waves share its work: KS ways over k, the rest over features; row tiles of up to Rows.
+template <bool Few>
+struct Split {
+    static constexpr int kRows = Few ? 16 : 64;
+    static constexpr int KS = Few ? 8 : 2;
+    static constexpr int FS = kWaves / KS;
+    static constexpr int kLds = FS * (KS / 2) * kGroupsOf16 * (kRows / 16) * kWave * 16;
+};
+
+struct FewArgs {
+    const char* x;         // [P][K] bf16
+    const char* w;         // [E][rows of both sides][K]
+    const char* scale;
+    char* out;             // [P][N] bf16
+    int K, N;              // N: features of the output
+    SavedActs saved;       // of the projections
+    int across;            // blocks over N
+};
+
+__device__ __forceinline__ unsigned short bf16_of(float v) { return (unsigned short)bf16_pack2(v, v); }
+
+// Keeps a row's pre-activations of features n (a) and n + 16 (b), the gate's (side 0) or the up projection's; the
+// sixteen lanes of a row hold a group of an 8-bit checkpoint.
+__device__ __forceinline__ void save(const SavedActs& to, int64_t row, int side, int n, int N, float a, float b, bool ok)
+{
+    const bool in_a = ok && n < N, in_b = ok && n + 16 < N;
+    const int64_t at = row * 2 * N + (side ? N : 0) + n;
+    if (!to.scale) {
+        if (in_a) ((unsigned short*)to.data)[at] = bf16_of(a);
+        if (in_b) ((unsigned short*)to.data)[at + 16] = bf16_of(b);
+        return;
+    }
+    const float x = n < N ? fabsf(a) : 0.0f, y = n + 16 < N ? fabsf(b) : 0.0f;
+    float top = fmaxf(x, y);
+    if (!(x <= 3.40282347e38f) || !(y <= 3.40282347e38f)) top = __uint_as_float(0x7f800000u);
+#pragma unroll
+    for (int d = 1; d < 16; d <<= 1) top = fmaxf(top, __shfl_xor(top, d, kWave));
+    const float step = step8(top), inv = 1.0f / step;
+    if (in_a) ((unsigned char*)to.data)[at] = (unsigned char)pack8x4(a, a, a, a, inv);
+    if (in_b) ((unsigned char*)to.data)[at + 16] = (unsigned char)pack8x4(b, b, b, b, inv);
+    if (in_a && (n & 31) == 0)
+        ((unsigned short*)to.scale)[(row * 2 + side) * ((N + kGroup8 - 1) / kGroup8) + n / kGroup8] =
+            (unsigned short)(__float_as_uint(step) >> 16);
+}
+
+// Up: features c and c + N of the weights make feature c of the output, h = act(gate) * up.
+template <int Group, bool Up, bool Few, bool Whole>
+__global__ __launch_bounds__(kThreads) void ffn_few_kernel(ExpertShape S, FewArgs A, GridSpan span)
+{
+    typedef Split<Few> P;
+    constexpr int kOut = Up ? 32 : 64;  // output features of a wave
+    __shared__ __align__(16) char lds[P::kLds];
+    const int b = span_block(span), tile = b / A.across, place = b - tile * A.across;
+    int row0, nr;
+    const int bad = *S.status, e = segment_tile(S.offset, S.E, P::kRows, 16, tile, &row0, &nr);
+    if (bad || e < 0) return;
+    const int ks = wave_id() % P::KS, fs = wave_id() / P::KS, K = A.K, N = A.N;
+    const int n0 = (place * P::FS + fs) * kOut;
+    Weights<Group> W;
+    const int64_t wrow = (int64_t)e * (Up ? 2 * N : N) + n0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int64_t first = wrow + (Up ? (i ? N : 0) : 32 * i);
+        W.side(i, A.w + first * (Group ? K / 2 : K * 2), Group ? A.scale + first * (K / (Group ? Group : 1)) * 2 : nullptr,
+               Up ? N - n0 : N - n0 - 32 * i, K);
+    }
+    const __amdgpu_buffer_rsrc_t rows = buffer(A.x + (int64_t)row0 * K * 2, (int64_t)nr * K * 2);
+    const auto run = [&](auto tiles) {
+        constexpr int RT = decltype(tiles)::value;
+        f32x4 acc[kGroupsOf16][RT];
+#pragma unroll
+        for (int s = 0; s < kGroupsOf16; ++s)
+#pragma unroll
+            for (int t = 0; t < RT; ++t) acc[s][t] = f32x4{0, 0, 0, 0};
+        const int chunks = (K + kChunk - 1) / kChunk;
+        Chunk<Group, RT, Whole> chunk;  // past the last one, loads read nothing
+        chunk.load(W, rows, ks, K);
+#pragma unroll 1
+        for (int c = ks; c < chunks; c += P::KS) chunk.add_to(acc, W, rows, c + P::KS, K);
+        // the waves of a feature set add up pairwise
+        f32x4* const mine = (f32x4*)lds + (size_t)fs * (P::KS / 2) * kGroupsOf16 * RT * kWave;
+#pragma unroll
+        for (int half = P::KS / 2; half >= 1; half /= 2) {
+            if (half < P::KS / 2) __syncthreads();
+            if (ks >= half && ks < 2 * half)
+#pragma unroll
+                for (int s = 0; s < kGroupsOf16; ++s)
+#pragma unroll
+                    for (int t = 0; t < RT; ++t)
+                        mine[((ks - half) * kGroupsOf16 * RT + s * RT + t) * kWave + lane_id()] = acc[s][t];
+            __syncthreads();
+            if (ks < half)
+#pragma unroll
+                for (int s = 0; s < kGroupsOf16; ++s)
+#pragma unroll
+                    for (int t = 0; t < RT; ++t) acc[s][t] += mine[(ks * kGroupsOf16 * RT + s * RT + t) * kWave + lane_id()];
+        }
+        if (ks != 0) return;
+        unsigned short* const out = (unsigned short*)A.out;
+#pragma unroll
+        for (int t = 0; t < RT; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = 16 * t + 4 * (lane_id() >> 4) + i, n = n0 + (lane_id() & 15);
+                const int64_t row = row0 + r;
+                if constexpr (!Up) {
+#pragma unroll
+                    for (int s = 0; s < 4; ++s)
+                        if (r < nr && n + 16 * s < N) out[row * N + n + 16 * s] = bf16_of(acc[s][t][i]);
+                } else {
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        float slope;
+                        const float g = acc[s][t][i], u = acc[2 + s][t][i];
+                        if (r < nr && n + 16 * s < N)
+                            out[row * N + n + 16 * s] = bf16_of(g * gate_sigmoid(g, S.c0, S.c1, &slope) * u);
+                    }
+                    if (Group == 0 && A.saved.data) {
+#pragma unroll
+                        for (int side = 0; side < 2; ++side)
+                            save(A.saved, row, side, n, N, acc[2 * side][t][i], acc[2 * side + 1][t][i], r < nr);
+                    }
+                }
+            }
+    };
+    if constexpr (Few) {
+        run(std::integral_constant<int, 1>());
+    } else {
+        if (nr <= 32) run(std::integral_constant<int, 2>());
+        else run(std::integral_constant<int, 4>());
+    }
+}
+
+template <int Group, bool Up, bool Few, bool Whole>
+hipError_t launch(const ExpertShape& S, FewArgs A, hipStream_t s)
+{
+    typedef Split<Few> P;
+    const int out = (Up ? 32 : 64) * P::FS;
+    A.across = (A.N + out - 1) / out;
+    const int64_t tiles = (int64_t)S.P / P::kRows + (S.P < S.E ? S.P : S.E);
+    return launch_spans(tiles * A.across, kThreads, [&](dim3 grid, GridSpan span) {
+        ffn_few_kernel<Group, Up, Few, Whole><<<grid, kThreads, 0, s>>>(S, A, span);
+    });
+}
+
+// Rows an expert has on average, of those that can have one.
+bool few_each(const ExpertShape& S, int rows) { return S.P <= (int64_t)rows * (S.P < S.E ? S.P : S.E); }
+
+template <bool Up, bool Few>
+hipError_t launch_w4_of(const ExpertShape& S, const FewArgs& A, int group, hipStream_t s)
+{
+    const bool whole = A.K % kChunk == 0;
+    if (group == 128) return launch<128, Up, Few, true>(S, A, s);
+    if (group == 64) return whole ? launch<64, Up, Few, true>(S, A, s) : launch<64, Up, Few, false>(S, A, s);
+    return whole ? launch<32, Up, Few, true>(S, A, s) : launch<32, Up, Few, false>(S, A, s);
+}
+
+template <bool Up>
+hipError_t launch_w4(const ExpertShape& S, const FewArgs& A, int group, hipStream_t s)
+{
+    return few_each(S, 16) ? launch_w4_of<Up, true>(S, A, group, s) : launch_w4_of<Up, false>(S, A, group, s);
+}
+
+}  // namespace
+
+bool ffn_is_few(const ExpertShape& S) { return few_each(S, 16); }
+
+hipError_t launch_few_up(const ExpertShape& S, const void* xe, const void* w_gate_up, void* h, SavedActs saved,
+                         hipStream_t s)
+{
+    return launch<0, true, true, false>(S, FewArgs{(const char*)xe, (const char*)w_gate_up, nullptr, (char*)h, S.H, S.I, saved, 0}, s);
+}
+
+hipError_t launch_few_down(const ExpertShape& S, const void* h, const void* w_down, void* ye, hipStream_t s)
+{
+    return launch<0, false, true, false>(S, FewArgs{(const char*)h, (const char*)w_down, nullptr, (char*)ye, S.I, S.H, SavedActs{}, 0}, s);
+}
+
+hipError_t launch_w4_up(const ExpertShape& S, const void* xe, const void* q, const void* scale, int group, void* h,
+                        hipStream_t s)
+{
+    return launch_w4<true>(S, FewArgs{(const char*)xe, (const char*)q, (const char*)scale, (char*)h, S.H, S.I, SavedActs{}, 0}, group, s);
+}
+
+hipError_t launch_w4_down(const ExpertShape& S, const void* h, const void* q, const void* scale, int group, void* ye,
+                          hipStream_t s)
+{
+    return launch_w4<false>(S, FewArgs{(const char*)h, (const char*)q, (const char*)scale, (char*)ye, S.I, S.H, SavedActs{}, 0}, group, s);
+}
+
+}  // namespace ms

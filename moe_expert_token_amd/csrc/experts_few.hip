@@ -31,43 +31,61 @@ constexpr int kThreads = 512;
 constexpr int kWaves = kThreads / kWave;
 constexpr int kChunk = 128;
 constexpr int kGroupsOf16 = 4;  // feature groups of a wave
+constexpr int kLongK = 4096;    // from here on eight waves share a sum; below, where each would get few chunks, two
 constexpr unsigned kOutside = 0x80000000u;
 
-// A buffer whose reads past `bytes` are zero.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* p, int64_t bytes)
-{
-    const uint64_t a = (uint64_t)p;
-    const uint64_t u = (unsigned)__builtin_amdgcn_readfirstlane((int)a) |
-                       (uint64_t)(unsigned)__builtin_amdgcn_readfirstlane((int)(a >> 32)) << 32;
-    const int n = bytes > 0 ? (int)bytes : 0;
-    return __builtin_amdgcn_make_buffer_rsrc((void*)u, 0, __builtin_amdgcn_readfirstlane(n), 0x00020000);
-}
+// Memory of `bytes` bytes that is read a chunk of k at a time; what lies past its end reads as zero.
+struct Stream {
+    uint64_t p;
+    int bytes;
+
+    __device__ __forceinline__ void init(const void* from, int64_t n)
+    {
+        const uint64_t a = (uint64_t)from;  // the same in every lane
+        p = (unsigned)__builtin_amdgcn_readfirstlane((int)a) |
+            (uint64_t)(unsigned)__builtin_amdgcn_readfirstlane((int)(a >> 32)) << 32;
+        bytes = __builtin_amdgcn_readfirstlane(n > 0 ? (int)n : 0);
+    }
+    // The buffer from `skip` bytes on; empty past the end, or unless `any`.
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t from(int skip, bool any) const
+    {
+        const int left = any && skip < bytes ? bytes - skip : 0;
+        return __builtin_amdgcn_make_buffer_rsrc((void*)(p + (unsigned)skip), 0, __builtin_amdgcn_readfirstlane(left),
+                                                 0x00020000);
+    }
+};
 
 __device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t r, unsigned at)
 {
     return __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0);
 }
 
-// The weights of a wave's feature groups: rows of `ld` bytes; group s lies in buffer s >> 1, 16 (s & 1) rows in.
-// Group is 0 for bf16 weights, else the 4-bit weights' group size.
+// What a wave reads: the weights of its feature groups (group s lies in stream s >> 1, 16 (s & 1) rows of `ld`
+// bytes in), their scales and the rows.  Group is 0 for bf16 weights, else the 4-bit weights' group size.
 template <int Group>
-struct Weights {
-    __amdgpu_buffer_rsrc_t w[2], sc[2];
-    unsigned ld, sld;
+struct Source {
+    Stream w[2], sc[2], x;
+    int K, chunks;
+    unsigned ld, sld, xld;
 
-    __device__ __forceinline__ void side(int i, const char* rows, const char* scales, int valid, int K)
+    __device__ __forceinline__ void init(int k_len)
     {
+        K = k_len;
+        chunks = (K + kChunk - 1) / kChunk;
         ld = Group ? K / 2 : K * 2;
-        w[i] = buffer(rows, (int64_t)min(valid, 32) * ld);
-        if (Group) {
-            sld = K / (Group ? Group : 1) * 2;
-            sc[i] = buffer(scales, (int64_t)min(valid, 32) * sld);
-        }
+        sld = Group ? K / (Group ? Group : 1) * 2 : 0;
+        xld = K * 2;
+    }
+    __device__ __forceinline__ void side(int i, const char* rows, const char* scales, int valid)
+    {
+        w[i].init(rows, (int64_t)min(valid, 32) * ld);
+        if (Group) sc[i].init(scales, (int64_t)min(valid, 32) * sld);
     }
 };
 
 // What a wave has in hand of one chunk: weights, their scales (bf16 pairs) and the rows' fragments.  As soon as a
-// part is in use, the next chunk's is loaded in its place.  Whole: K is a multiple of the chunk.
+// part is in use, the next chunk's is loaded in its place.  Whole: K is a multiple of the chunk, so that only
+// whole chunks are read and a lane's offsets never change.
 template <int Group, int RT, bool Whole>
 struct Chunk {
     u32x4 w[kGroupsOf16][Group ? 1 : 4];
@@ -75,31 +93,38 @@ struct Chunk {
     u32x4 x[RT][4];
 
     // 4-bit weights and scales of chunk c
-    __device__ __forceinline__ void load_packed(const Weights<Group>& W, int c, int K)
+    __device__ __forceinline__ void load_packed(const Source<Group>& S, int c)
     {
         constexpr int G = Group ? Group : 1;
         const int lane = lane_id(), r = lane & 15, q = lane >> 4, k0 = c * kChunk;
-        const unsigned at = k0 + q * 32 < K ? r * W.ld + q * 16 + c * 64 : kOutside;
+        const bool any = c < S.chunks;
+        unsigned at = r * S.ld + q * 16;
+        if (!Whole && k0 + q * 32 >= S.K) at = kOutside;
 #pragma unroll
-        for (int s = 0; s < kGroupsOf16; ++s) w[s][0] = load16(W.w[s >> 1], at + (s & 1) * 16 * W.ld);
-        const unsigned sat = k0 < K ? r * W.sld + c * (kChunk / G) * 2 : kOutside;
+        for (int i = 0; i < 2; ++i) {
+            const __amdgpu_buffer_rsrc_t b = S.w[i].from(c * (kChunk / 2), any);
+            w[2 * i][0] = load16(b, at);
+            w[2 * i + 1][0] = load16(b, at + 16 * S.ld);
+        }
+        const unsigned sat = r * S.sld;
 #pragma unroll
         for (int s = 0; s < kGroupsOf16; ++s) {
-            const unsigned f = sat + (s & 1) * 16 * W.sld;
+            const __amdgpu_buffer_rsrc_t b = S.sc[s >> 1].from(c * (kChunk / G) * 2, any);
+            const unsigned f = sat + (s & 1) * 16 * S.sld;
             if constexpr (Group == 128) {
-                sc[s][0] = __builtin_amdgcn_raw_buffer_load_b16(W.sc[s >> 1], f, 0, 0);
+                sc[s][0] = __builtin_amdgcn_raw_buffer_load_b16(b, f, 0, 0);
             } else if constexpr (!Whole) {  // a row's scales need not be aligned, and the last chunk has fewer of them
 #pragma unroll
                 for (int i = 0; i < kChunk / G; i += 2) {
-                    const unsigned lo = k0 + i * G < K ? f + 2 * i : kOutside;
-                    const unsigned hi = k0 + (i + 1) * G < K ? f + 2 * i + 2 : kOutside;
-                    sc[s][i >> 1] = (unsigned)__builtin_amdgcn_raw_buffer_load_b16(W.sc[s >> 1], lo, 0, 0) |
-                                    (unsigned)__builtin_amdgcn_raw_buffer_load_b16(W.sc[s >> 1], hi, 0, 0) << 16;
+                    const unsigned lo = k0 + i * G < S.K ? f + 2 * i : kOutside;
+                    const unsigned hi = k0 + (i + 1) * G < S.K ? f + 2 * i + 2 : kOutside;
+                    sc[s][i >> 1] = (unsigned)__builtin_amdgcn_raw_buffer_load_b16(b, lo, 0, 0) |
+                                    (unsigned)__builtin_amdgcn_raw_buffer_load_b16(b, hi, 0, 0) << 16;
                 }
             } else if constexpr (Group == 64) {
-                sc[s][0] = __builtin_amdgcn_raw_buffer_load_b32(W.sc[s >> 1], f, 0, 0);
+                sc[s][0] = __builtin_amdgcn_raw_buffer_load_b32(b, f, 0, 0);
             } else {
-                const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(W.sc[s >> 1], f, 0, 0);
+                const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(b, f, 0, 0);
                 sc[s][0] = v[0];
                 sc[s][1] = v[1];
             }
@@ -107,29 +132,34 @@ struct Chunk {
     }
 
     // the 32 k at j of chunk c: fragments, and weights where they are bf16
-    __device__ __forceinline__ void load_part(const Weights<Group>& W, const __amdgpu_buffer_rsrc_t& rows, int c, int j, int K)
+    __device__ __forceinline__ void load_part(const Source<Group>& S, int c, int j)
     {
-        const int lane = lane_id(), r = lane & 15, k = c * kChunk + j * 32 + (lane >> 4) * 8;
+        const int lane = lane_id(), r = lane & 15, q = lane >> 4;
+        const bool any = c < S.chunks, in = Whole || c * kChunk + j * 32 + q * 8 < S.K;
         if constexpr (Group == 0) {
-            const unsigned at = k < K ? r * W.ld + k * 2 : kOutside;
+            const unsigned at = in ? r * S.ld + j * 64 + q * 16 : kOutside;
 #pragma unroll
-            for (int s = 0; s < kGroupsOf16; ++s) w[s][j] = load16(W.w[s >> 1], at + (s & 1) * 16 * W.ld);
+            for (int i = 0; i < 2; ++i) {
+                const __amdgpu_buffer_rsrc_t b = S.w[i].from(c * kChunk * 2, any);
+                w[2 * i][j] = load16(b, at);
+                w[2 * i + 1][j] = load16(b, at + 16 * S.ld);
+            }
         }
-        const unsigned at = k < K ? (unsigned)r * (unsigned)(K * 2) + k * 2 : kOutside;
+        const __amdgpu_buffer_rsrc_t b = S.x.from(c * kChunk * 2, any);
+        const unsigned at = in ? r * S.xld + j * 64 + q * 16 : kOutside;
 #pragma unroll
-        for (int t = 0; t < RT; ++t) x[t][j] = load16(rows, at + t * 16 * (unsigned)(K * 2));
+        for (int t = 0; t < RT; ++t) x[t][j] = load16(b, at + t * 16 * S.xld);
     }
 
-    __device__ __forceinline__ void load(const Weights<Group>& W, const __amdgpu_buffer_rsrc_t& rows, int c, int K)
+    __device__ __forceinline__ void load(const Source<Group>& S, int c)
     {
-        if constexpr (Group != 0) load_packed(W, c, K);
+        if constexpr (Group != 0) load_packed(S, c);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) load_part(W, rows, c, j, K);
+        for (int j = 0; j < 4; ++j) load_part(S, c, j);
     }
 
     // Adds this chunk's products to acc, and leaves chunk `next` in its place.
-    __device__ __forceinline__ void add_to(f32x4 (&acc)[kGroupsOf16][RT], const Weights<Group>& W,
-                                           const __amdgpu_buffer_rsrc_t& rows, int next, int K)
+    __device__ __forceinline__ void add_to(f32x4 (&acc)[kGroupsOf16][RT], const Source<Group>& S, int next)
     {
         if constexpr (Group == 0) {
 #pragma unroll
@@ -140,7 +170,7 @@ struct Chunk {
                     for (int t = 0; t < RT; ++t)
                         acc[s][t] = mfma_16x16x32(__builtin_bit_cast(bf16x8, x[t][j]),
                                                   __builtin_bit_cast(bf16x8, w[s][j]), acc[s][t]);
-                load_part(W, rows, next, j, K);
+                load_part(S, next, j);
             }
         } else {
             constexpr int kPer = Group / 32;  // matrix instructions a group
@@ -158,42 +188,47 @@ struct Chunk {
                 now[s][0] = sc[s][0];
                 now[s][1] = sc[s][1];
             }
-            load_packed(W, next, K);
-            f32x4 sum[kGroupsOf16][RT], base[RT];
+            load_packed(S, next);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                bf16x8 xs[RT];
+            for (int j0 = 0; j0 < 4; j0 += kPer) {
+                bf16x8 xs[RT][kPer];
+                f32x4 base[RT];
 #pragma unroll
-                for (int t = 0; t < RT; ++t) {
-                    // k in the order (0, 4), (1, 5), (2, 6), (3, 7) in which the weights' nibbles come apart
-                    const u32x4 v = x[t][j];
-                    const u32x4 p = {__builtin_amdgcn_perm(v[2], v[0], 0x05040100),
-                                     __builtin_amdgcn_perm(v[2], v[0], 0x07060302),
-                                     __builtin_amdgcn_perm(v[3], v[1], 0x05040100),
-                                     __builtin_amdgcn_perm(v[3], v[1], 0x07060302)};
-                    xs[t] = __builtin_bit_cast(bf16x8, p);
-                    if (j % kPer == 0) base[t] = f32x4{0, 0, 0, 0};
-                    base[t] = mfma_16x16x32(xs[t], __builtin_bit_cast(bf16x8, minus136), base[t]);
-                }
-                load_part(W, rows, next, j, K);
-#pragma unroll
-                for (int s = 0; s < kGroupsOf16; ++s) {
-                    const unsigned v = d[s][j];
-                    const u32x4 p = {(v & 0x000f000fu) | 0x43004300u, ((v >> 4) & 0x000f000fu) | 0x43004300u,
-                                     ((v >> 8) & 0x000f000fu) | 0x43004300u, ((v >> 12) & 0x000f000fu) | 0x43004300u};
+                for (int j = 0; j < kPer; ++j) {
 #pragma unroll
                     for (int t = 0; t < RT; ++t) {
-                        if (j % kPer == 0) sum[s][t] = f32x4{0, 0, 0, 0};
-                        sum[s][t] = mfma_16x16x32(xs[t], __builtin_bit_cast(bf16x8, p), sum[s][t]);
+                        // k in the order (0, 4), (1, 5), (2, 6), (3, 7) in which the weights' nibbles come apart
+                        const u32x4 v = x[t][j0 + j];
+                        const u32x4 p = {__builtin_amdgcn_perm(v[2], v[0], 0x05040100),
+                                         __builtin_amdgcn_perm(v[2], v[0], 0x07060302),
+                                         __builtin_amdgcn_perm(v[3], v[1], 0x05040100),
+                                         __builtin_amdgcn_perm(v[3], v[1], 0x07060302)};
+                        xs[t][j] = __builtin_bit_cast(bf16x8, p);
+                        const f32x4 zero = {0, 0, 0, 0};
+                        base[t] = mfma_16x16x32(xs[t][j], __builtin_bit_cast(bf16x8, minus136), j ? base[t] : zero);
                     }
-                    if (j % kPer == kPer - 1) {
-                        const int g = j / kPer;
-                        const float f = g & 1 ? bf16_hi(now[s][g >> 1]) : bf16_lo(now[s][g >> 1]);
+                    load_part(S, next, j0 + j);
+                }
+#pragma unroll
+                for (int s = 0; s < kGroupsOf16; ++s) {
+                    f32x4 sum[RT];
+#pragma unroll
+                    for (int j = 0; j < kPer; ++j) {
+                        const unsigned v = d[s][j0 + j];
+                        const u32x4 p = {(v & 0x000f000fu) | 0x43004300u, ((v >> 4) & 0x000f000fu) | 0x43004300u,
+                                         ((v >> 8) & 0x000f000fu) | 0x43004300u,
+                                         ((v >> 12) & 0x000f000fu) | 0x43004300u};
 #pragma unroll
                         for (int t = 0; t < RT; ++t)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) acc[s][t][i] = fmaf(sum[s][t][i] + base[t][i], f, acc[s][t][i]);
+                            sum[t] = mfma_16x16x32(xs[t][j], __builtin_bit_cast(bf16x8, p), j ? sum[t] : base[t]);
                     }
+                    const int g = j0 / kPer;
+                    const float f = g & 1 ? bf16_hi(now[s][g >> 1]) : bf16_lo(now[s][g >> 1]);
+#pragma unroll
+                    for (int t = 0; t < RT; ++t)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) acc[s][t][i] = fmaf(sum[t][i], f, acc[s][t][i]);
+                    if (RT > 2) __builtin_amdgcn_sched_barrier(0);  // keeps the registers of one group apart
                 }
             }
         }
@@ -201,10 +236,10 @@ struct Chunk {
 };
 
 // How a block's eight waves share its work: KS ways over k, the rest over features; row tiles of up to Rows.
-template <bool Few>
+template <bool Few, int Ways>
 struct Split {
     static constexpr int kRows = Few ? 16 : 64;
-    static constexpr int KS = Few ? 8 : 2;
+    static constexpr int KS = Ways;
     static constexpr int FS = kWaves / KS;
     static constexpr int kLds = FS * (KS / 2) * kGroupsOf16 * (kRows / 16) * kWave * 16;
 };
@@ -246,10 +281,10 @@ __device__ __forceinline__ void save(const SavedActs& to, int64_t row, int side,
 }
 
 // Up: features c and c + N of the weights make feature c of the output, h = act(gate) * up.
-template <int Group, bool Up, bool Few, bool Whole>
+template <int Group, bool Up, bool Few, int Ways, bool Whole>
 __global__ __launch_bounds__(kThreads) void ffn_few_kernel(ExpertShape S, FewArgs A, GridSpan span)
 {
-    typedef Split<Few> P;
+    typedef Split<Few, Ways> P;
     constexpr int kOut = Up ? 32 : 64;  // output features of a wave
     __shared__ __align__(16) char lds[P::kLds];
     const int b = span_block(span), tile = b / A.across, place = b - tile * A.across;
@@ -258,15 +293,15 @@ __global__ __launch_bounds__(kThreads) void ffn_few_kernel(ExpertShape S, FewArg
     if (bad || e < 0) return;
     const int ks = wave_id() % P::KS, fs = wave_id() / P::KS, K = A.K, N = A.N;
     const int n0 = (place * P::FS + fs) * kOut;
-    Weights<Group> W;
+    Source<Group> from;
+    from.init(K);
     const int64_t wrow = (int64_t)e * (Up ? 2 * N : N) + n0;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int64_t first = wrow + (Up ? (i ? N : 0) : 32 * i);
-        W.side(i, A.w + first * (Group ? K / 2 : K * 2), Group ? A.scale + first * (K / (Group ? Group : 1)) * 2 : nullptr,
-               Up ? N - n0 : N - n0 - 32 * i, K);
+        from.side(i, A.w + first * from.ld, A.scale + first * from.sld, Up ? N - n0 : N - n0 - 32 * i);
     }
-    const __amdgpu_buffer_rsrc_t rows = buffer(A.x + (int64_t)row0 * K * 2, (int64_t)nr * K * 2);
+    from.x.init(A.x + (int64_t)row0 * K * 2, (int64_t)nr * K * 2);
     const auto run = [&](auto tiles) {
         constexpr int RT = decltype(tiles)::value;
         f32x4 acc[kGroupsOf16][RT];
@@ -274,28 +309,28 @@ __global__ __launch_bounds__(kThreads) void ffn_few_kernel(ExpertShape S, FewArg
         for (int s = 0; s < kGroupsOf16; ++s)
 #pragma unroll
             for (int t = 0; t < RT; ++t) acc[s][t] = f32x4{0, 0, 0, 0};
-        const int chunks = (K + kChunk - 1) / kChunk;
         Chunk<Group, RT, Whole> chunk;  // past the last one, loads read nothing
-        chunk.load(W, rows, ks, K);
+        chunk.load(from, ks);
 #pragma unroll 1
-        for (int c = ks; c < chunks; c += P::KS) chunk.add_to(acc, W, rows, c + P::KS, K);
+        for (int c = ks; c < from.chunks; c += P::KS) chunk.add_to(acc, from, c + P::KS);
         // the waves of a feature set add up pairwise
-        f32x4* const mine = (f32x4*)lds + (size_t)fs * (P::KS / 2) * kGroupsOf16 * RT * kWave;
+        f32x4* const mine = (f32x4*)lds + (size_t)fs * (P::KS / 2) * kGroupsOf16 * RT * kWave + lane_id();
 #pragma unroll
-        for (int half = P::KS / 2; half >= 1; half /= 2) {
-            if (half < P::KS / 2) __syncthreads();
+        for (int level = 0; (2 << level) <= P::KS; ++level) {
+            const int half = P::KS >> (level + 1);
+            if (level > 0) __syncthreads();
             if (ks >= half && ks < 2 * half)
 #pragma unroll
                 for (int s = 0; s < kGroupsOf16; ++s)
 #pragma unroll
                     for (int t = 0; t < RT; ++t)
-                        mine[((ks - half) * kGroupsOf16 * RT + s * RT + t) * kWave + lane_id()] = acc[s][t];
+                        mine[(((ks - half) * kGroupsOf16 + s) * RT + t) * kWave] = acc[s][t];
             __syncthreads();
             if (ks < half)
 #pragma unroll
                 for (int s = 0; s < kGroupsOf16; ++s)
 #pragma unroll
-                    for (int t = 0; t < RT; ++t) acc[s][t] += mine[(ks * kGroupsOf16 * RT + s * RT + t) * kWave + lane_id()];
+                    for (int t = 0; t < RT; ++t) acc[s][t] += mine[((ks * kGroupsOf16 + s) * RT + t) * kWave];
         }
         if (ks != 0) return;
         unsigned short* const out = (unsigned short*)A.out;
@@ -333,34 +368,43 @@ __global__ __launch_bounds__(kThreads) void ffn_few_kernel(ExpertShape S, FewArg
     }
 }
 
-template <int Group, bool Up, bool Few, bool Whole>
+template <int Group, bool Up, bool Few, int Ways, bool Whole>
 hipError_t launch(const ExpertShape& S, FewArgs A, hipStream_t s)
 {
-    typedef Split<Few> P;
+    typedef Split<Few, Ways> P;
     const int out = (Up ? 32 : 64) * P::FS;
     A.across = (A.N + out - 1) / out;
     const int64_t tiles = (int64_t)S.P / P::kRows + (S.P < S.E ? S.P : S.E);
     return launch_spans(tiles * A.across, kThreads, [&](dim3 grid, GridSpan span) {
-        ffn_few_kernel<Group, Up, Few, Whole><<<grid, kThreads, 0, s>>>(S, A, span);
+        ffn_few_kernel<Group, Up, Few, Ways, Whole><<<grid, kThreads, 0, s>>>(S, A, span);
     });
 }
 
 // Rows an expert has on average, of those that can have one.
 bool few_each(const ExpertShape& S, int rows) { return S.P <= (int64_t)rows * (S.P < S.E ? S.P : S.E); }
 
-template <bool Up, bool Few>
-hipError_t launch_w4_of(const ExpertShape& S, const FewArgs& A, int group, hipStream_t s)
+template <int Group, bool Up, bool Whole>
+hipError_t launch_as(const ExpertShape& S, const FewArgs& A, hipStream_t s)
 {
-    const bool whole = A.K % kChunk == 0;
-    if (group == 128) return launch<128, Up, Few, true>(S, A, s);
-    if (group == 64) return whole ? launch<64, Up, Few, true>(S, A, s) : launch<64, Up, Few, false>(S, A, s);
-    return whole ? launch<32, Up, Few, true>(S, A, s) : launch<32, Up, Few, false>(S, A, s);
+    if (!few_each(S, 16)) return launch<Group, Up, false, 2, Whole>(S, A, s);
+    if (A.K >= kLongK) return launch<Group, Up, true, 8, Whole>(S, A, s);
+    return launch<Group, Up, true, 2, Whole>(S, A, s);
 }
 
 template <bool Up>
 hipError_t launch_w4(const ExpertShape& S, const FewArgs& A, int group, hipStream_t s)
 {
-    return few_each(S, 16) ? launch_w4_of<Up, true>(S, A, group, s) : launch_w4_of<Up, false>(S, A, group, s);
+    const bool whole = A.K % kChunk == 0;
+    if (group == 128) return launch_as<128, Up, true>(S, A, s);
+    if (group == 64) return whole ? launch_as<64, Up, true>(S, A, s) : launch_as<64, Up, false>(S, A, s);
+    return whole ? launch_as<32, Up, true>(S, A, s) : launch_as<32, Up, false>(S, A, s);
+}
+
+template <bool Up>
+hipError_t launch_bf16(const ExpertShape& S, const FewArgs& A, hipStream_t s)
+{
+    if (A.K % kChunk) return launch<0, Up, true, 8, false>(S, A, s);
+    return A.K >= kLongK ? launch<0, Up, true, 8, true>(S, A, s) : launch<0, Up, true, 2, true>(S, A, s);
 }
 
 }  // namespace
@@ -370,12 +414,12 @@ bool ffn_is_few(const ExpertShape& S) { return few_each(S, 16); }
 hipError_t launch_few_up(const ExpertShape& S, const void* xe, const void* w_gate_up, void* h, SavedActs saved,
                          hipStream_t s)
 {
-    return launch<0, true, true, false>(S, FewArgs{(const char*)xe, (const char*)w_gate_up, nullptr, (char*)h, S.H, S.I, saved, 0}, s);
+    return launch_bf16<true>(S, FewArgs{(const char*)xe, (const char*)w_gate_up, nullptr, (char*)h, S.H, S.I, saved, 0}, s);
 }
 
 hipError_t launch_few_down(const ExpertShape& S, const void* h, const void* w_down, void* ye, hipStream_t s)
 {
-    return launch<0, false, true, false>(S, FewArgs{(const char*)h, (const char*)w_down, nullptr, (char*)ye, S.I, S.H, SavedActs{}, 0}, s);
+    return launch_bf16<false>(S, FewArgs{(const char*)h, (const char*)w_down, nullptr, (char*)ye, S.I, S.H, SavedActs{}, 0}, s);
 }
 
 hipError_t launch_w4_up(const ExpertShape& S, const void* xe, const void* q, const void* scale, int group, void* h,

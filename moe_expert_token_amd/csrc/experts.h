@@ -118,27 +118,42 @@ __device__ __forceinline__ float int8_of(unsigned u, int i) { return (float)(int
 __device__ __forceinline__ int segment_tile(const int32_t* __restrict__ offset, int E, int rows_per_tile, int unit,
                                             int t, int* first, int* count)
 {
-    const int lane = lane_id();
-    int base = 0;
-    for (int e0 = 0; e0 < E; e0 += kWave) {
-        const int e = e0 + lane;
-        const int lo = offset[e < E ? e : E], hi = offset[e < E ? e + 1 : E];
-        const int rows = hi - lo, tiles = (rows + rows_per_tile - 1) / rows_per_tile;
-        const int upto = wave_inclusive_scan(tiles), all = __builtin_amdgcn_readlane(upto, kWave - 1);
-        if (t < base + all) {
-            const unsigned long long m = __ballot(base + upto > t);
-            const int src = __builtin_ctzll(m);
-            const int slo = __builtin_amdgcn_readlane(lo, src), srows = __builtin_amdgcn_readlane(rows, src);
-            const int stiles = __builtin_amdgcn_readlane(tiles, src);
-            const int i = t - base - (__builtin_amdgcn_readlane(upto, src) - stiles);
-            const int units = (srows + unit - 1) / unit, each = (units + stiles - 1) / stiles * unit;
-            *first = slo + i * each;
-            *count = min(each, srows - i * each);
-            return e0 + src;
-        }
-        base += all;
+    // a lane has `per` neighbouring experts; their offsets are loaded together, and again (from the cache) to find
+    // the tile's among them
+    const int lane = lane_id(), per = (E + kWave - 1) / kWave, e0 = min(lane * per, E), e1 = min(e0 + per, E);
+    const auto tiles_of = [=](int rows) { return (rows + rows_per_tile - 1) / rows_per_tile; };
+    int mine = 0, lo = offset[e0];
+#pragma unroll 4
+    for (int i = 1; i <= per; ++i) {
+        const int hi = offset[min(e0 + i, e1)];
+        mine += tiles_of(hi - lo);
+        lo = hi;
     }
-    return -1;
+    const int upto = wave_inclusive_scan(mine);
+    const unsigned long long m = __ballot(upto > t);
+    if (!m) return -1;
+    const int src = __builtin_ctzll(m);
+    int left = t - (upto - mine), found = 0, at = 0, rows = 0, tiles = 0;
+    lo = offset[e0];
+#pragma unroll 4
+    for (int i = 1; i <= per; ++i) {
+        const int hi = offset[min(e0 + i, e1)], n = tiles_of(hi - lo);
+        if (left >= 0 && left < n) {
+            found = e0 + i - 1;
+            at = lo;
+            rows = hi - lo;
+            tiles = n;
+            break;
+        }
+        left -= n;
+        lo = hi;
+    }
+    const int i = __builtin_amdgcn_readlane(left, src), first_row = __builtin_amdgcn_readlane(at, src);
+    const int all = __builtin_amdgcn_readlane(rows, src), n = __builtin_amdgcn_readlane(tiles, src);
+    const int units = (all + unit - 1) / unit, each = (units + n - 1) / n * unit;
+    *first = first_row + i * each;
+    *count = min(each, all - i * each);
+    return __builtin_amdgcn_readlane(found, src);
 }
 
 }  // namespace ms

@@ -61,10 +61,12 @@ __device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t r, unsigned at)
 }
 
 // What a wave reads: the weights of its feature groups (group s lies in stream s >> 1, 16 (s & 1) rows of `ld`
-// bytes in), their scales and the rows.  Group is 0 for bf16 weights, else the 4-bit weights' group size.
+// bytes in), their scales (rows of `sld` bytes, in memory or copied to LDS) and the rows.  Group is 0 for bf16
+// weights, else the 4-bit weights' group size.
 template <int Group>
 struct Source {
     Stream w[2], sc[2], x;
+    const char* staged[2];
     int K, chunks;
     unsigned ld, sld, xld;
 
@@ -83,56 +85,68 @@ struct Source {
     }
 };
 
-// What a wave has in hand of one chunk: weights, their scales (bf16 pairs) and the rows' fragments.  As soon as a
-// part is in use, the next chunk's is loaded in its place.  Whole: K is a multiple of the chunk, so that only
-// whole chunks are read and a lane's offsets never change.
-template <int Group, int RT, bool Whole>
-struct Chunk {
+// 16 rows a group and stream: what a wave has of the weights of one chunk.
+template <int Group>
+struct Packed {
     u32x4 w[kGroupsOf16][Group ? 1 : 4];
-    unsigned sc[Group ? kGroupsOf16 : 1][2];
+};
+
+// The rows' fragments of a chunk.  As soon as a part of weights or rows is in use, a later chunk's is loaded in its
+// place.  Whole: K is a multiple of the chunk, so that only whole chunks are read and a lane's offsets never change.
+template <int Group, int RT, bool Whole, bool Staged>
+struct Chunk {
     u32x4 x[RT][4];
 
-    // 4-bit weights and scales of chunk c
-    __device__ __forceinline__ void load_packed(const Source<Group>& S, int c)
+    // 4-bit weights of chunk c
+    __device__ __forceinline__ static void load_packed(Packed<Group>& to, const Source<Group>& S, int c)
     {
-        constexpr int G = Group ? Group : 1;
-        const int lane = lane_id(), r = lane & 15, q = lane >> 4, k0 = c * kChunk;
+        const int lane = lane_id(), r = lane & 15, q = lane >> 4;
         const bool any = c < S.chunks;
         unsigned at = r * S.ld + q * 16;
-        if (!Whole && k0 + q * 32 >= S.K) at = kOutside;
+        if (!Whole && c * kChunk + q * 32 >= S.K) at = kOutside;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const __amdgpu_buffer_rsrc_t b = S.w[i].from(c * (kChunk / 2), any);
-            w[2 * i][0] = load16(b, at);
-            w[2 * i + 1][0] = load16(b, at + 16 * S.ld);
+            to.w[2 * i][0] = load16(b, at);
+            to.w[2 * i + 1][0] = load16(b, at + 16 * S.ld);
         }
-        const unsigned sat = r * S.sld;
-#pragma unroll
-        for (int s = 0; s < kGroupsOf16; ++s) {
-            const __amdgpu_buffer_rsrc_t b = S.sc[s >> 1].from(c * (kChunk / G) * 2, any);
-            const unsigned f = sat + (s & 1) * 16 * S.sld;
-            if constexpr (Group == 128) {
-                sc[s][0] = __builtin_amdgcn_raw_buffer_load_b16(b, f, 0, 0);
-            } else if constexpr (!Whole) {  // a row's scales need not be aligned, and the last chunk has fewer of them
-#pragma unroll
-                for (int i = 0; i < kChunk / G; i += 2) {
-                    const unsigned lo = k0 + i * G < S.K ? f + 2 * i : kOutside;
-                    const unsigned hi = k0 + (i + 1) * G < S.K ? f + 2 * i + 2 : kOutside;
-                    sc[s][i >> 1] = (unsigned)__builtin_amdgcn_raw_buffer_load_b16(b, lo, 0, 0) |
-                                    (unsigned)__builtin_amdgcn_raw_buffer_load_b16(b, hi, 0, 0) << 16;
-                }
-            } else if constexpr (Group == 64) {
-                sc[s][0] = __builtin_amdgcn_raw_buffer_load_b32(b, f, 0, 0);
+    }
+
+    // the scales of a row of group s in chunk c, as bf16 pairs
+    __device__ __forceinline__ static void scales_of(const Source<Group>& S, int c, int s, unsigned (&to)[2])
+    {
+        constexpr int G = Group ? Group : 1, kPer = kChunk / G;
+        const int r = (lane_id() & 15) + (s & 1) * 16;
+        if constexpr (Staged) {
+            const char* const row = S.staged[s >> 1] + r * S.sld;
+            if constexpr (Whole && Group == 32) {
+                const u32x2 v = *(const u32x2*)(row + c * 8);
+                to[0] = v[0];
+                to[1] = v[1];
+            } else if constexpr (Whole && Group == 64) {
+                to[0] = *(const unsigned*)(row + c * 4);
             } else {
-                const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(b, f, 0, 0);
-                sc[s][0] = v[0];
-                sc[s][1] = v[1];
+                // groups past the row's last stand for weights of zero; their scale must be one of the row's own
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) {
+                    const int g = min(c * kPer + i, S.K / G - 1);
+                    const unsigned v = *(const unsigned short*)(row + 2 * g);
+                    to[i >> 1] = i & 1 ? to[i >> 1] | v << 16 : v;
+                }
+            }
+        } else {
+            const __amdgpu_buffer_rsrc_t b = S.sc[s >> 1].from(0, true);
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const int g = min(c * kPer + i, S.K / G - 1);
+                const unsigned v = __builtin_amdgcn_raw_buffer_load_b16(b, r * S.sld + 2 * g, 0, 0);
+                to[i >> 1] = i & 1 ? to[i >> 1] | v << 16 : v;
             }
         }
     }
 
     // the 32 k at j of chunk c: fragments, and weights where they are bf16
-    __device__ __forceinline__ void load_part(const Source<Group>& S, int c, int j)
+    __device__ __forceinline__ void load_part(Packed<Group>& to, const Source<Group>& S, int c, int j)
     {
         const int lane = lane_id(), r = lane & 15, q = lane >> 4;
         const bool any = c < S.chunks, in = Whole || c * kChunk + j * 32 + q * 8 < S.K;
@@ -141,8 +155,8 @@ struct Chunk {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const __amdgpu_buffer_rsrc_t b = S.w[i].from(c * kChunk * 2, any);
-                w[2 * i][j] = load16(b, at);
-                w[2 * i + 1][j] = load16(b, at + 16 * S.ld);
+                to.w[2 * i][j] = load16(b, at);
+                to.w[2 * i + 1][j] = load16(b, at + 16 * S.ld);
             }
         }
         const __amdgpu_buffer_rsrc_t b = S.x.from(c * kChunk * 2, any);
@@ -151,15 +165,9 @@ struct Chunk {
         for (int t = 0; t < RT; ++t) x[t][j] = load16(b, at + t * 16 * S.xld);
     }
 
-    __device__ __forceinline__ void load(const Source<Group>& S, int c)
-    {
-        if constexpr (Group != 0) load_packed(S, c);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) load_part(S, c, j);
-    }
-
-    // Adds this chunk's products to acc, and leaves chunk `next` in its place.
-    __device__ __forceinline__ void add_to(f32x4 (&acc)[kGroupsOf16][RT], const Source<Group>& S, int next)
+    // Adds chunk c's products to acc, and leaves chunk `next` in its place.
+    __device__ __forceinline__ void add_to(f32x4 (&acc)[kGroupsOf16][RT], Packed<Group>& P, const Source<Group>& S,
+                                           int c, int next)
     {
         if constexpr (Group == 0) {
 #pragma unroll
@@ -169,8 +177,9 @@ struct Chunk {
 #pragma unroll
                     for (int t = 0; t < RT; ++t)
                         acc[s][t] = mfma_16x16x32(__builtin_bit_cast(bf16x8, x[t][j]),
-                                                  __builtin_bit_cast(bf16x8, w[s][j]), acc[s][t]);
-                load_part(S, next, j);
+                                                  __builtin_bit_cast(bf16x8, P.w[s][j]), acc[s][t]);
+                load_part(P, S, next, j);
+                __builtin_amdgcn_sched_barrier(0);
             }
         } else {
             constexpr int kPer = Group / 32;  // matrix instructions a group
@@ -180,15 +189,18 @@ struct Chunk {
 #pragma unroll
             for (int s = 0; s < kGroupsOf16; ++s) {
                 // register j of quarter q <-> register q of quarter j
-                const auto a = __builtin_amdgcn_permlane32_swap(w[s][0][0], w[s][0][2], false, false);
-                const auto b = __builtin_amdgcn_permlane32_swap(w[s][0][1], w[s][0][3], false, false);
+                const u32x4 w = P.w[s][0];
+                const auto a = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
+                const auto b = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
                 const auto e = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
                 const auto f = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
                 d[s] = u32x4{e[0], e[1], f[0], f[1]};
-                now[s][0] = sc[s][0];
-                now[s][1] = sc[s][1];
+                scales_of(S, c, s, now[s]);
             }
-            load_packed(S, next);
+            load_packed(P, S, next);
+            __builtin_amdgcn_sched_barrier(0);  // loads go out here, not where the compiler would save registers
+            unsigned magic = 0x43004300u;       // in a vector register, for v_and_or_b32 to take it with the mask
+            asm("" : "+v"(magic));
 #pragma unroll
             for (int j0 = 0; j0 < 4; j0 += kPer) {
                 bf16x8 xs[RT][kPer];
@@ -207,17 +219,17 @@ struct Chunk {
                         const f32x4 zero = {0, 0, 0, 0};
                         base[t] = mfma_16x16x32(xs[t][j], __builtin_bit_cast(bf16x8, minus136), j ? base[t] : zero);
                     }
-                    load_part(S, next, j0 + j);
+                    load_part(P, S, next, j0 + j);
                 }
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int s = 0; s < kGroupsOf16; ++s) {
                     f32x4 sum[RT];
 #pragma unroll
                     for (int j = 0; j < kPer; ++j) {
                         const unsigned v = d[s][j0 + j];
-                        const u32x4 p = {(v & 0x000f000fu) | 0x43004300u, ((v >> 4) & 0x000f000fu) | 0x43004300u,
-                                         ((v >> 8) & 0x000f000fu) | 0x43004300u,
-                                         ((v >> 12) & 0x000f000fu) | 0x43004300u};
+                        const u32x4 p = {(v & 0x000f000fu) | magic, ((v >> 4) & 0x000f000fu) | magic,
+                                         ((v >> 8) & 0x000f000fu) | magic, ((v >> 12) & 0x000f000fu) | magic};
 #pragma unroll
                         for (int t = 0; t < RT; ++t)
                             sum[t] = mfma_16x16x32(xs[t][j], __builtin_bit_cast(bf16x8, p), j ? sum[t] : base[t]);
@@ -241,7 +253,8 @@ struct Split {
     static constexpr int kRows = Few ? 16 : 64;
     static constexpr int KS = Ways;
     static constexpr int FS = kWaves / KS;
-    static constexpr int kLds = FS * (KS / 2) * kGroupsOf16 * (kRows / 16) * kWave * 16;
+    static constexpr int kSums = kWaves * kGroupsOf16 * (kRows / 16) * kWave * 16;  // bytes of the waves' sums
+    static constexpr int kStage = kSums > (64 << 10) ? kSums : 64 << 10;             // room for scales, then sums
 };
 
 struct FewArgs {
@@ -256,109 +269,120 @@ struct FewArgs {
 
 __device__ __forceinline__ unsigned short bf16_of(float v) { return (unsigned short)bf16_pack2(v, v); }
 
-// Keeps a row's pre-activations of features n (a) and n + 16 (b), the gate's (side 0) or the up projection's; the
-// sixteen lanes of a row hold a group of an 8-bit checkpoint.
-__device__ __forceinline__ void save(const SavedActs& to, int64_t row, int side, int n, int N, float a, float b, bool ok)
+// Keeps a row's pre-activation of feature n, the gate's (side 0) or the up projection's; 32 neighbouring lanes hold
+// a group of an 8-bit checkpoint (zeros past the row's end).
+__device__ __forceinline__ void save(const SavedActs& to, int64_t row, int side, int n, int N, float v, bool ok)
 {
-    const bool in_a = ok && n < N, in_b = ok && n + 16 < N;
     const int64_t at = row * 2 * N + (side ? N : 0) + n;
     if (!to.scale) {
-        if (in_a) ((unsigned short*)to.data)[at] = bf16_of(a);
-        if (in_b) ((unsigned short*)to.data)[at + 16] = bf16_of(b);
+        if (ok) ((unsigned short*)to.data)[at] = bf16_of(v);
         return;
     }
-    const float x = n < N ? fabsf(a) : 0.0f, y = n + 16 < N ? fabsf(b) : 0.0f;
-    float top = fmaxf(x, y);
-    if (!(x <= 3.40282347e38f) || !(y <= 3.40282347e38f)) top = __uint_as_float(0x7f800000u);
+    float top = ok ? fabsf(v) : 0.0f;
+    if (!(top <= 3.40282347e38f)) top = __uint_as_float(0x7f800000u);
 #pragma unroll
-    for (int d = 1; d < 16; d <<= 1) top = fmaxf(top, __shfl_xor(top, d, kWave));
-    const float step = step8(top), inv = 1.0f / step;
-    if (in_a) ((unsigned char*)to.data)[at] = (unsigned char)pack8x4(a, a, a, a, inv);
-    if (in_b) ((unsigned char*)to.data)[at + 16] = (unsigned char)pack8x4(b, b, b, b, inv);
-    if (in_a && (n & 31) == 0)
+    for (int d = 1; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor(top, d, kWave));
+    const float step = step8(top);
+    if (ok) ((unsigned char*)to.data)[at] = (unsigned char)pack8x4(v, v, v, v, 1.0f / step);
+    if (ok && n % kGroup8 == 0)
         ((unsigned short*)to.scale)[(row * 2 + side) * ((N + kGroup8 - 1) / kGroup8) + n / kGroup8] =
             (unsigned short)(__float_as_uint(step) >> 16);
 }
 
 // Up: features c and c + N of the weights make feature c of the output, h = act(gate) * up.
-template <int Group, bool Up, bool Few, int Ways, bool Whole>
+template <int Group, bool Up, bool Few, int Ways, bool Whole, bool Staged>
 __global__ __launch_bounds__(kThreads) void ffn_few_kernel(ExpertShape S, FewArgs A, GridSpan span)
 {
     typedef Split<Few, Ways> P;
     constexpr int kOut = Up ? 32 : 64;  // output features of a wave
-    __shared__ __align__(16) char lds[P::kLds];
+    __shared__ __align__(16) char lds[Staged ? P::kStage : P::kSums];
     const int b = span_block(span), tile = b / A.across, place = b - tile * A.across;
     int row0, nr;
     const int bad = *S.status, e = segment_tile(S.offset, S.E, P::kRows, 16, tile, &row0, &nr);
     if (bad || e < 0) return;
     const int ks = wave_id() % P::KS, fs = wave_id() / P::KS, K = A.K, N = A.N;
-    const int n0 = (place * P::FS + fs) * kOut;
     Source<Group> from;
     from.init(K);
+    from.x.init(A.x + (int64_t)row0 * K * 2, (int64_t)nr * K * 2);
+    const int n0 = (place * P::FS + fs) * kOut;  // this wave's first output feature
     const int64_t wrow = (int64_t)e * (Up ? 2 * N : N) + n0;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int64_t first = wrow + (Up ? (i ? N : 0) : 32 * i);
         from.side(i, A.w + first * from.ld, A.scale + first * from.sld, Up ? N - n0 : N - n0 - 32 * i);
     }
-    from.x.init(A.x + (int64_t)row0 * K * 2, (int64_t)nr * K * 2);
+    if constexpr (Staged) {  // side i of feature set f at (2 f + i) * 32 rows: contiguous in memory, 64 bytes aligned
+        const int side_bytes = 32 * from.sld, t = ks * kWave + lane_id();
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            char* const to = lds + (2 * fs + i) * side_bytes;
+            from.staged[i] = to;
+            const __amdgpu_buffer_rsrc_t b = from.sc[i].from(0, true);
+            for (int at = t * 16; at < side_bytes; at += P::KS * kWave * 16) *(u32x4*)(to + at) = load16(b, at);
+        }
+    }
     const auto run = [&](auto tiles) {
         constexpr int RT = decltype(tiles)::value;
+        constexpr int kSet = kGroupsOf16 * RT * kWave;  // f32x4 of a wave's sums
+        // bf16 rows are read 1 KiB at a time, four chunks, before another wave's turn (340 us against 364 chunk by
+        // chunk, four tokens of 4096 x 14336); with 4-bit weights that made no difference
+        constexpr int kRun = Group ? 1 : 4;
+        const auto after = [](int c) { return (c + 1) % kRun ? c + 1 : c + 1 + (P::KS - 1) * kRun; };
         f32x4 acc[kGroupsOf16][RT];
 #pragma unroll
         for (int s = 0; s < kGroupsOf16; ++s)
 #pragma unroll
             for (int t = 0; t < RT; ++t) acc[s][t] = f32x4{0, 0, 0, 0};
-        Chunk<Group, RT, Whole> chunk;  // past the last one, loads read nothing
-        chunk.load(from, ks);
+        typedef Chunk<Group, RT, Whole, Staged> C;
+        C chunk;
+        Packed<Group> weights;
+        int c = ks * kRun;
+        if constexpr (Group != 0) C::load_packed(weights, from, c);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) chunk.load_part(weights, from, c, j);
+        if (Staged) __syncthreads();
 #pragma unroll 1
-        for (int c = ks; c < from.chunks; c += P::KS) chunk.add_to(acc, from, c + P::KS);
-        // the waves of a feature set add up pairwise
-        f32x4* const mine = (f32x4*)lds + (size_t)fs * (P::KS / 2) * kGroupsOf16 * RT * kWave + lane_id();
-#pragma unroll
-        for (int level = 0; (2 << level) <= P::KS; ++level) {
-            const int half = P::KS >> (level + 1);
-            if (level > 0) __syncthreads();
-            if (ks >= half && ks < 2 * half)
-#pragma unroll
-                for (int s = 0; s < kGroupsOf16; ++s)
-#pragma unroll
-                    for (int t = 0; t < RT; ++t)
-                        mine[(((ks - half) * kGroupsOf16 + s) * RT + t) * kWave] = acc[s][t];
-            __syncthreads();
-            if (ks < half)
-#pragma unroll
-                for (int s = 0; s < kGroupsOf16; ++s)
-#pragma unroll
-                    for (int t = 0; t < RT; ++t) acc[s][t] += mine[((ks * kGroupsOf16 + s) * RT + t) * kWave];
+        while (c < from.chunks) {  // past the last chunk, loads read nothing
+            chunk.add_to(acc, weights, from, c, after(c));
+            c = after(c);
         }
-        if (ks != 0) return;
-        unsigned short* const out = (unsigned short*)A.out;
+        {
+            if (Staged) __syncthreads();  // the scales' room is the sums'
+            f32x4* const all = (f32x4*)lds + (size_t)fs * P::KS * kSet;
 #pragma unroll
-        for (int t = 0; t < RT; ++t)
+            for (int s = 0; s < kGroupsOf16; ++s)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r = 16 * t + 4 * (lane_id() >> 4) + i, n = n0 + (lane_id() & 15);
+                for (int t = 0; t < RT; ++t) all[ks * kSet + (s * RT + t) * kWave + lane_id()] = acc[s][t];
+            __syncthreads();
+            // the feature set's waves share its outputs; row r, feature f of a group is element r & 3 of lane
+            // (f & 15) + 16 (r >> 2 & 3) of row tile r >> 4
+            const float* const sums = (const float*)all;
+            const auto total = [&](int s, int r, int f) {
+                const int at = ((s * RT + (r >> 4)) * kWave + (f & 15) + 16 * ((r >> 2) & 3)) * 4 + (r & 3);
+                float v = 0;
+#pragma unroll
+                for (int i = 0; i < P::KS; ++i) v += sums[i * kSet * 4 + at];
+                return v;
+            };
+            // whole rows a turn, so that the lanes of a group stay together
+            for (int i = ks * kWave + lane_id(); i < (nr * kOut + kWave - 1) / kWave * kWave; i += P::KS * kWave) {
+                const int r = i / kOut, f = i % kOut, n = n0 + f;
+                const bool ok = r < nr && n < N;
                 const int64_t row = row0 + r;
                 if constexpr (!Up) {
-#pragma unroll
-                    for (int s = 0; s < 4; ++s)
-                        if (r < nr && n + 16 * s < N) out[row * N + n + 16 * s] = bf16_of(acc[s][t][i]);
+                    const float v = total(f >> 4, min(r, nr - 1), f);
+                    if (ok) ((unsigned short*)A.out)[row * N + n] = bf16_of(v);
                 } else {
-#pragma unroll
-                    for (int s = 0; s < 2; ++s) {
-                        float slope;
-                        const float g = acc[s][t][i], u = acc[2 + s][t][i];
-                        if (r < nr && n + 16 * s < N)
-                            out[row * N + n + 16 * s] = bf16_of(g * gate_sigmoid(g, S.c0, S.c1, &slope) * u);
-                    }
+                    float slope;
+                    const float g = total(f >> 4, min(r, nr - 1), f), u = total(2 + (f >> 4), min(r, nr - 1), f);
+                    if (ok) ((unsigned short*)A.out)[row * N + n] = bf16_of(g * gate_sigmoid(g, S.c0, S.c1, &slope) * u);
                     if (Group == 0 && A.saved.data) {
-#pragma unroll
-                        for (int side = 0; side < 2; ++side)
-                            save(A.saved, row, side, n, N, acc[2 * side][t][i], acc[2 * side + 1][t][i], r < nr);
+                        save(A.saved, row, 0, n, N, g, ok);
+                        save(A.saved, row, 1, n, N, u, ok);
                     }
                 }
             }
+        }
     };
     if constexpr (Few) {
         run(std::integral_constant<int, 1>());
@@ -368,7 +392,7 @@ __global__ __launch_bounds__(kThreads) void ffn_few_kernel(ExpertShape S, FewArg
     }
 }
 
-template <int Group, bool Up, bool Few, int Ways, bool Whole>
+template <int Group, bool Up, bool Few, int Ways, bool Whole, bool Staged>
 hipError_t launch(const ExpertShape& S, FewArgs A, hipStream_t s)
 {
     typedef Split<Few, Ways> P;
@@ -376,35 +400,42 @@ hipError_t launch(const ExpertShape& S, FewArgs A, hipStream_t s)
     A.across = (A.N + out - 1) / out;
     const int64_t tiles = (int64_t)S.P / P::kRows + (S.P < S.E ? S.P : S.E);
     return launch_spans(tiles * A.across, kThreads, [&](dim3 grid, GridSpan span) {
-        ffn_few_kernel<Group, Up, Few, Ways, Whole><<<grid, kThreads, 0, s>>>(S, A, span);
+        ffn_few_kernel<Group, Up, Few, Ways, Whole, Staged><<<grid, kThreads, 0, s>>>(S, A, span);
     });
 }
 
 // Rows an expert has on average, of those that can have one.
 bool few_each(const ExpertShape& S, int rows) { return S.P <= (int64_t)rows * (S.P < S.E ? S.P : S.E); }
 
-template <int Group, bool Up, bool Whole>
-hipError_t launch_as(const ExpertShape& S, const FewArgs& A, hipStream_t s)
+template <int Group, bool Up, bool Few, int Ways>
+hipError_t launch_w4_ways(const ExpertShape& S, const FewArgs& A, hipStream_t s)
 {
-    if (!few_each(S, 16)) return launch<Group, Up, false, 2, Whole>(S, A, s);
-    if (A.K >= kLongK) return launch<Group, Up, true, 8, Whole>(S, A, s);
-    return launch<Group, Up, true, 2, Whole>(S, A, s);
+    // the scales of a block's features fit the LDS kept for them
+    if ((int64_t)64 * Split<Few, Ways>::FS * (A.K / Group) * 2 > Split<Few, Ways>::kStage)
+        return launch<Group, Up, Few, Ways, false, false>(S, A, s);
+    return A.K % kChunk ? launch<Group, Up, Few, Ways, false, true>(S, A, s)
+                        : launch<Group, Up, Few, Ways, true, true>(S, A, s);
+}
+
+template <int Group, bool Up>
+hipError_t launch_w4_group(const ExpertShape& S, const FewArgs& A, hipStream_t s)
+{
+    if (!few_each(S, 16)) return launch_w4_ways<Group, Up, false, 2>(S, A, s);
+    return A.K >= kLongK ? launch_w4_ways<Group, Up, true, 8>(S, A, s) : launch_w4_ways<Group, Up, true, 2>(S, A, s);
 }
 
 template <bool Up>
 hipError_t launch_w4(const ExpertShape& S, const FewArgs& A, int group, hipStream_t s)
 {
-    const bool whole = A.K % kChunk == 0;
-    if (group == 128) return launch_as<128, Up, true>(S, A, s);
-    if (group == 64) return whole ? launch_as<64, Up, true>(S, A, s) : launch_as<64, Up, false>(S, A, s);
-    return whole ? launch_as<32, Up, true>(S, A, s) : launch_as<32, Up, false>(S, A, s);
+    if (group == 128) return launch_w4_group<128, Up>(S, A, s);
+    return group == 64 ? launch_w4_group<64, Up>(S, A, s) : launch_w4_group<32, Up>(S, A, s);
 }
 
 template <bool Up>
 hipError_t launch_bf16(const ExpertShape& S, const FewArgs& A, hipStream_t s)
 {
-    if (A.K % kChunk) return launch<0, Up, true, 8, false>(S, A, s);
-    return A.K >= kLongK ? launch<0, Up, true, 8, true>(S, A, s) : launch<0, Up, true, 2, true>(S, A, s);
+    if (A.K % kChunk) return launch<0, Up, true, 8, false, false>(S, A, s);
+    return A.K >= kLongK ? launch<0, Up, true, 8, true, false>(S, A, s) : launch<0, Up, true, 2, true, false>(S, A, s);
 }
 
 }  // namespace

@@ -179,7 +179,6 @@ struct Chunk {
                         acc[s][t] = mfma_16x16x32(__builtin_bit_cast(bf16x8, x[t][j]),
                                                   __builtin_bit_cast(bf16x8, P.w[s][j]), acc[s][t]);
                 load_part(P, S, next, j);
-                __builtin_amdgcn_sched_barrier(0);
             }
         } else {
             constexpr int kPer = Group / 32;  // matrix instructions a group
@@ -407,21 +406,35 @@ hipError_t launch(const ExpertShape& S, FewArgs A, hipStream_t s)
 // Rows an expert has on average, of those that can have one.
 bool few_each(const ExpertShape& S, int rows) { return S.P <= (int64_t)rows * (S.P < S.E ? S.P : S.E); }
 
+// Whether the scales of a block's features fit the LDS kept for them.
+template <bool Few, int Ways>
+bool scales_fit(int K, int group)
+{
+    return (int64_t)64 * Split<Few, Ways>::FS * (K / group) * 2 <= Split<Few, Ways>::kStage;
+}
+
 template <int Group, bool Up, bool Few, int Ways>
 hipError_t launch_w4_ways(const ExpertShape& S, const FewArgs& A, hipStream_t s)
 {
-    // the scales of a block's features fit the LDS kept for them
-    if ((int64_t)64 * Split<Few, Ways>::FS * (A.K / Group) * 2 > Split<Few, Ways>::kStage)
-        return launch<Group, Up, Few, Ways, false, false>(S, A, s);
     return A.K % kChunk ? launch<Group, Up, Few, Ways, false, true>(S, A, s)
                         : launch<Group, Up, Few, Ways, true, true>(S, A, s);
+}
+
+// Few ways over k leave more features to a block, which then share its rows' loads; many ways fit longer rows of
+// scales, and keep every wave busy where there is little else to do (203 tokens, 14336 to 4096, groups of 32: 153 us
+// with eight ways against 446 with two and scales from memory; 4096 to 2 x 14336: 313 with two, 346 with eight).
+template <int Group, bool Up, bool Few>
+hipError_t launch_w4_rows(const ExpertShape& S, const FewArgs& A, hipStream_t s)
+{
+    if (scales_fit<Few, 2>(A.K, Group) && (!Few || A.K < kLongK)) return launch_w4_ways<Group, Up, Few, 2>(S, A, s);
+    if (scales_fit<Few, 8>(A.K, Group)) return launch_w4_ways<Group, Up, Few, 8>(S, A, s);
+    return launch<Group, Up, Few, 8, false, false>(S, A, s);
 }
 
 template <int Group, bool Up>
 hipError_t launch_w4_group(const ExpertShape& S, const FewArgs& A, hipStream_t s)
 {
-    if (!few_each(S, 16)) return launch_w4_ways<Group, Up, false, 2>(S, A, s);
-    return A.K >= kLongK ? launch_w4_ways<Group, Up, true, 8>(S, A, s) : launch_w4_ways<Group, Up, true, 2>(S, A, s);
+    return few_each(S, 16) ? launch_w4_rows<Group, Up, true>(S, A, s) : launch_w4_rows<Group, Up, false>(S, A, s);
 }
 
 template <bool Up>

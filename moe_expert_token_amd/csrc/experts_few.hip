@@ -246,10 +246,12 @@ struct Chunk {
     }
 };
 
-// How a block's eight waves share its work: KS ways over k, the rest over features; row tiles of up to Rows.
-template <bool Few, int Ways>
+// How a block's eight waves share its work: KS ways over k, the rest over features; row tiles of up to kRows.
+template <int Group, bool Few, int Ways>
 struct Split {
-    static constexpr int kRows = Few ? 16 : 64;
+    // 64 rows take every register, which groups of 32 leave just enough of; with larger groups they spill (64 rows an
+    // expert, 32 experts of 2048 x 2048, groups of 128: 312 us, against 212 in tiles of 32 rows)
+    static constexpr int kRows = Few ? 16 : Group == 32 ? 64 : 32;
     static constexpr int KS = Ways;
     static constexpr int FS = kWaves / KS;
     static constexpr int kSums = kWaves * kGroupsOf16 * (kRows / 16) * kWave * 16;  // bytes of the waves' sums
@@ -292,7 +294,7 @@ __device__ __forceinline__ void save(const SavedActs& to, int64_t row, int side,
 template <int Group, bool Up, bool Few, int Ways, bool Whole, bool Staged>
 __global__ __launch_bounds__(kThreads) void ffn_few_kernel(ExpertShape S, FewArgs A, GridSpan span)
 {
-    typedef Split<Few, Ways> P;
+    typedef Split<Group, Few, Ways> P;
     constexpr int kOut = Up ? 32 : 64;  // output features of a wave
     __shared__ __align__(16) char lds[Staged ? P::kStage : P::kSums];
     const int b = span_block(span), tile = b / A.across, place = b - tile * A.across;
@@ -386,15 +388,20 @@ __global__ __launch_bounds__(kThreads) void ffn_few_kernel(ExpertShape S, FewArg
     if constexpr (Few) {
         run(std::integral_constant<int, 1>());
     } else {
-        if (nr <= 32) run(std::integral_constant<int, 2>());
-        else run(std::integral_constant<int, 4>());
+        if constexpr (P::kRows == 32) {
+            if (nr <= 16) run(std::integral_constant<int, 1>());
+            else run(std::integral_constant<int, 2>());
+        } else {
+            if (nr <= 32) run(std::integral_constant<int, 2>());
+            else run(std::integral_constant<int, 4>());
+        }
     }
 }
 
 template <int Group, bool Up, bool Few, int Ways, bool Whole, bool Staged>
 hipError_t launch(const ExpertShape& S, FewArgs A, hipStream_t s)
 {
-    typedef Split<Few, Ways> P;
+    typedef Split<Group, Few, Ways> P;
     const int out = (Up ? 32 : 64) * P::FS;
     A.across = (A.N + out - 1) / out;
     const int64_t tiles = (int64_t)S.P / P::kRows + (S.P < S.E ? S.P : S.E);
@@ -407,10 +414,11 @@ hipError_t launch(const ExpertShape& S, FewArgs A, hipStream_t s)
 bool few_each(const ExpertShape& S, int rows) { return S.P <= (int64_t)rows * (S.P < S.E ? S.P : S.E); }
 
 // Whether the scales of a block's features fit the LDS kept for them.
-template <bool Few, int Ways>
-bool scales_fit(int K, int group)
+template <int Group, bool Few, int Ways>
+bool scales_fit(int K)
 {
-    return (int64_t)64 * Split<Few, Ways>::FS * (K / group) * 2 <= Split<Few, Ways>::kStage;
+    typedef Split<Group, Few, Ways> P;
+    return (int64_t)64 * P::FS * (K / Group) * 2 <= P::kStage;
 }
 
 template <int Group, bool Up, bool Few, int Ways>
@@ -426,15 +434,17 @@ hipError_t launch_w4_ways(const ExpertShape& S, const FewArgs& A, hipStream_t s)
 template <int Group, bool Up, bool Few>
 hipError_t launch_w4_rows(const ExpertShape& S, const FewArgs& A, hipStream_t s)
 {
-    if (scales_fit<Few, 2>(A.K, Group) && (!Few || A.K < kLongK)) return launch_w4_ways<Group, Up, Few, 2>(S, A, s);
-    if (scales_fit<Few, 8>(A.K, Group)) return launch_w4_ways<Group, Up, Few, 8>(S, A, s);
+    if (scales_fit<Group, Few, 2>(A.K) && (!Few || A.K < kLongK)) return launch_w4_ways<Group, Up, Few, 2>(S, A, s);
+    if (scales_fit<Group, Few, 8>(A.K)) return launch_w4_ways<Group, Up, Few, 8>(S, A, s);
     return launch<Group, Up, Few, 8, false, false>(S, A, s);
 }
 
 template <int Group, bool Up>
 hipError_t launch_w4_group(const ExpertShape& S, const FewArgs& A, hipStream_t s)
 {
-    return few_each(S, 16) ? launch_w4_rows<Group, Up, true>(S, A, s) : launch_w4_rows<Group, Up, false>(S, A, s);
+    // 12: at 16 rows on average half of the experts have a second tile of 16 (77 and 87 us in larger tiles, 89 and 77 in
+    // these, for 32 experts of 2048 x 2048 and 8 of 4096 x 4096)
+    return few_each(S, 12) ? launch_w4_rows<Group, Up, true>(S, A, s) : launch_w4_rows<Group, Up, false>(S, A, s);
 }
 
 template <bool Up>
@@ -453,7 +463,10 @@ hipError_t launch_bf16(const ExpertShape& S, const FewArgs& A, hipStream_t s)
 
 }  // namespace
 
-bool ffn_is_few(const ExpertShape& S) { return few_each(S, 16); }
+// Up to 8 rows on average the streams win (173 us against 206, 8 experts of 4096 x 4096; 181 against 214, 32 of 2048 x
+// 2048); at 16, where many experts have more than a tile of 16, the tiles of experts_ffn do (215 against 207, 225
+// against 213).
+bool ffn_is_few(const ExpertShape& S) { return few_each(S, 10); }
 
 hipError_t launch_few_up(const ExpertShape& S, const void* xe, const void* w_gate_up, void* h, SavedActs saved,
                          hipStream_t s)

@@ -59,11 +59,14 @@ __device__ __forceinline__ Place place_of(const GridSpan& g, int across)
 // Blocks that cover tiles x across under place_of.
 int64_t places(int64_t tiles, int across) { return ((tiles + 3) / 4 * 4 * across + 255) / 256 * 256; }
 
-// Calls f with the fragment rows (1 .. 8) that cover nr rows as a constant.
-template <class F>
+// Calls f with the fragment rows (1 .. 8, or Small 1 .. 2) that cover nr rows as a constant.
+template <bool Small, class F>
 __device__ __forceinline__ void with_rows(int nr, F&& f)
 {
-    switch ((nr + 31) >> 5) {
+    if constexpr (Small) {
+        if (nr <= 32) f(std::integral_constant<int, 1>());
+        else f(std::integral_constant<int, 2>());
+    } else switch ((nr + 31) >> 5) {
         case 1: f(std::integral_constant<int, 1>()); break;
         case 2: f(std::integral_constant<int, 2>()); break;
         case 3: f(std::integral_constant<int, 3>()); break;
@@ -79,7 +82,7 @@ __device__ __forceinline__ void with_rows(int nr, F&& f)
 template <int MF>
 __device__ __forceinline__ void row_slots(KContiguous& r, const char* first, int width, int nr)
 {
-    constexpr int kFirst = 32 * ((MF + 1) / 2);
+    constexpr int kFirst = 32 * low_rows(MF);
     r.slot(0, first, min(nr, kFirst));
     r.slot(1, first + (int64_t)kFirst * width * 2, nr - kFirst);
 }
@@ -103,15 +106,20 @@ __device__ __forceinline__ float group_top(f32x4 a, f32x4 b, bool past_a, bool p
     return fmaxf(top, __shfl_xor(top, 32, kWave));
 }
 
+// Rows an expert has on average, up to which tiles of 64 rows with two blocks a CU win (forward and backward pass, 48
+// rows on average, 32 experts of 2048 x 2048: 650 us against 675; at 64, where half of the experts have a second tile,
+// 739 against 704).
+constexpr int kSmallRows = 48;
 constexpr int kUpFeatures = kTileFeatures / 2;  // of h: each of them takes a gate and an up feature
 
-__global__ __launch_bounds__(kGemmThreads, 2) void ffn_up_kernel(ExpertShape S, const char* xe, const char* w,
+template <bool Small>
+__global__ __launch_bounds__(kGemmThreads, Small ? 4 : 2) void ffn_up_kernel(ExpertShape S, const char* xe, const char* w,
                                                                  char* h, SavedActs saved, int across, GridSpan span)
 {
-    __shared__ __align__(1024) char lds[kGemmLds];
+    __shared__ __align__(1024) char lds[Lds<Small>::kBytes];
     const Place at = place_of(span, across);
     int row0, nr;
-    const int bad = *S.status, e = segment_tile(S.offset, S.E, kTileRows, 32, at.tile, &row0, &nr);
+    const int bad = *S.status, e = segment_tile(S.offset, S.E, Lds<Small>::kRows, 32, at.tile, &row0, &nr);
     if (bad || e < 0) return;
     const int c0 = at.across * kUpFeatures, H = S.H, I = S.I;
     const int valid = min(kUpFeatures, I - c0);
@@ -122,14 +130,14 @@ __global__ __launch_bounds__(kGemmThreads, 2) void ffn_up_kernel(ExpertShape S, 
     f.slot(0, w + ((int64_t)e * 2 * I + c0) * H * 2, valid);
     f.slot(1, w + ((int64_t)e * 2 * I + I + c0) * H * 2, valid);
     const int lane = lane_id(), wf = wave_id() & 3, groups = (I + kGroup8 - 1) / kGroup8;
-    with_rows(nr, [&](auto mf) {
+    with_rows<Small>(nr, [&](auto mf) {
         constexpr int MF = decltype(mf)::value;
         Acc<MF> acc;
         row_slots<MF>(r, xe + (int64_t)row0 * H * 2, H, nr);
-        tile_product<MF>(r, f, H, lds, acc);
+        tile_product<Small, MF>(r, f, H, lds, acc);
         typedef Stage<kUpFeatures * 2> Wide;
         typedef Stage<kUpFeatures> Narrow;
-        char* const second = lds + 256 * kUpFeatures * 2;
+        char* const second = lds + Lds<Small>::kRows * kUpFeatures * 2;
 #pragma unroll
         for (int m = 0; m < MF; ++m) {
             const int row = row_of<MF>(m) + (lane & 15);
@@ -151,7 +159,7 @@ __global__ __launch_bounds__(kGemmThreads, 2) void ffn_up_kernel(ExpertShape S, 
             for (int which = 0; which < 2; ++which) {
                 const f32x4 a = acc[m][2 * which], b = acc[m][2 * which + 1];
                 const float step = step8(group_top(a, b, c0 + c >= I, c0 + c + 16 >= I)), inv = 1.0f / step;
-                char* const to = second + which * 256 * kUpFeatures;
+                char* const to = second + which * Lds<Small>::kRows * kUpFeatures;
                 *(unsigned*)Narrow::at(to, row, c) = pack8x4(a[0], a[1], a[2], a[3], inv);
                 *(unsigned*)Narrow::at(to, row, c + 16) = pack8x4(b[0], b[1], b[2], b[3], inv);
                 if (row < nr && lane < 16 && c0 + 32 * wf < I)
@@ -165,7 +173,7 @@ __global__ __launch_bounds__(kGemmThreads, 2) void ffn_up_kernel(ExpertShape S, 
         char* const out = (char*)saved.data + ((int64_t)row0 * 2 * I + c0) * (saved.scale ? 1 : 2);
         if (saved.scale) {
             Narrow::store<u32x2, MF>(second, nr, valid, out, (int64_t)2 * I);
-            Narrow::store<u32x2, MF>(second + 256 * kUpFeatures, nr, valid, out + I, (int64_t)2 * I);
+            Narrow::store<u32x2, MF>(second + Lds<Small>::kRows * kUpFeatures, nr, valid, out + I, (int64_t)2 * I);
             return;
         }
         Wide::store<u32x4, MF>(second, nr, 2 * valid, out, (int64_t)4 * I);
@@ -201,15 +209,15 @@ __device__ __forceinline__ void write_tile(char* lds, int nr, int valid, char* o
 
 // out[row] = in[row] F^T for the rows of every expert; in [P, K], out [P, N], F of an expert [N][K] (or, Strided,
 // [K][N]) at w.
-template <bool Strided>
-__global__ __launch_bounds__(kGemmThreads, 2) void ffn_rows_kernel(ExpertShape S, const char* in, int K,
+template <bool Strided, bool Small>
+__global__ __launch_bounds__(kGemmThreads, Small ? 4 : 2) void ffn_rows_kernel(ExpertShape S, const char* in, int K,
                                                                    const char* w, int N, char* out, int across,
                                                                    GridSpan span)
 {
-    __shared__ __align__(1024) char lds[kGemmLds];
+    __shared__ __align__(1024) char lds[Lds<Small>::kBytes];
     const Place at = place_of(span, across);
     int row0, nr;
-    const int bad = *S.status, e = segment_tile(S.offset, S.E, kTileRows, 32, at.tile, &row0, &nr);
+    const int bad = *S.status, e = segment_tile(S.offset, S.E, Lds<Small>::kRows, 32, at.tile, &row0, &nr);
     if (bad || e < 0) return;
     const int n0 = at.across * kTileFeatures;
     KContiguous r;
@@ -220,22 +228,22 @@ __global__ __launch_bounds__(kGemmThreads, 2) void ffn_rows_kernel(ExpertShape S
         const int n = n0 + 128 * i;
         f.slot(i, w + (Strided ? (int64_t)e * K * N + n : ((int64_t)e * N + n) * K) * 2, N - n);
     }
-    with_rows(nr, [&](auto mf) {
+    with_rows<Small>(nr, [&](auto mf) {
         constexpr int MF = decltype(mf)::value;
         Acc<MF> acc;
         row_slots<MF>(r, in + (int64_t)row0 * K * 2, K, nr);
-        tile_product<MF>(r, f, K, lds, acc);
+        tile_product<Small, MF>(r, f, K, lds, acc);
         write_tile<MF>(lds, nr, min(N - n0, kTileFeatures), out + ((int64_t)row0 * N + n0) * 2, (int64_t)N * 2,
                        [&](int m, int n) { return pack4(acc[m][n]); });
     });
 }
 
 // Fragment rows [M0, M0 + MC) of dh, a slot's, with the saved pre-activations to dg, du and h.
-template <int M0, int MC, int MF>
+template <bool Small, int M0, int MC, int MF>
 __device__ __forceinline__ void dh_rows(const ExpertShape& S, char* lds, const Acc<MF>& acc, const SavedActs& saved,
                                         int row0, int nr, int n0, int valid, char* h, char* dgu)
 {
-    constexpr int kHalf = 128 * kTileFeatures * 2, kFirst = M0 ? 32 * ((MF + 1) / 2) : 0;
+    constexpr int kHalf = (Small ? 64 : 128) * kTileFeatures * 2, kFirst = M0 ? 32 * low_rows(MF) : 0;
     const int lane = lane_id(), I = S.I, groups = (I + kGroup8 - 1) / kGroup8;
     struct Held {
         u32x2 g, u;
@@ -310,14 +318,15 @@ __device__ __forceinline__ void dh_rows(const ExpertShape& S, char* lds, const A
     __syncthreads();
 }
 
-__global__ __launch_bounds__(kGemmThreads, 2) void ffn_dh_kernel(ExpertShape S, const char* gy, const char* w,
+template <bool Small>
+__global__ __launch_bounds__(kGemmThreads, Small ? 4 : 2) void ffn_dh_kernel(ExpertShape S, const char* gy, const char* w,
                                                                  SavedActs saved, char* h, char* dgu, int across,
                                                                  GridSpan span)
 {
-    __shared__ __align__(1024) char lds[kGemmLds];
+    __shared__ __align__(1024) char lds[Lds<Small>::kBytes];
     const Place at = place_of(span, across);
     int row0, nr;
-    const int bad = *S.status, e = segment_tile(S.offset, S.E, kTileRows, 32, at.tile, &row0, &nr);
+    const int bad = *S.status, e = segment_tile(S.offset, S.E, Lds<Small>::kRows, 32, at.tile, &row0, &nr);
     if (bad || e < 0) return;
     const int n0 = at.across * kTileFeatures, H = S.H, I = S.I;
     KContiguous r;
@@ -326,15 +335,15 @@ __global__ __launch_bounds__(kGemmThreads, 2) void ffn_dh_kernel(ExpertShape S, 
     f.init(I, H);
     for (int i = 0; i < 2; ++i) f.slot(i, w + ((int64_t)e * H * I + n0 + 128 * i) * 2, I - n0 - 128 * i);
     const int valid = min(I - n0, kTileFeatures);
-    with_rows(nr, [&](auto mf) {
+    with_rows<Small>(nr, [&](auto mf) {
         constexpr int MF = decltype(mf)::value;
         Acc<MF> acc;
         row_slots<MF>(r, gy + (int64_t)row0 * H * 2, H, nr);
-        tile_product<MF>(r, f, H, lds, acc);
+        tile_product<Small, MF>(r, f, H, lds, acc);
         // a slot's rows at a time: dg and du go through LDS side by side, then h
-        constexpr int A = (MF + 1) / 2;
-        dh_rows<0, A>(S, lds, acc, saved, row0, nr, n0, valid, h, dgu);
-        if constexpr (MF > A) dh_rows<A, MF - A>(S, lds, acc, saved, row0, nr, n0, valid, h, dgu);
+        constexpr int A = low_rows(MF);
+        dh_rows<Small, 0, A>(S, lds, acc, saved, row0, nr, n0, valid, h, dgu);
+        if constexpr (MF > A) dh_rows<Small, A, MF - A>(S, lds, acc, saved, row0, nr, n0, valid, h, dgu);
     });
 }
 
@@ -343,7 +352,7 @@ __global__ __launch_bounds__(kGemmThreads, 2) void ffn_wgrad_kernel(ExpertShape 
                                                                     const char* b, int nb, char* out, int down,
                                                                     int across, GridSpan span)
 {
-    __shared__ __align__(1024) char lds[kGemmLds];
+    __shared__ __align__(1024) char lds[Lds<false>::kBytes];
     if (*S.status) return;
     const Place at = place_of(span, across);
     const int e = at.tile / down, m0 = (at.tile - e * down) * kTileRows, n0 = at.across * kTileFeatures;
@@ -357,13 +366,28 @@ __global__ __launch_bounds__(kGemmThreads, 2) void ffn_wgrad_kernel(ExpertShape 
         f.slot(i, b + ((int64_t)q0 * nb + n0 + 128 * i) * 2, nb - n0 - 128 * i);
     }
     Acc<8> acc;
-    tile_product<8>(r, f, rows, lds, acc);
+    tile_product<false, 8>(r, f, rows, lds, acc);
     write_tile<8>(lds, min(na - m0, kTileRows), min(nb - n0, kTileFeatures),
                   out + (((int64_t)e * na + m0) * nb + n0) * 2, (int64_t)nb * 2,
                   [&](int m, int n) { return pack4(acc[m][n]); });
 }
 
-int64_t row_tiles(const ExpertShape& S) { return (int64_t)S.P / kTileRows + (S.P < S.E ? S.P : S.E); }
+template <bool Small>
+int64_t row_tiles(const ExpertShape& S)
+{
+    return (int64_t)S.P / Lds<Small>::kRows + (S.P < S.E ? S.P : S.E);
+}
+
+// Whether experts have so few rows on average that tiles of 64 are the faster ones.
+bool is_small(const ExpertShape& S) { return S.P <= (int64_t)kSmallRows * (S.P < S.E ? S.P : S.E); }
+
+// Calls f with whether tiles are small as a constant.
+template <class F>
+hipError_t by_size(const ExpertShape& S, F&& f)
+{
+    return is_small(S) ? f(std::true_type()) : f(std::false_type());
+}
+
 int tiles_of(int n, int tile) { return (n + tile - 1) / tile; }
 
 }  // namespace
@@ -372,18 +396,24 @@ hipError_t launch_ffn_up(const ExpertShape& S, const void* xe, const void* w_gat
                          hipStream_t s)
 {
     const int across = tiles_of(S.I, kUpFeatures);
-    return launch_spans(places(row_tiles(S), across), kGemmThreads, [&](dim3 grid, GridSpan span) {
-        ffn_up_kernel<<<grid, kGemmThreads, 0, s>>>(S, (const char*)xe, (const char*)w_gate_up, (char*)h, saved, across,
-                                                    span);
+    return by_size(S, [&](auto small) {
+        constexpr bool kSmall = decltype(small)::value;
+        return launch_spans(places(row_tiles<kSmall>(S), across), kGemmThreads, [&](dim3 grid, GridSpan span) {
+            ffn_up_kernel<kSmall><<<grid, kGemmThreads, 0, s>>>(S, (const char*)xe, (const char*)w_gate_up, (char*)h, saved,
+                                                                across, span);
+        });
     });
 }
 
 hipError_t launch_ffn_down(const ExpertShape& S, const void* h, const void* w_down, void* ye, hipStream_t s)
 {
     const int across = tiles_of(S.H, kTileFeatures);
-    return launch_spans(places(row_tiles(S), across), kGemmThreads, [&](dim3 grid, GridSpan span) {
-        ffn_rows_kernel<false><<<grid, kGemmThreads, 0, s>>>(S, (const char*)h, S.I, (const char*)w_down, S.H, (char*)ye,
+    return by_size(S, [&](auto small) {
+        constexpr bool kSmall = decltype(small)::value;
+        return launch_spans(places(row_tiles<kSmall>(S), across), kGemmThreads, [&](dim3 grid, GridSpan span) {
+            ffn_rows_kernel<false, kSmall><<<grid, kGemmThreads, 0, s>>>(S, (const char*)h, S.I, (const char*)w_down, S.H, (char*)ye,
                                                              across, span);
+        });
     });
 }
 
@@ -391,18 +421,24 @@ hipError_t launch_ffn_dh(const ExpertShape& S, const void* grad_ye, const void* 
                          void* dgu, hipStream_t s)
 {
     const int across = tiles_of(S.I, kTileFeatures);
-    return launch_spans(places(row_tiles(S), across), kGemmThreads, [&](dim3 grid, GridSpan span) {
-        ffn_dh_kernel<<<grid, kGemmThreads, 0, s>>>(S, (const char*)grad_ye, (const char*)w_down, saved, (char*)h,
+    return by_size(S, [&](auto small) {
+        constexpr bool kSmall = decltype(small)::value;
+        return launch_spans(places(row_tiles<kSmall>(S), across), kGemmThreads, [&](dim3 grid, GridSpan span) {
+            ffn_dh_kernel<kSmall><<<grid, kGemmThreads, 0, s>>>(S, (const char*)grad_ye, (const char*)w_down, saved, (char*)h,
                                                     (char*)dgu, across, span);
+        });
     });
 }
 
 hipError_t launch_ffn_dx(const ExpertShape& S, const void* dgu, const void* w_gate_up, void* grad_xe, hipStream_t s)
 {
     const int across = tiles_of(S.H, kTileFeatures);
-    return launch_spans(places(row_tiles(S), across), kGemmThreads, [&](dim3 grid, GridSpan span) {
-        ffn_rows_kernel<true><<<grid, kGemmThreads, 0, s>>>(S, (const char*)dgu, 2 * S.I, (const char*)w_gate_up, S.H,
+    return by_size(S, [&](auto small) {
+        constexpr bool kSmall = decltype(small)::value;
+        return launch_spans(places(row_tiles<kSmall>(S), across), kGemmThreads, [&](dim3 grid, GridSpan span) {
+            ffn_rows_kernel<true, kSmall><<<grid, kGemmThreads, 0, s>>>(S, (const char*)dgu, 2 * S.I, (const char*)w_gate_up, S.H,
                                                             (char*)grad_xe, across, span);
+        });
     });
 }
 

@@ -38,7 +38,19 @@ constexpr int kTileK = 64;
 constexpr int kTileFeatures = 256;
 constexpr int kTileRows = 256;
 constexpr int kSlot = 128 * kTileK * 2;  // 16 KiB
-constexpr int kGemmLds = 8 * kSlot;
+
+// The LDS of a product.  Where the experts have few rows, a tile of 64 (Small) needs one slot of 8 KiB for them, so
+// that two blocks fit a CU: with nothing but weights to wait for, that is what counts.
+template <bool Small>
+struct Lds {
+    static constexpr int kRows = Small ? 64 : kTileRows;
+    static constexpr int kFeatures = Small ? kSlot / 2 : 2 * kSlot;  // where F0 lies in a tile
+    static constexpr int kTile = kFeatures + 2 * kSlot;
+    static constexpr int kBytes = 2 * kTile;
+};
+
+// Row fragments of a wave in R0, of MF in all; R1 has the others.
+constexpr int low_rows(int MF) { return MF <= 2 ? MF : (MF + 1) / 2; }
 
 typedef __attribute__((address_space(3))) void lds_void;
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
@@ -176,21 +188,23 @@ template <int MF>
 using Acc = f32x4[MF][4];
 
 // Where acc[m][n] of this wave lies in the tile: rows row_of<MF>(m) + (lane & 15), features feature_of(n) +
-// 4 (lane >> 4) .. + 4.  Slot R0 holds the first 32 ceil(MF / 2) rows, R1 the rest.
+// 4 (lane >> 4) .. + 4.  Slot R0 holds the first 32 low_rows(MF) rows, R1 the rest.
 template <int MF>
 __device__ __forceinline__ int row_of(int m)
 {
-    constexpr int A = (MF + 1) / 2, B = MF / 2;
+    constexpr int A = low_rows(MF), B = MF - A;
     const int wr = wave_id() >> 2;
     return m < A ? 16 * (A * wr + m) : 32 * A + 16 * (B * wr + m - A);
 }
 __device__ __forceinline__ int feature_of(int n) { return (n >> 1) * 128 + 32 * (wave_id() & 3) + 16 * (n & 1); }
 
-// The tile's product.  `lds`: kGemmLds bytes.  Ends with a barrier: LDS is free.
-template <int MF, class R, class F>
+// The tile's product.  `lds`: Lds<Small>::kBytes.  Ends with a barrier: LDS is free.
+template <bool Small, int MF, class R, class F>
 __device__ __forceinline__ void tile_product(const R& r, const F& f, int K, char* lds, Acc<MF>& acc)
 {
-    constexpr int A = (MF + 1) / 2, B = MF / 2;  // row fragments of a wave in R0 and R1
+    constexpr int A = low_rows(MF), B = MF - A;  // row fragments of a wave in R0 and R1
+    constexpr int kTile = Lds<Small>::kTile, kFeatures = Lds<Small>::kFeatures;
+    static_assert(!Small || B == 0, "no slot for R1");
     constexpr int a = R::kTransposed ? 2 : (A + 1) / 2, b = R::kTransposed ? 2 : (B + 1) / 2;  // loads of R0 and R1
     const int wr = wave_id() >> 2, wf = wave_id() & 3, nk = (K + kTileK - 1) / kTileK;
 #pragma unroll
@@ -201,20 +215,20 @@ __device__ __forceinline__ void tile_product(const R& r, const F& f, int K, char
     const unsigned base = __builtin_amdgcn_readfirstlane(lds_offset(lds));
     // slots of a tile: R0, R1, F0, F1
     const auto load_r = [&](int s, int kt) {
-        const unsigned at = base + (kt & 1) * 4 * kSlot + s * kSlot;
+        const unsigned at = base + (kt & 1) * kTile + s * kSlot;
         if (s == 0) r.template load<a>(0, kt, at);
         else r.template load<b>(1, kt, at);
     };
-    const auto load_f = [&](int s, int kt) { f.template load<2>(s, kt, base + (kt & 1) * 4 * kSlot + (2 + s) * kSlot); };
+    const auto load_f = [&](int s, int kt) { f.template load<2>(s, kt, base + (kt & 1) * kTile + kFeatures + s * kSlot); };
     bf16x8 r0[A][2], r1[B ? B : 1][2], fx[2][2], fy[2][2];
     const auto read_r0 = [&](int kt, int i) {
-        r0[i >> 1][i & 1] = R::fragment(lds + (kt & 1) * 4 * kSlot, 16 * (A * wr + (i >> 1)), i & 1);
+        r0[i >> 1][i & 1] = R::fragment(lds + (kt & 1) * kTile, 16 * (A * wr + (i >> 1)), i & 1);
     };
     const auto read_r1 = [&](int kt, int i) {
-        r1[i >> 1][i & 1] = R::fragment(lds + (kt & 1) * 4 * kSlot + kSlot, 16 * (B * wr + (i >> 1)), i & 1);
+        r1[i >> 1][i & 1] = R::fragment(lds + (kt & 1) * kTile + kSlot, 16 * (B * wr + (i >> 1)), i & 1);
     };
     const auto read_f = [&](bf16x8 (&to)[2][2], int s, int kt, int i) {
-        to[i >> 1][i & 1] = F::fragment(lds + (kt & 1) * 4 * kSlot + (2 + s) * kSlot, 32 * wf + 16 * (i >> 1), i & 1);
+        to[i >> 1][i & 1] = F::fragment(lds + (kt & 1) * kTile + kFeatures + s * kSlot, 32 * wf + 16 * (i >> 1), i & 1);
     };
     // One phase: products of `count` row fragments with two feature fragments; the `reads` LDS reads of the next
     // phase go out in the first half of the products, the loads in their middle.

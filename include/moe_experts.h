@@ -32,9 +32,12 @@
  * moe_shuffle.h do.  With T = 0 forward calls write nothing and return
  * MOE_SHUFFLE_OK; the backward call writes zero weight gradients.
  *
+ * No output may overlap an input, another output, the workspace or the plan's
+ * workspace (MOE_SHUFFLE_E_INVALID_ARG).
+ *
  * Limits: I > 0, I % 8 == 0, H and I below 2^20, and all row and weight
- * pointers 16-byte aligned.  P * ceil(I / 32) and E * ceil(2I / 64) *
- * ceil(H / 64) and P * ceil(2 max(H, I) / 64) below 2^31
+ * pointers 16-byte aligned.  With Q = P + 1024, Q * ceil(I / 32) and
+ * E * ceil(2I / 64) * ceil(H / 64) and Q * ceil(2 max(H, I) / 64) below 2^31
  * (MOE_SHUFFLE_E_OVERFLOW).
  */
 #ifndef MOE_EXPERTS_H
@@ -67,7 +70,7 @@ int moe_experts_ffn_workspace_size(const moe_shuffle_dims* dims, int32_t inter, 
  *   xe         device bf16 [P, H], expert-major as dispatch leaves it
  *   w_gate_up  device bf16 [E, 2I, H];  w_down  device bf16 [E, H, I]
  *   act        MOE_EXPERTS_ACT_*
- *   ye         device bf16 [P, H]; may not overlap any input
+ *   ye         device bf16 [P, H]
  *   saved, saved_scale  what the backward pass needs of the pre-activations:
  *     both NULL               nothing is kept (inference)
  *     saved alone             bf16 [P, 2I]: g, then u, each rounded to bf16
@@ -112,7 +115,8 @@ int moe_experts_ffn_backward(moe_shuffle_plan_t plan, const void* grad_ye, const
  *   q_down     device uint8 [E, H, I / 2];    s_down    bf16 [E, H, I / group]
  *   group      32, 64 or 128; H and I multiples of it (MOE_SHUFFLE_E_ALIGN)
  * (q - 8) is exact in the products and a group's sum is scaled in fp32, so
- * no weight is rounded.  Any number of rows is computed.  Other arguments as
+ * no weight is rounded.  An infinite x gives NaN.  Any number of rows is
+ * computed; with hundreds for an expert, bf16 weights are the faster form.  Other arguments as
  * for moe_experts_ffn_forward; all pointers 16-byte aligned.
  */
 int moe_experts_ffn_w4_forward(moe_shuffle_plan_t plan, const void* xe, const void* q_gate_up, const void* s_gate_up,

@@ -9,6 +9,7 @@
 
 namespace {
 
+constexpr int kTileRoom = 1024;
 constexpr int kMaxWidth = 1 << 20;  // H and I below this: offsets inside a tile stay below 2^31
 
 bool misaligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) != 0; }
@@ -41,7 +42,8 @@ int check_inter(const moe_shuffle_dims& d, int32_t inter)
     if (inter <= 0) return MOE_SHUFFLE_E_INVALID_ARG;
     if (inter % 8 != 0) return MOE_SHUFFLE_E_ALIGN;
     if (inter >= kMaxWidth || d.hidden >= kMaxWidth) return MOE_SHUFFLE_E_OVERFLOW;
-    const int64_t P = (int64_t)d.num_tokens * d.top_k, lim = (int64_t)1 << 31;
+    // the kernels round row counts up to tiles, and count tiles and pieces of rows with int
+    const int64_t P = (int64_t)d.num_tokens * d.top_k + kTileRoom, lim = (int64_t)1 << 31;
     const int64_t wide = d.hidden > inter ? d.hidden : inter;
     const int64_t up = (2 * (int64_t)inter + 63) / 64, hid = ((int64_t)d.hidden + 63) / 64;
     if (P * ((inter + 31) / 32) >= lim || P * ((2 * wide + 63) / 64) >= lim || d.num_experts * up * hid >= lim)
@@ -89,6 +91,9 @@ int check_workspace(const ms::ExpertShape& S, bool backward, const void* workspa
 size_t saved_bytes(const ms::ExpertShape& S, bool eight) { return (size_t)S.P * 2 * S.I * (eight ? 1 : 2); }
 size_t scale_bytes(const ms::ExpertShape& S) { return (size_t)S.P * 2 * ((S.I + ms::kGroup8 - 1) / ms::kGroup8) * 2; }
 
+// The plan's own workspace, which nothing may write.
+Span plan_span(moe_shuffle_plan_t plan) { return Span{plan->ws, plan->L.total}; }
+
 int status_of(hipError_t e) { return e == hipSuccess ? MOE_SHUFFLE_OK : ms::hip_fail(e); }
 
 }  // namespace
@@ -126,7 +131,7 @@ int moe_experts_ffn_forward(moe_shuffle_plan_t plan, const void* xe, const void*
     const size_t rows = (size_t)S.P * S.H * 2, proj = (size_t)S.E * S.I * S.H * 2;
     if (overlaps({{ye, rows}, {saved, saved_bytes(S, saved_scale)}, {saved_scale, scale_bytes(S)},
                   {workspace, workspace_bytes_of(S, false)}},
-                 {{xe, rows}, {w_gate_up, 2 * proj}, {w_down, proj}}))
+                 {{xe, rows}, {w_gate_up, 2 * proj}, {w_down, proj}, plan_span(plan)}))
         return MOE_SHUFFLE_E_INVALID_ARG;
     hipStream_t s = (hipStream_t)stream;
     const bool few = ms::ffn_is_few(S);
@@ -159,7 +164,7 @@ int moe_experts_ffn_backward(moe_shuffle_plan_t plan, const void* grad_ye, const
     if (overlaps({{grad_xe, rows}, {grad_w_gate_up, 2 * proj}, {grad_w_down, proj},
                   {workspace, workspace_bytes_of(S, true)}},
                  {{grad_ye, rows}, {xe, rows}, {w_gate_up, 2 * proj}, {w_down, proj},
-                  {saved, saved_bytes(S, saved_scale)}, {saved_scale, scale_bytes(S)}}))
+                  {saved, saved_bytes(S, saved_scale)}, {saved_scale, scale_bytes(S)}, plan_span(plan)}))
         return MOE_SHUFFLE_E_INVALID_ARG;
     if (!grad_xe && !grad_w_gate_up && !grad_w_down) return MOE_SHUFFLE_OK;
     hipStream_t s = (hipStream_t)stream;
@@ -194,7 +199,7 @@ int moe_experts_ffn_w4_forward(moe_shuffle_plan_t plan, const void* xe, const vo
     const size_t rows = (size_t)S.P * S.H * 2, proj = (size_t)S.E * S.I * S.H / 2;
     if (overlaps({{ye, rows}, {workspace, workspace_bytes_of(S, false)}},
                  {{xe, rows}, {q_gate_up, 2 * proj}, {q_down, proj}, {s_gate_up, 8 * proj / group},
-                  {s_down, 4 * proj / group}}))
+                  {s_down, 4 * proj / group}, plan_span(plan)}))
         return MOE_SHUFFLE_E_INVALID_ARG;
     hipError_t e = ms::launch_w4_up(S, xe, q_gate_up, s_gate_up, group, workspace, (hipStream_t)stream);
     if (e == hipSuccess) e = ms::launch_w4_down(S, workspace, q_down, s_down, group, ye, (hipStream_t)stream);

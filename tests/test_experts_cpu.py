@@ -60,6 +60,7 @@ def test_workspace_size():
     ((4, 64, 8, 9, 4), 8, "E_INVALID_ARG"), ((4, 64, 8, 2, 4), 1 << 20, "E_OVERFLOW"),
     ((4, 1 << 20, 8, 2, 4), 8, "E_OVERFLOW"),
     ((1 << 24, 64, 8, 8, 4), 1 << 14, "E_OVERFLOW"),          # P * I / 32 at 2^36
+    (((1 << 27) - 10, 8, 16, 16, 4), 8, "E_OVERFLOW"),        # P = 2^31 - 160, within 1024 of 2^31
     ((4, 1 << 19, 512, 2, 4), 1 << 19, "E_OVERFLOW"),         # tiles of the weight gradients
 ])
 def test_workspace_size_refusals(dims, inter, code):

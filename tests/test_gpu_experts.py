@@ -604,6 +604,8 @@ def test_refusals_with_a_plan():
     assert fwd(sc=scale.data_ptr()) == ms.E_INVALID_ARG                  # a scale without saved
     assert fwd(y=c.xe.data_ptr()) == fwd(y=c.w2.data_ptr()) == ms.E_INVALID_ARG
     assert fwd(sv=c.xe.data_ptr()) == fwd(ws=c.w1.data_ptr()) == ms.E_INVALID_ARG
+    # the plan's workspace is no scratch
+    assert c.plan_ws.numel() > 256 and fwd(ws=c.plan_ws.data_ptr()) == fwd(y=c.plan_ws.data_ptr()) == ms.E_INVALID_ARG
 
     gx, g1, g2 = torch.empty_like(c.xe), torch.empty_like(c.w1), torch.empty_like(c.w2)
 

@@ -106,10 +106,10 @@ __device__ __forceinline__ float group_top(f32x4 a, f32x4 b, bool past_a, bool p
     return fmaxf(top, __shfl_xor(top, 32, kWave));
 }
 
-// Rows an expert has on average, up to which tiles of 64 rows with two blocks a CU win (forward and backward pass, 48
-// rows on average, 32 experts of 2048 x 2048: 650 us against 675; at 64, where half of the experts have a second tile,
-// 739 against 704).
-constexpr int kSmallRows = 48;
+// Rows an expert has on average, up to which tiles of 64 rows with two blocks a CU win: forward and backward pass, 32
+// experts of 2048 x 2048, 48 rows each on average, 650 us against 675; 48 experts of 1160 x 520 with uneven rows, 49 on
+// average, 208 against 256.  At 64 half of the experts have a second such tile (739 against 704).
+constexpr int kSmallRows = 56;
 constexpr int kUpFeatures = kTileFeatures / 2;  // of h: each of them takes a gate and an up feature
 
 template <bool Small>

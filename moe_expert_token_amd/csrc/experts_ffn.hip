@@ -1,4 +1,6 @@
 // experts_ffn.hip -- the matrix products of the experts' gated block.
+#include <math.h>
+
 #include <type_traits>
 
 #include "experts_gemm.h"
@@ -110,16 +112,18 @@ __device__ __forceinline__ float group_top(f32x4 a, f32x4 b, bool past_a, bool p
 // experts of 2048 x 2048, 48 rows each on average, 650 us against 675; 48 experts of 1160 x 520 with uneven rows, 49 on
 // average, 208 against 256.  At 64 half of the experts have a second such tile (739 against 704).
 constexpr int kSmallRows = 56;
+constexpr int kCUs = 256;
 constexpr int kUpFeatures = kTileFeatures / 2;  // of h: each of them takes a gate and an up feature
 
 template <bool Small>
 __global__ __launch_bounds__(kGemmThreads, Small ? 4 : 2) void ffn_up_kernel(ExpertShape S, const char* xe, const char* w,
-                                                                 char* h, SavedActs saved, int across, GridSpan span)
+                                                                 char* h, SavedActs saved, int tile_rows, int across,
+                                                                           GridSpan span)
 {
     __shared__ __align__(1024) char lds[Lds<Small>::kBytes];
     const Place at = place_of(span, across);
     int row0, nr;
-    const int bad = *S.status, e = segment_tile(S.offset, S.E, Lds<Small>::kRows, 32, at.tile, &row0, &nr);
+    const int bad = *S.status, e = segment_tile(S.offset, S.E, tile_rows, 32, at.tile, &row0, &nr);
     if (bad || e < 0) return;
     const int c0 = at.across * kUpFeatures, H = S.H, I = S.I;
     const int valid = min(kUpFeatures, I - c0);
@@ -211,13 +215,13 @@ __device__ __forceinline__ void write_tile(char* lds, int nr, int valid, char* o
 // [K][N]) at w.
 template <bool Strided, bool Small>
 __global__ __launch_bounds__(kGemmThreads, Small ? 4 : 2) void ffn_rows_kernel(ExpertShape S, const char* in, int K,
-                                                                   const char* w, int N, char* out, int across,
-                                                                   GridSpan span)
+                                                                   const char* w, int N, char* out,
+                                                                              int tile_rows, int across, GridSpan span)
 {
     __shared__ __align__(1024) char lds[Lds<Small>::kBytes];
     const Place at = place_of(span, across);
     int row0, nr;
-    const int bad = *S.status, e = segment_tile(S.offset, S.E, Lds<Small>::kRows, 32, at.tile, &row0, &nr);
+    const int bad = *S.status, e = segment_tile(S.offset, S.E, tile_rows, 32, at.tile, &row0, &nr);
     if (bad || e < 0) return;
     const int n0 = at.across * kTileFeatures;
     KContiguous r;
@@ -320,13 +324,13 @@ __device__ __forceinline__ void dh_rows(const ExpertShape& S, char* lds, const A
 
 template <bool Small>
 __global__ __launch_bounds__(kGemmThreads, Small ? 4 : 2) void ffn_dh_kernel(ExpertShape S, const char* gy, const char* w,
-                                                                 SavedActs saved, char* h, char* dgu, int across,
-                                                                 GridSpan span)
+                                                                 SavedActs saved, char* h, char* dgu, int tile_rows,
+                                                                            int across, GridSpan span)
 {
     __shared__ __align__(1024) char lds[Lds<Small>::kBytes];
     const Place at = place_of(span, across);
     int row0, nr;
-    const int bad = *S.status, e = segment_tile(S.offset, S.E, Lds<Small>::kRows, 32, at.tile, &row0, &nr);
+    const int bad = *S.status, e = segment_tile(S.offset, S.E, tile_rows, 32, at.tile, &row0, &nr);
     if (bad || e < 0) return;
     const int n0 = at.across * kTileFeatures, H = S.H, I = S.I;
     KContiguous r;
@@ -372,23 +376,50 @@ __global__ __launch_bounds__(kGemmThreads, 2) void ffn_wgrad_kernel(ExpertShape 
                   [&](int m, int n) { return pack4(acc[m][n]); });
 }
 
-template <bool Small>
-int64_t row_tiles(const ExpertShape& S)
-{
-    return (int64_t)S.P / Lds<Small>::kRows + (S.P < S.E ? S.P : S.E);
-}
-
-// Whether experts have so few rows on average that tiles of 64 are the faster ones.
-bool is_small(const ExpertShape& S) { return S.P <= (int64_t)kSmallRows * (S.P < S.E ? S.P : S.E); }
-
-// Calls f with whether tiles are small as a constant.
-template <class F>
-hipError_t by_size(const ExpertShape& S, F&& f)
-{
-    return is_small(S) ? f(std::true_type()) : f(std::false_type());
-}
-
 int tiles_of(int n, int tile) { return (n + tile - 1) / tile; }
+
+// The rows of a tile, 128 to 256, for an estimate of the time of `across` feature tiles: a tile takes 1.5 + its
+// fragment rows (32 rows each), and the CUs take the tiles in rounds of 256, so that a few tiles more than whole rounds
+// cost a round.  The rows of an expert are not known here; five counts around the mean stand for them, spread as
+// even routing spreads them.  (8 experts of 1024 rows, 28672 to 4096: 1663 us with 192 rows against 1894 with 256;
+// 16 experts of 375 rows, 2048 to 1000: 67 us with 160 against 85.  The estimates are 0.83 and 0.73 of the other.)
+int pick_tile_rows(const ExpertShape& S, int across)
+{
+    const int used = S.P < S.E ? S.P : S.E;
+    const double mean = (double)S.P / (used > 0 ? used : 1), spread = 0.6 * sqrt(mean);
+    int best = kTileRows;
+    double least = 0;
+    for (int rows = kTileRows; rows >= 128; rows -= 32) {
+        double tiles = 0, cost = 0;
+        for (int j = -2; j <= 2; ++j) {
+            const int64_t count = (int64_t)(mean + j * spread + 0.5), n = (count + rows - 1) / rows;
+            tiles += (double)n;
+            cost += n ? n * (1.5 + (double)((count + 32 * n - 1) / (32 * n))) : 0;
+        }
+        if (tiles == 0) continue;
+        const double time = ceil(tiles / 5 * used * across / kCUs) * (cost / tiles);
+        if (best == kTileRows && rows == kTileRows) least = time;
+        if (time < 0.98 * least) {
+            least = time;
+            best = rows;
+        }
+    }
+    return best;
+}
+
+// Calls launch(small, tile rows, blocks' grid, span) for a product of row tiles by `across` feature tiles.
+template <class F>
+hipError_t by_rows(const ExpertShape& S, int across, F&& launch)
+{
+    const auto with = [&](auto small) {
+        constexpr bool kSmall = decltype(small)::value;
+        const int rows = kSmall ? Lds<true>::kRows : pick_tile_rows(S, across);
+        const int64_t tiles = (int64_t)S.P / rows + (S.P < S.E ? S.P : S.E);
+        return launch_spans(places(tiles, across), kGemmThreads,
+                            [&](dim3 grid, GridSpan span) { launch(small, rows, grid, span); });
+    };
+    return S.P <= (int64_t)kSmallRows * (S.P < S.E ? S.P : S.E) ? with(std::true_type()) : with(std::false_type());
+}
 
 }  // namespace
 
@@ -396,24 +427,18 @@ hipError_t launch_ffn_up(const ExpertShape& S, const void* xe, const void* w_gat
                          hipStream_t s)
 {
     const int across = tiles_of(S.I, kUpFeatures);
-    return by_size(S, [&](auto small) {
-        constexpr bool kSmall = decltype(small)::value;
-        return launch_spans(places(row_tiles<kSmall>(S), across), kGemmThreads, [&](dim3 grid, GridSpan span) {
-            ffn_up_kernel<kSmall><<<grid, kGemmThreads, 0, s>>>(S, (const char*)xe, (const char*)w_gate_up, (char*)h, saved,
-                                                                across, span);
-        });
+    return by_rows(S, across, [&](auto small, int rows, dim3 grid, GridSpan span) {
+        ffn_up_kernel<decltype(small)::value><<<grid, kGemmThreads, 0, s>>>(
+            S, (const char*)xe, (const char*)w_gate_up, (char*)h, saved, rows, across, span);
     });
 }
 
 hipError_t launch_ffn_down(const ExpertShape& S, const void* h, const void* w_down, void* ye, hipStream_t s)
 {
     const int across = tiles_of(S.H, kTileFeatures);
-    return by_size(S, [&](auto small) {
-        constexpr bool kSmall = decltype(small)::value;
-        return launch_spans(places(row_tiles<kSmall>(S), across), kGemmThreads, [&](dim3 grid, GridSpan span) {
-            ffn_rows_kernel<false, kSmall><<<grid, kGemmThreads, 0, s>>>(S, (const char*)h, S.I, (const char*)w_down, S.H, (char*)ye,
-                                                             across, span);
-        });
+    return by_rows(S, across, [&](auto small, int rows, dim3 grid, GridSpan span) {
+        ffn_rows_kernel<false, decltype(small)::value><<<grid, kGemmThreads, 0, s>>>(
+            S, (const char*)h, S.I, (const char*)w_down, S.H, (char*)ye, rows, across, span);
     });
 }
 
@@ -421,24 +446,18 @@ hipError_t launch_ffn_dh(const ExpertShape& S, const void* grad_ye, const void* 
                          void* dgu, hipStream_t s)
 {
     const int across = tiles_of(S.I, kTileFeatures);
-    return by_size(S, [&](auto small) {
-        constexpr bool kSmall = decltype(small)::value;
-        return launch_spans(places(row_tiles<kSmall>(S), across), kGemmThreads, [&](dim3 grid, GridSpan span) {
-            ffn_dh_kernel<kSmall><<<grid, kGemmThreads, 0, s>>>(S, (const char*)grad_ye, (const char*)w_down, saved, (char*)h,
-                                                    (char*)dgu, across, span);
-        });
+    return by_rows(S, across, [&](auto small, int rows, dim3 grid, GridSpan span) {
+        ffn_dh_kernel<decltype(small)::value><<<grid, kGemmThreads, 0, s>>>(
+            S, (const char*)grad_ye, (const char*)w_down, saved, (char*)h, (char*)dgu, rows, across, span);
     });
 }
 
 hipError_t launch_ffn_dx(const ExpertShape& S, const void* dgu, const void* w_gate_up, void* grad_xe, hipStream_t s)
 {
     const int across = tiles_of(S.H, kTileFeatures);
-    return by_size(S, [&](auto small) {
-        constexpr bool kSmall = decltype(small)::value;
-        return launch_spans(places(row_tiles<kSmall>(S), across), kGemmThreads, [&](dim3 grid, GridSpan span) {
-            ffn_rows_kernel<true, kSmall><<<grid, kGemmThreads, 0, s>>>(S, (const char*)dgu, 2 * S.I, (const char*)w_gate_up, S.H,
-                                                            (char*)grad_xe, across, span);
-        });
+    return by_rows(S, across, [&](auto small, int rows, dim3 grid, GridSpan span) {
+        ffn_rows_kernel<true, decltype(small)::value><<<grid, kGemmThreads, 0, s>>>(
+            S, (const char*)dgu, 2 * S.I, (const char*)w_gate_up, S.H, (char*)grad_xe, rows, across, span);
     });
 }
 

@@ -180,6 +180,9 @@ SHAPES = [
     ("long sums", routed(70, 4, 2), 2304, 1288, 4, 2),
     ("many rows", routed(2100, 4, 2), 320, 192, 4, 2),
     ("wide experts", routed(600, 3, 1), 1024, 776, 3, 3),
+    # tile heights other than 256 and 64 are taken where they make the rounds of blocks come out better
+    ("shorter tiles", routed(1500, 16, 4), 136, 1000, 16, 4),
+    ("shorter tiles of rows", routed(4096, 8, 2), 4096, 72, 8, 8),
 ]
 IDS = [s[0].replace(" ", "-") for s in SHAPES]
 

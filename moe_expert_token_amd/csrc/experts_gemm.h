@@ -21,7 +21,13 @@
 //
 // A slot is free as soon as its fragments are in registers, so its next load
 // starts seven phases before it is read: that is what hides the memory's
-// latency.
+// latency.  (With loads one step ahead, grad_xe of 32 experts of 7168 x 2048
+// ran at 1.12 PFLOP/s, and at 1.45 with the loads left out.)
+//
+// Weight gradients of 8 experts of 1024 rows, 4096 x 14336, take 33 us a tile
+// on average.  Cut to one step of k they take 10.6: so 1.5 us a step, 1.43
+// PFLOP/s over 256 CUs, and a third of the time is the start and the end of
+// tiles; without the stores the whole takes 1066 us instead of 1393.
 //
 // Rows, features and k past the operand's end are loads out of the buffer
 // descriptor's range: they read as zero and touch no memory.

@@ -1,11 +1,13 @@
-// experts_pack.hip -- 8-bit activation checkpoints of rows.
+// experts_pack.hip -- 8-bit activation checkpoints of rows: q = rne(x / step), step = max |x| / 127 of 32 neighbours
+// rounded up to bf16, so that no quotient passes 127 and q * step is exact in fp32.
 #include "experts.h"
 
 namespace ms {
 namespace {
 
-// Both kernels move bytes and nothing else: a lane has one vector of 8 elements, four neighbouring lanes a group,
-// and vectors that nothing reads again soon pass the caches by.  8192 x 7168 (361 MB of traffic for both): PERF.
+// Both kernels are bound by the bytes they move: a lane has one vector of 8 elements, four neighbouring lanes a group
+// (two shuffles find its largest), and vectors that nothing reads again soon pass the caches by.  8192 x 7168, 180 MB
+// each way: 34 us a kernel, 5.3 TB/s (a plain copy of 2 GiB runs at 6.5).
 
 // The vector of unit i, its group g and whether it is in the row; units are four a group.  Where rows are whole
 // groups (Whole) units and vectors are the same, and no division is needed.

@@ -1,4 +1,5 @@
-// experts_w4.hip -- the making of 4-bit weights.
+// experts_w4.hip -- the making of 4-bit weights: step = max |w| / 7 of a group, rounded to bf16, q = rne(w / step) + 8.
+// Done once for a set of weights; not timed.
 #include "experts.h"
 
 namespace ms {

@@ -5,6 +5,7 @@ A thin Python face of the C ABI in include/moe_shuffle.h and
 include/moe_experts.h; every step runs in
 the HIP kernels of libmoe_shuffle.so.  Tensors are torch tensors on the GPU;
 bf16 activations may be torch.bfloat16 or any 16-bit view of the same bits.
+The experts' calls compute with the values and refuse other floating types.
 """
 
 from ._lib import (  # noqa: F401

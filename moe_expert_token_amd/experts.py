@@ -1,18 +1,23 @@
 """ctypes binding of the experts' block (include/moe_experts.h).
 
-Argument marshalling as in _lib, and one check more: the sizes the library
-cannot see in a pointer (of weights, of what forward saved) are compared
-with the tensors given, since a short one would be read or written past its
-end.  A tensor that is not contiguous, of another element size or another
-shape is refused with E_INVALID_ARG like the library's own refusals.
+Argument marshalling as in _lib, and what the library cannot see in a
+pointer: the sizes (of weights, of what forward saved) are compared with the
+tensors given, since a short one would be read or written past its end, and
+the kernels run on the stream's device (the current one's where no stream is
+given), so every tensor must lie there.  A tensor that is not contiguous, of
+another element size or shape, of a floating type other than bfloat16, in host
+memory or on another device is refused with E_INVALID_ARG like the library's
+own refusals.
 """
 
 from __future__ import annotations
 
 import ctypes
 
+import torch
+
 from . import _lib
-from ._lib import Dims, E_INVALID_ARG, MoeShuffleError, Plan, _check, _stream
+from ._lib import Dims, E_INVALID_ARG, MoeShuffleError, Plan, _check, _cur_device, _stream
 
 ACT_SILU, ACT_GELU_TANH = 0, 1
 GROUP8 = 32  # MOE_EXPERTS_GROUP8
@@ -52,13 +57,29 @@ def _refuse(func: str, what: str):
 
 
 def _at(func: str, name: str, t, shape, width: int):
-    """The address of a contiguous tensor of this shape and element size (None stays None)."""
+    """The address of a contiguous tensor of this shape and element size (None stays None).  Any type of that size
+    stands for its bits (int16 for bf16, uint8 for int8), but another floating type means other values."""
     if t is None:
         return None
     if tuple(t.shape) != tuple(shape) or t.element_size() != width or not t.is_contiguous():
         _refuse(func, f"{name} must be contiguous {list(shape)} of {width}-byte elements, "
                       f"not {list(t.shape)} of {t.element_size()}")
+    if t.is_floating_point() and t.dtype != torch.bfloat16:
+        _refuse(func, f"{name} must not be {t.dtype}")
     return t.data_ptr()
+
+
+def _on_gpu(func: str, stream, **tensors):
+    """Every tensor given lies on the device that the kernels run on."""
+    for name, t in tensors.items():
+        if t is not None and not t.is_cuda:
+            _refuse(func, f"{name} must be on the GPU, not on {t.device}")
+    device = getattr(stream, "device_index", None)
+    if device is None:
+        device = _cur_device() if _cur_device is not None else torch.cuda.current_device()
+    for name, t in tensors.items():
+        if t is not None and t.get_device() != device:
+            _refuse(func, f"{name} must be on GPU {device}, not on {t.device}")
 
 
 def _block(func: str, plan: Plan, w, half: int, name: str):
@@ -100,10 +121,12 @@ def moe_experts_ffn_forward(plan: Plan, xe, w_gate_up, w_down, ye, workspace, sa
     P, H, E, inter = _block(f, plan, w_down, 1, "w_down")
     ws, ws_bytes = _workspace(f, workspace)
     held, scale = _saved(f, saved, saved_scale, P, inter)
-    _check(f, _load().moe_experts_ffn_forward(
-        plan.handle, _at(f, "xe", xe, (P, H), 2), _at(f, "w_gate_up", w_gate_up, (E, 2 * inter, H), 2),
-        _at(f, "w_down", w_down, (E, H, inter), 2), inter, int(act), _at(f, "ye", ye, (P, H), 2), held, scale, ws,
-        ws_bytes, _stream(stream)))
+    args = (_at(f, "xe", xe, (P, H), 2), _at(f, "w_gate_up", w_gate_up, (E, 2 * inter, H), 2),
+            _at(f, "w_down", w_down, (E, H, inter), 2), inter, int(act), _at(f, "ye", ye, (P, H), 2), held, scale, ws,
+            ws_bytes)
+    _on_gpu(f, stream, xe=xe, w_gate_up=w_gate_up, w_down=w_down, ye=ye, saved=saved, saved_scale=saved_scale,
+            workspace=workspace)
+    _check(f, _load().moe_experts_ffn_forward(plan.handle, *args, _stream(stream)))
 
 
 def moe_experts_ffn_backward(plan: Plan, grad_ye, xe, w_gate_up, w_down, saved, grad_xe, grad_w_gate_up,
@@ -114,11 +137,13 @@ def moe_experts_ffn_backward(plan: Plan, grad_ye, xe, w_gate_up, w_down, saved, 
     ws, ws_bytes = _workspace(f, workspace)
     held, scale = _saved(f, saved, saved_scale, P, inter)
     up, down = (E, 2 * inter, H), (E, H, inter)
-    _check(f, _load().moe_experts_ffn_backward(
-        plan.handle, _at(f, "grad_ye", grad_ye, (P, H), 2), _at(f, "xe", xe, (P, H), 2),
-        _at(f, "w_gate_up", w_gate_up, up, 2), _at(f, "w_down", w_down, down, 2), inter, int(act), held, scale,
-        _at(f, "grad_xe", grad_xe, (P, H), 2), _at(f, "grad_w_gate_up", grad_w_gate_up, up, 2),
-        _at(f, "grad_w_down", grad_w_down, down, 2), ws, ws_bytes, _stream(stream)))
+    args = (_at(f, "grad_ye", grad_ye, (P, H), 2), _at(f, "xe", xe, (P, H), 2), _at(f, "w_gate_up", w_gate_up, up, 2),
+            _at(f, "w_down", w_down, down, 2), inter, int(act), held, scale, _at(f, "grad_xe", grad_xe, (P, H), 2),
+            _at(f, "grad_w_gate_up", grad_w_gate_up, up, 2), _at(f, "grad_w_down", grad_w_down, down, 2), ws, ws_bytes)
+    _on_gpu(f, stream, grad_ye=grad_ye, xe=xe, w_gate_up=w_gate_up, w_down=w_down, saved=saved,
+            saved_scale=saved_scale, grad_xe=grad_xe, grad_w_gate_up=grad_w_gate_up, grad_w_down=grad_w_down,
+            workspace=workspace)
+    _check(f, _load().moe_experts_ffn_backward(plan.handle, *args, _stream(stream)))
 
 
 def moe_experts_ffn_w4_forward(plan: Plan, xe, q_gate_up, s_gate_up, q_down, s_down, ye, workspace, group: int = 128,
@@ -129,11 +154,13 @@ def moe_experts_ffn_w4_forward(plan: Plan, xe, q_gate_up, s_gate_up, q_down, s_d
     if group <= 0:
         _refuse(f, "group must be 32, 64 or 128")
     ws, ws_bytes = _workspace(f, workspace)
-    _check(f, _load().moe_experts_ffn_w4_forward(
-        plan.handle, _at(f, "xe", xe, (P, H), 2), _at(f, "q_gate_up", q_gate_up, (E, 2 * inter, H // 2), 1),
-        _at(f, "s_gate_up", s_gate_up, (E, 2 * inter, H // group), 2), _at(f, "q_down", q_down, (E, H, inter // 2), 1),
-        _at(f, "s_down", s_down, (E, H, inter // group), 2), inter, int(group), int(act),
-        _at(f, "ye", ye, (P, H), 2), ws, ws_bytes, _stream(stream)))
+    args = (_at(f, "xe", xe, (P, H), 2), _at(f, "q_gate_up", q_gate_up, (E, 2 * inter, H // 2), 1),
+            _at(f, "s_gate_up", s_gate_up, (E, 2 * inter, H // group), 2),
+            _at(f, "q_down", q_down, (E, H, inter // 2), 1), _at(f, "s_down", s_down, (E, H, inter // group), 2), inter,
+            int(group), int(act), _at(f, "ye", ye, (P, H), 2), ws, ws_bytes)
+    _on_gpu(f, stream, xe=xe, q_gate_up=q_gate_up, s_gate_up=s_gate_up, q_down=q_down, s_down=s_down, ye=ye,
+            workspace=workspace)
+    _check(f, _load().moe_experts_ffn_w4_forward(plan.handle, *args, _stream(stream)))
 
 
 def moe_experts_w4_quantize(w, q, scale, group: int = 128, stream=None):
@@ -142,24 +169,27 @@ def moe_experts_w4_quantize(w, q, scale, group: int = 128, stream=None):
     if group <= 0:
         _refuse(f, "group must be 32, 64 or 128")
     lead, cols = tuple(w.shape[:-1]), w.shape[-1]
-    _check(f, _load().moe_experts_w4_quantize(
-        _at(f, "w", w, w.shape, 2), w.numel() // max(cols, 1), cols, int(group),
-        _at(f, "q", q, lead + (cols // 2,), 1), _at(f, "scale", scale, lead + (cols // group,), 2), _stream(stream)))
+    args = (_at(f, "w", w, w.shape, 2), w.numel() // max(cols, 1), cols, int(group),
+            _at(f, "q", q, lead + (cols // 2,), 1), _at(f, "scale", scale, lead + (cols // group,), 2))
+    _on_gpu(f, stream, w=w, q=q, scale=scale)
+    _check(f, _load().moe_experts_w4_quantize(*args, _stream(stream)))
 
 
 def moe_experts_pack8(x, q, scale, stream=None):
     """Rows of x (bf16) to int8 with a bf16 scale for every 32 elements along the last axis."""
     f = "moe_experts_pack8"
     lead, cols = tuple(x.shape[:-1]), x.shape[-1]
-    _check(f, _load().moe_experts_pack8(
-        _at(f, "x", x, x.shape, 2), x.numel() // max(cols, 1), cols, _at(f, "q", q, x.shape, 1),
-        _at(f, "scale", scale, lead + (-(-cols // GROUP8),), 2), _stream(stream)))
+    args = (_at(f, "x", x, x.shape, 2), x.numel() // max(cols, 1), cols, _at(f, "q", q, x.shape, 1),
+            _at(f, "scale", scale, lead + (-(-cols // GROUP8),), 2))
+    _on_gpu(f, stream, x=x, q=q, scale=scale)
+    _check(f, _load().moe_experts_pack8(*args, _stream(stream)))
 
 
 def moe_experts_unpack8(q, scale, x, stream=None):
     """The bf16 values that packed rows hold."""
     f = "moe_experts_unpack8"
     lead, cols = tuple(x.shape[:-1]), x.shape[-1]
-    _check(f, _load().moe_experts_unpack8(
-        _at(f, "q", q, x.shape, 1), _at(f, "scale", scale, lead + (-(-cols // GROUP8),), 2),
-        x.numel() // max(cols, 1), cols, _at(f, "x", x, x.shape, 2), _stream(stream)))
+    args = (_at(f, "q", q, x.shape, 1), _at(f, "scale", scale, lead + (-(-cols // GROUP8),), 2),
+            x.numel() // max(cols, 1), cols, _at(f, "x", x, x.shape, 2))
+    _on_gpu(f, stream, q=q, scale=scale, x=x)
+    _check(f, _load().moe_experts_unpack8(*args, _stream(stream)))

@@ -1,0 +1,283 @@
+"""Every form of the experts' kernels that the library chooses by size, against
+64 bits under bounds that a wrong result exceeds (test_experts_bounds.py shows
+what they catch), and values at the ends of their ranges: gates far from zero,
+subnormal rows, offsets past 2^31."""
+
+import numpy as np
+import pytest
+import torch
+
+import experts_bounds as eb
+import experts_inputs as inputs
+import experts_ref as ref
+from test_gpu_experts import SENTINEL, W4_SHAPES, Case, routed, say
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import moe_expert_token_amd as ms
+    ms.load()
+
+
+class Block:
+    """A plan with rows and weights given; calls that return whole outputs."""
+
+    def __init__(self, counts, H, I, seed):
+        import moe_expert_token_amd as ms
+        self.ms, self.counts, self.P, self.H, self.I, self.E = ms, counts, sum(counts), H, I, len(counts)
+        idx = inputs.ids(counts)
+        self.dims = ms.dims_of(self.P, H, self.E, 1, 1)
+        self.plan_ws = torch.empty(ms.moe_shuffle_workspace_size(self.dims), dtype=torch.uint8, device="cuda")
+        self.plan = ms.moe_shuffle_plan(self.dims, torch.from_numpy(idx).cuda(), self.plan_ws)
+        self.offset = np.concatenate([[0], np.cumsum(counts)])
+        self.gen = torch.Generator(device="cuda").manual_seed(seed)
+        self.ws = torch.empty(ms.moe_experts_ffn_workspace_size(self.dims, I, True), dtype=torch.uint8, device="cuda")
+
+    def segments(self):
+        return [(e, int(self.offset[e]), int(self.offset[e + 1])) for e in range(self.E) if self.counts[e]]
+
+    def out(self):
+        return torch.full((self.P + 1, self.H), SENTINEL, dtype=torch.bfloat16, device="cuda")
+
+    def forward(self, x, w1, w2, act=0, saved=None, scale=None):
+        ye = self.out()
+        self.ms.moe_experts_ffn_forward(self.plan, x, w1, w2, ye[:self.P], self.ws, saved=saved, saved_scale=scale,
+                                        act=act)
+        return ye
+
+    def w4(self, x, weights, group, act=0):
+        ye = self.out()
+        self.ms.moe_experts_ffn_w4_forward(self.plan, x, *weights, ye[:self.P], self.ws, group=group, act=act)
+        return ye
+
+
+def inside(what, ye, lo, hi, r, worst):
+    a, b = eb.excess(ye[lo:hi], r["y"], r["e_y"]), eb.row_excess(ye[lo:hi], r["y"], r["n_y"])
+    assert a <= 1, f"{what}: an element's error is {a:.3g} of its bound"
+    assert b <= 1, f"{what}: a row's error norm is {b:.3g} of its bound"
+    worst[0], worst[1] = max(worst[0], a), max(worst[1], b)
+
+
+def check_saved(what, c, saved, scale, lo, hi, r):
+    for which, (v, d) in enumerate(((r["g"], r["e_g"]), (r["u"], r["e_u"]))):
+        held = saved[lo:hi, which * c.I:(which + 1) * c.I]
+        if scale is None:
+            assert eb.excess(held, v, d + ref.U * (v.abs() + d) + ref.TINY) <= 1, f"{what}: saved"
+            continue
+        step = scale[lo:hi, which].double()
+        wide = step.repeat_interleave(32, -1)[:, :c.I]
+        # the nearest of the 8-bit values; the reciprocal's and the product's roundings move 127 by 2^-23 each
+        assert eb.excess(ref.unpack8(held, scale[lo:hi, which]), v, d + wide * (0.5 + 127 * 2.0 ** -22) + ref.TINY) <= 1, \
+            f"{what}: 8 bits"
+        pad = torch.nn.functional.pad
+        top = pad(v.abs(), (0, -c.I % 32)).unflatten(-1, (-1, 32)).amax(-1)
+        dt = pad(d, (0, -c.I % 32)).unflatten(-1, (-1, 32)).amax(-1)
+        # the step is the largest / 127 rounded up to bf16: never under it, less than a bf16 step (2^-7) over it
+        assert bool((step * 127 >= (top - dt) * (1 - 2.0 ** -23)).all()), what
+        assert bool((step * 127 <= (top + dt) * (1 + 2.0 ** -7 + 2.0 ** -22) + 2.0 ** -118).all()), what
+
+
+@pytest.mark.parametrize("kind", ["dense", "sparse"])
+@pytest.mark.parametrize("H,I", inputs.BF16_FORMS)
+def test_bf16_streams(H, I, kind):
+    act = (H > I) * 1
+    say(f"[experts] bf16 streams {H} x {I} {kind}")
+    c = Block(inputs.FEW, H, I, H + I)
+    x = inputs.rows(kind, c.P, H, I, c.gen, "cuda")
+    w1, w2 = inputs.bf16(kind, c.E, H, I, c.gen, "cuda")
+    ye = c.forward(x, w1, w2, act)
+    held = [(torch.empty((c.P, 2 * I), dtype=torch.bfloat16, device="cuda"), None),
+            (torch.empty((c.P, 2 * I), dtype=torch.int8, device="cuda"),
+             torch.empty((c.P, 2, -(-I // 32)), dtype=torch.bfloat16, device="cuda"))]
+    for saved, scale in held:
+        assert torch.equal(c.forward(x, w1, w2, act, saved, scale), ye), "what is saved does not change ye"
+    assert bool((ye[c.P:] == SENTINEL).all())
+    worst = [0.0, 0.0]
+    for e, lo, hi in c.segments():
+        r = eb.forward(x[lo:hi].double(), eb.bf16_weights(w1[e]), eb.bf16_weights(w2[e]), act)
+        inside(f"expert {e}", ye, lo, hi, r, worst)
+        for saved, scale in held:
+            check_saved(f"expert {e}", c, saved, scale, lo, hi, r)
+    say(f"[experts] bf16 streams {H} x {I} {kind}: of the bounds {worst}")
+
+
+@pytest.mark.parametrize("kind", ["dense", "sparse"])
+@pytest.mark.parametrize("group,rows,k", inputs.W4_FORMS)
+def test_w4_forms(group, rows, k, kind):
+    counts = inputs.FEW if rows == "few" else inputs.MANY
+    for H, I in ((k, 128), (512, k)):
+        act = (H > I) * 1
+        say(f"[experts] w4 group {group} {rows} rows {H} x {I} {kind}")
+        c = Block(counts, H, I, H + I + group)
+        x = inputs.rows(kind, c.P, H, I, c.gen, "cuda")
+        q1, s1, q2, s2 = inputs.w4(kind, c.E, H, I, group, c.gen, "cuda")
+        ye = c.w4(x, (q1, s1, q2, s2), group, act)
+        assert bool((ye[c.P:] == SENTINEL).all())
+        worst = [0.0, 0.0]
+        for e, lo, hi in c.segments():
+            r = eb.forward(x[lo:hi].double(), eb.w4_weights(q1[e], s1[e], group), eb.w4_weights(q2[e], s2[e], group), act)
+            inside(f"expert {e}", ye, lo, hi, r, worst)
+        say(f"[experts] w4 group {group} {rows} rows {H} x {I} {kind}: of the bounds {worst}")
+
+
+@pytest.mark.parametrize("name,idx,H,I,E,R,group", W4_SHAPES, ids=[s[0].replace(" ", "-") for s in W4_SHAPES])
+def test_w4_shapes_under_narrow_bounds(name, idx, H, I, E, R, group):
+    """The shapes of test_w4_forward; the bounds count what a group's sum rounds, not 64 terms for each of k."""
+    say(f"[experts] w4 narrow {name}")
+    c = Case(idx, H, I, E, R, seed=len(name) + 8)
+    q1, s1, q2, s2 = inputs.w4("dense", E, H, I, group, c.gen, "cuda")
+    whole, ye = c.out(c.P, H)
+    act = len(name) % 2
+    c.ms.moe_experts_ffn_w4_forward(c.plan, c.xe, q1, s1, q2, s2, ye, c.ws, group=group, act=act)
+    worst = [0.0, 0.0]
+    for e, lo, hi in c.segments():
+        if lo < hi:
+            r = eb.forward(c.xe[lo:hi].double(), eb.w4_weights(q1[e], s1[e], group), eb.w4_weights(q2[e], s2[e], group),
+                           act)
+            inside(f"expert {e}", whole, lo, hi, r, worst)
+    say(f"[experts] w4 narrow {name}: of the bounds {worst}")
+
+
+# ---- gates far from zero ----
+
+@pytest.mark.parametrize("act", [0, 1], ids=["silu", "gelu"])
+@pytest.mark.parametrize("rows", [3, 40, 90], ids=["streams", "small-tiles", "tiles"])
+def test_far_gates(rows, act):
+    """Gates of about +-1e7: act(g) is g or 0, its derivative 1 or 0, in every form of the block."""
+    H, I = 64, 32
+    c = Case(inputs.ids([rows, rows]), H, I, 2, 1, seed=rows + act)
+    c.xe *= 1e4
+    c.w1 *= 1e3
+    ye, saved, scale = c.forward(act, "bf16")
+    got = c.backward(saved, scale, act)
+    for e, lo, hi in c.segments():
+        x, w1, w2, gy = (t.double() for t in (c.xe[lo:hi], c.w1[e], c.w2[e], c.gy[lo:hi]))
+        r = eb.forward(x, eb.bf16_weights(w1), eb.bf16_weights(w2), act)
+        inside(f"expert {e}", ye, lo, hi, r, [0.0, 0.0])
+        check_saved(f"expert {e}", c, saved, None, lo, hi, r)
+        g, u = saved[lo:hi, :I].double(), saved[lo:hi, I:].double()
+        b = eb.backward(gy, x, w1, w2, g, u, act)
+        for n in ("grad_xe", "grad_w_gate_up", "grad_w_down"):
+            mine = got[n][lo:hi] if n == "grad_xe" else got[n][e]
+            a = eb.excess(mine, b[n], b["e_" + n])
+            d = mine.double() - b[n]
+            size = float(((d.norm(dim=1) if n == "grad_xe" else d.norm()) / b["n_" + n]).max())
+            assert a <= 1 and size <= 1, (e, n, a, size)
+
+
+# ---- subnormal rows ----
+
+def test_pack8_of_subnormals_that_round_to_one_step():
+    """Magnitudes between 2^-127 and 2^-126 with the least step, 2^-126: q is +-1, or 0 at 2^-127 itself (a tie)."""
+    import moe_expert_token_amd as ms
+    k = torch.arange(64, 128, device="cuda").repeat(3, 2)[:, :96]  # x = k 2^-133
+    sign = torch.where(torch.arange(96, device="cuda") % 3 == 0, -1.0, 1.0)
+    x = (k.double() * 2.0 ** -133 * sign).to(torch.bfloat16)
+    assert bool(((x.double() * 2.0 ** 133).abs() == k).all())
+    q = torch.empty(x.shape, dtype=torch.int8, device="cuda")
+    s = torch.empty((3, 3), dtype=torch.bfloat16, device="cuda")
+    back = torch.empty_like(x)
+    ms.moe_experts_pack8(x, q, s)
+    ms.moe_experts_unpack8(q, s, back)
+    assert bool((s.double() == 2.0 ** -126).all())
+    want = torch.where(k > 64, sign.expand(3, -1), 0.0)
+    assert torch.equal(q.double(), want.double())
+    assert torch.equal(back.double(), want.double() * 2.0 ** -126)
+
+
+@pytest.mark.parametrize("rows", [3, 40, 90], ids=["streams", "small-tiles", "tiles"])
+def test_subnormal_rows_through_the_block(rows):
+    """Rows of k 2^-133 with weights of order 2^124: g and u are of order 1 and a little above."""
+    H, I = 128, 64
+    c = Case(inputs.ids([rows, rows]), H, I, 2, 1, seed=rows)
+    k = torch.randint(-127, 128, (c.P, H), device="cuda", generator=c.gen)
+    c.xe = (k.double() * 2.0 ** -133).to(torch.bfloat16)
+    assert bool((c.xe.double() * 2.0 ** 133 == k).all())
+    c.w1 = (c.w1.float() * 2.0 ** 127).to(torch.bfloat16)
+    ye, _, _ = c.forward(0)
+    for e, lo, hi in c.segments():
+        r = eb.forward(c.xe[lo:hi].double(), eb.bf16_weights(c.w1[e]), eb.bf16_weights(c.w2[e]), 0)
+        assert float(r["g"].abs().mean()) > 0.1
+        inside(f"expert {e}", ye, lo, hi, r, [0.0, 0.0])
+
+
+@pytest.mark.parametrize("counts", [[5, 9], [40, 30]], ids=["few", "many"])
+def test_subnormal_rows_with_4_bit_weights(counts):
+    H, I, group = 128, 128, 32
+    c = Block(counts, H, I, 9)
+    q1, s1, q2, s2 = inputs.w4("dense", c.E, H, I, group, c.gen, "cuda")
+    s1 = (s1.float() * 2.0 ** 127).to(torch.bfloat16)
+    k = torch.randint(-127, 128, (c.P, H), device="cuda", generator=c.gen)
+    x = (k.double() * 2.0 ** -133).to(torch.bfloat16)
+    ye = c.w4(x, (q1, s1, q2, s2), group)
+    for e, lo, hi in c.segments():
+        w1, m1 = eb.w4_weights(q1[e], s1[e], group)
+        # a group's sum is a multiple of 2^-133 far below 2^-119: fp32 holds it without rounding (24 bits from 2^-149)
+        r = eb.forward(x[lo:hi].double(), (w1, m1), eb.w4_weights(q2[e], s2[e], group), 0)
+        assert float(r["g"].abs().mean()) > 0.1
+        inside(f"expert {e}", ye, lo, hi, r, [0.0, 0.0])
+
+
+# ---- offsets past 2^31 bytes ----
+
+@pytest.mark.parametrize("rows", [3, 20, 70], ids=["streams", "small-tiles", "tiles"])
+def test_weights_past_two_gigabytes(rows):
+    """136 experts of 4096 x 2048: the last ones' weights lie past 2^31 (down) and 2^32 bytes (up)."""
+    H, I, E = 4096, 2048, 136
+    say(f"[experts] {rows} rows an expert, 4.6 GB of weights")
+    c = Case(inputs.ids([rows] * E), H, I, E, 1, seed=rows)
+    assert c.w2[-1].data_ptr() - c.w2.data_ptr() > 1 << 31 and c.w1[-1].data_ptr() - c.w1.data_ptr() > 1 << 32
+    ye, saved, scale = c.forward(0, "bf16")
+    got = c.backward(saved, scale) if rows > 3 else None
+    for e in (0, E // 2, E - 1):
+        lo, hi = int(c.offset[e]), int(c.offset[e + 1])
+        x, w1, w2, gy = (t.double() for t in (c.xe[lo:hi], c.w1[e], c.w2[e], c.gy[lo:hi]))
+        r = eb.forward(x, eb.bf16_weights(w1), eb.bf16_weights(w2), 0)
+        inside(f"expert {e}", ye, lo, hi, r, [0.0, 0.0])
+        if got is None:
+            continue
+        b = eb.backward(gy, x, w1, w2, saved[lo:hi, :I].double(), saved[lo:hi, I:].double(), 0)
+        for n in got:
+            mine = got[n][lo:hi] if n == "grad_xe" else got[n][e]
+            a = eb.excess(mine, b[n], b["e_" + n])
+            d = mine.double() - b[n]
+            size = float(((d.norm(dim=1) if n == "grad_xe" else d.norm()) / b["n_" + n]).max())
+            assert a <= 1 and size <= 1, (e, n, a, size)
+
+
+def test_4_bit_weights_past_two_gigabytes():
+    H, I, E, group = 4096, 4096, 144, 128
+    say("[experts] 3.6 GB of 4-bit weights")
+    c = Block([2] * E, H, I, 5)
+    q1, s1, q2, s2 = inputs.w4("dense", E, H, I, group, c.gen, "cuda")
+    assert q1[-1].data_ptr() - q1.data_ptr() > 1 << 31
+    x = inputs.rows("dense", c.P, H, I, c.gen, "cuda")
+    ye = c.w4(x, (q1, s1, q2, s2), group)
+    for e in (0, E // 2, E - 1):
+        lo, hi = int(c.offset[e]), int(c.offset[e + 1])
+        r = eb.forward(x[lo:hi].double(), eb.w4_weights(q1[e], s1[e], group), eb.w4_weights(q2[e], s2[e], group), 0)
+        inside(f"expert {e}", ye, lo, hi, r, [0.0, 0.0])
+
+
+def test_rows_past_two_gigabytes():
+    """300000 rows of 4096: xe, ye and grad_xe pass 2^31 bytes; and of what is saved, 2I = 4096."""
+    H, I, E = 4096, 2048, 4
+    T = 300000
+    c = Case(routed(T, E, 1, seed=2), H, I, E, 1, seed=6)
+    say("[experts] 300000 rows")
+    ye, saved, scale = c.forward(0, "bf16")
+    got = c.backward(saved, scale, want=("grad_xe",))["grad_xe"]
+    assert bool((ye[T:] == SENTINEL).all()) and bool((got[T:] == SENTINEL).all())
+    for lo in (0, T // 2, T - 40):
+        for i in (lo, lo + 39):
+            e = int(np.searchsorted(c.offset, i, side="right")) - 1
+            x, w1, w2, gy = (t.double() for t in (c.xe[i:i + 1], c.w1[e], c.w2[e], c.gy[i:i + 1]))
+            r = eb.forward(x, eb.bf16_weights(w1), eb.bf16_weights(w2), 0)
+            inside(f"row {i}", ye, i, i + 1, r, [0.0, 0.0])
+            b = eb.backward(gy, x, w1, w2, saved[i:i + 1, :I].double(), saved[i:i + 1, I:].double(), 0)
+            assert eb.excess(got[i:i + 1], b["grad_xe"], b["e_grad_xe"]) <= 1
+            assert eb.row_excess(got[i:i + 1], b["grad_xe"], b["n_grad_xe"]) <= 1

@@ -114,10 +114,13 @@ int moe_experts_ffn_backward(moe_shuffle_plan_t plan, const void* grad_ye, const
  *              column in the low four bits;   s_gate_up bf16 [E, 2I, H / group]
  *   q_down     device uint8 [E, H, I / 2];    s_down    bf16 [E, H, I / group]
  *   group      32, 64 or 128; H and I multiples of it (MOE_SHUFFLE_E_ALIGN)
- * (q - 8) is exact in the products and a group's sum is scaled in fp32, so
- * no weight is rounded.  An infinite x gives NaN.  Any number of rows is
- * computed; with hundreds for an expert, bf16 weights are the faster form.  Other arguments as
- * for moe_experts_ffn_forward; all pointers 16-byte aligned.
+ * A group's sum is sum q x - 8 sum x in fp32, scaled in fp32: no weight is
+ * rounded, and what is lost is the fp32 rounding of 2 * group terms of up to
+ * 15 |x|, also where q is 8.  An infinite x gives NaN, and so may finite ones
+ * whose magnitudes in a group sum to 2^128 / 15 (2.2e37) or more; the same
+ * goes for h in the down projection.  Any number of rows is computed; with
+ * hundreds for an expert, bf16 weights are the faster form.  Other arguments
+ * as for moe_experts_ffn_forward; all pointers 16-byte aligned.
  */
 int moe_experts_ffn_w4_forward(moe_shuffle_plan_t plan, const void* xe, const void* q_gate_up, const void* s_gate_up,
                                const void* q_down, const void* s_down, int32_t inter, int32_t group, int32_t act,

@@ -11,12 +11,17 @@
 // are its own: the block's waves split k and add their sums through LDS in a
 // fixed tree.
 //
-// A 4-bit value q enters the product as the bf16 number 128 + q, whose low
-// mantissa bits are q: one shift and one v_and_or_b32 make two of them.  What
-// that adds to a sum, 136 x over q - 8, is taken off by adding the product of
-// the rows with -136, which the feature groups share.  A group's sum is exact
-// up to fp32 rounding and is scaled in fp32 as it is added.  (An infinite x
-// therefore gives NaN.)  The 16 bytes that a lane loads of a weight
+// A 4-bit value q enters the product as the bf16 number q: as a byte it is the
+// e4m3 number q 2^-9, and v_cvt_scalef32_pk_bf16_fp8 makes two bf16 numbers of
+// two bytes.  The 8 of q - 8 is taken off by adding the product of the rows
+// with -8, which the feature groups share.  So a group's sum is one in fp32
+// over terms of up to 15 |x| and of 8 |x|, also where q - 8 is 0, and is scaled
+// in fp32 as it is added; an infinite x gives NaN, and so may finite ones whose
+// magnitudes in a group sum to 2^128 / 15 or more.  (Signed
+// numbers q - 8 need no second term and take longer to make: 45.9 us against
+// 39.2, one token, 256 experts of 7168 x 2048, and 1004 against 944, 48 tokens.
+// 128 + q from the mantissa's bits, with -136, takes the same time and loses
+// four bits more beside a large x.)  The 16 bytes that a lane loads of a weight
 // row are 32 neighbouring k; a transpose over the four quarters of the wave
 // (two v_permlane32_swap, two v_permlane16_swap) deals them out so that each
 // matrix instruction covers 32 neighbouring k, and so one group.
@@ -89,6 +94,14 @@ struct Source {
         if (Group) sc[i].init(scales, (int64_t)min(valid, 32) * sld);
     }
 };
+
+// Two bytes of 0 .. 15 (the upper two where High) as bf16 numbers: the e4m3 numbers that such bytes stand for, 2^-9 of
+// them each (the subnormal ones and the first exponent), times 2^9.
+template <bool High>
+__device__ __forceinline__ unsigned two_of_e4m3(unsigned v)
+{
+    return __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v, 512.0f, High));
+}
 
 // 16 rows a group and stream: what a wave has of the weights of one chunk.
 template <int Group>
@@ -187,7 +200,7 @@ struct Chunk {
             }
         } else {
             constexpr int kPer = Group / 32;  // matrix instructions a group
-            const u32x4 minus136 = {0xc308c308u, 0xc308c308u, 0xc308c308u, 0xc308c308u};
+            const u32x4 minus8 = {0xc100c100u, 0xc100c100u, 0xc100c100u, 0xc100c100u};
             u32x4 d[kGroupsOf16];
             unsigned now[kGroupsOf16][2];
 #pragma unroll
@@ -203,8 +216,6 @@ struct Chunk {
             }
             load_packed(P, S, next);
             __builtin_amdgcn_sched_barrier(0);  // loads go out here, not where the compiler would save registers
-            unsigned magic = 0x43004300u;       // in a vector register, for v_and_or_b32 to take it with the mask
-            asm("" : "+v"(magic));
 #pragma unroll
             for (int j0 = 0; j0 < 4; j0 += kPer) {
                 bf16x8 xs[RT][kPer];
@@ -213,15 +224,15 @@ struct Chunk {
                 for (int j = 0; j < kPer; ++j) {
 #pragma unroll
                     for (int t = 0; t < RT; ++t) {
-                        // k in the order (0, 4), (1, 5), (2, 6), (3, 7) in which the weights' nibbles come apart
+                        // k in the order (0, 2), (4, 6), (1, 3), (5, 7) in which the weights' nibbles come apart
                         const u32x4 v = x[t][j0 + j];
-                        const u32x4 p = {__builtin_amdgcn_perm(v[2], v[0], 0x05040100),
-                                         __builtin_amdgcn_perm(v[2], v[0], 0x07060302),
-                                         __builtin_amdgcn_perm(v[3], v[1], 0x05040100),
-                                         __builtin_amdgcn_perm(v[3], v[1], 0x07060302)};
+                        const u32x4 p = {__builtin_amdgcn_perm(v[1], v[0], 0x05040100),
+                                         __builtin_amdgcn_perm(v[3], v[2], 0x05040100),
+                                         __builtin_amdgcn_perm(v[1], v[0], 0x07060302),
+                                         __builtin_amdgcn_perm(v[3], v[2], 0x07060302)};
                         xs[t][j] = __builtin_bit_cast(bf16x8, p);
                         const f32x4 zero = {0, 0, 0, 0};
-                        base[t] = mfma_16x16x32(xs[t][j], __builtin_bit_cast(bf16x8, minus136), j ? base[t] : zero);
+                        base[t] = mfma_16x16x32(xs[t][j], __builtin_bit_cast(bf16x8, minus8), j ? base[t] : zero);
                     }
                     load_part(P, S, next, j0 + j);
                 }
@@ -231,9 +242,9 @@ struct Chunk {
                     f32x4 sum[RT];
 #pragma unroll
                     for (int j = 0; j < kPer; ++j) {
-                        const unsigned v = d[s][j0 + j];
-                        const u32x4 p = {(v & 0x000f000fu) | magic, ((v >> 4) & 0x000f000fu) | magic,
-                                         ((v >> 8) & 0x000f000fu) | magic, ((v >> 12) & 0x000f000fu) | magic};
+                        const unsigned v = d[s][j0 + j], lo = v & 0x0f0f0f0fu, hi = (v >> 4) & 0x0f0f0f0fu;
+                        const u32x4 p = {two_of_e4m3<false>(lo), two_of_e4m3<true>(lo), two_of_e4m3<false>(hi),
+                                         two_of_e4m3<true>(hi)};
 #pragma unroll
                         for (int t = 0; t < RT; ++t)
                             sum[t] = mfma_16x16x32(xs[t][j], __builtin_bit_cast(bf16x8, p), j ? sum[t] : base[t]);

@@ -1,7 +1,7 @@
 """Every form of the experts' kernels that the library chooses by size, against
 64 bits under bounds that a wrong result exceeds (test_experts_bounds.py shows
-what they catch), and values at the ends of their ranges: gates far from zero,
-subnormal rows, offsets past 2^31."""
+what they catch), and values at the ends of their ranges: 4-bit sums beside one
+large element, gates far from zero, subnormal rows, offsets past 2^31."""
 
 import numpy as np
 import pytest
@@ -140,6 +140,60 @@ def test_w4_shapes_under_narrow_bounds(name, idx, H, I, E, R, group):
                            act)
             inside(f"expert {e}", whole, lo, hi, r, worst)
     say(f"[experts] w4 narrow {name}: of the bounds {worst}")
+
+
+# ---- 4-bit sums beside a large element ----
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("counts", [[5, 9], [40, 30]], ids=["few", "many"])
+def test_w4_sum_beside_a_large_element(counts, group):
+    """One element is 2^18, its weights are all zero (q = 8), the others are odd integers up to 7.  Every product and
+    every partial sum, in any order, is an integer below 15 * 2^18 + 128 * 15 * 7 < 2^22, which fp32 holds: a group's
+    sum is exact, and the result is that of the other elements alone, within the roundings of scale, h and y."""
+    H, I = group, 128
+    c = Block(counts, H, I, group)
+    q1, s1, q2, s2 = inputs.w4("dense", c.E, H, I, group, c.gen, "cuda")
+    at = 2 * (H // 4) + 1  # an odd column: the high four bits
+    q1[:, :, at // 2] = (q1[:, :, at // 2] & 15) | 0x80
+    x = (torch.randint(-4, 4, (c.P, H), generator=c.gen, device="cuda") * 2 + 1).to(torch.bfloat16)
+    small = c.w4(x, (q1, s1, q2, s2), group)
+    x[:, at] = 2.0 ** 18
+    ye = c.w4(x, (q1, s1, q2, s2), group)
+    assert torch.equal(ye[:c.P], c.w4(x, (q1, s1, q2, s2), group)[:c.P])
+    for e, lo, hi in c.segments():
+        w, _ = eb.w4_weights(q1[e], s1[e], group)
+        # one group: its exact sum times the scale, rounded once; eight waves' sums, seven of them zero, are added
+        r = eb.forward(x[lo:hi].double(), (w, 2 * eb.STEP * w.abs()), eb.w4_weights(q2[e], s2[e], group), 0)
+        exact = x[lo:hi].double() @ w.T
+        r_row = (ye[lo:hi].double() - r["y"]).norm(dim=1) / r["n_y"]
+        say(f"[experts] w4 beside a large element, group {group}, expert {e}: {float(r_row.max()):.3g} of the row bound, "
+            f"sums up to {float(exact.abs().max()):.3g}")
+        assert bool((r_row <= 1).all())
+    # the large element has no weight: the result is what it is without it (its place held an odd integer of no weight)
+    assert torch.equal(ye[:c.P], small[:c.P])
+
+
+@pytest.mark.parametrize("counts", [[5, 9], [40, 30]], ids=["few", "many"])
+def test_w4_of_large_finite_rows(counts):
+    """Elements of 2^122 with weights of 1 to 7 steps of 2^-124 (q 9 to 15): g and u are of order 1, and 15 * 2^122 is
+    inside fp32."""
+    H, I, group = 256, 128, 64
+    c = Block(counts, H, I, 3)
+    q1, s1, q2, s2 = inputs.w4("dense", c.E, H, I, group, c.gen, "cuda")
+    q1 |= 0x88
+    q1 = torch.where((q1 & 15) == 8, q1 + 1, q1)
+    q1 = torch.where((q1 >> 4) == 8, q1 + 16, q1)
+    s1 = torch.full_like(s1, 2.0 ** -124)
+    x = torch.zeros((c.P, H), dtype=torch.bfloat16, device="cuda")
+    # one element a group; the fourth group has none
+    for i in range(3):
+        x[torch.arange(c.P, device="cuda"), 64 * i + (torch.arange(c.P, device="cuda") * 7 + 3 * i) % 64] = 2.0 ** 122
+    ye = c.w4(x, (q1, s1, q2, s2), group)
+    worst = [0.0, 0.0]
+    for e, lo, hi in c.segments():
+        r = eb.forward(x[lo:hi].double(), eb.w4_weights(q1[e], s1[e], group), eb.w4_weights(q2[e], s2[e], group), 0)
+        inside(f"expert {e}", ye, lo, hi, r, worst)
+    say(f"[experts] w4 of large rows: of the bounds {worst}")
 
 
 # ---- gates far from zero ----

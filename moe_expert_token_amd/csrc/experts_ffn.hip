@@ -311,7 +311,7 @@ __device__ __forceinline__ void dh_rows(const ExpertShape& S, char* lds, const A
                 const float d = acc[M0 + i][n][j], s = gate_sigmoid(g[j], S.c0, S.c1, &slope), a = g[j] * s;
                 vh[j] = a * u[j];
                 vu[j] = d * a;
-                vg[j] = d * u[j] * fmaf(a * (1.0f - s), slope, s);
+                vg[j] = d * (u[j] * fmaf(a * (1.0f - s), slope, s));  // a closed gate's 0 meets u first: d u may overflow
             }
             const int c = feature_of(n) + 4 * (lane >> 4);
             *(u32x2*)WideStage::at(lds, row, 2 * c) = pack4(vg);

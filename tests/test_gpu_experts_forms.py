@@ -223,6 +223,28 @@ def test_far_gates(rows, act):
             assert a <= 1 and size <= 1, (e, n, a, size)
 
 
+@pytest.mark.parametrize("act", [0, 1], ids=["silu", "gelu"])
+@pytest.mark.parametrize("rows", [40, 90], ids=["small-tiles", "tiles"])
+def test_closed_gates_stop_large_gradients(rows, act):
+    """dh and u are 2^70 each, so dh u passes fp32's range; where the gate is closed (g = -200, act' = 0) dg is 0 all
+    the same, and where it is open (g = 200) and u is 2^-70, dg = dh u is 1."""
+    H, I = 64, 32
+    c = Case(inputs.ids([rows]), H, I, 1, 1, seed=rows)
+    g = torch.where(torch.rand((rows, I), device="cuda", generator=c.gen) < 0.5, -200.0, 200.0)
+    u = torch.where(g < 0, 2.0 ** 70, 2.0 ** -70)
+    saved = torch.cat((g, u), 1).to(torch.bfloat16)
+    c.gy.zero_()
+    c.gy[:, :I] = 1.0
+    c.w2.zero_()
+    c.w2[0, :I] = torch.eye(I, device="cuda").to(torch.bfloat16) * 2.0 ** 70  # dh = gy Wd = 2^70
+    c.xe.zero_()
+    c.xe[torch.arange(rows), torch.arange(rows) % H] = 1.0
+    got = c.backward(saved, None, act, want=("grad_w_gate_up",))["grad_w_gate_up"][0]
+    want = torch.zeros((I, H), dtype=torch.float64, device="cuda")
+    want.index_add_(1, torch.arange(rows, device="cuda") % H, (g > 0).double().T)
+    assert torch.equal(got[:I].double(), want)  # small whole numbers: exact
+
+
 # ---- subnormal rows ----
 
 def test_pack8_of_subnormals_that_round_to_one_step():

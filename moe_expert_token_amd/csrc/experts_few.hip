@@ -440,8 +440,9 @@ bool scales_fit(int K)
 template <int Group, bool Up, bool Few, int Ways>
 hipError_t launch_w4_ways(const ExpertShape& S, const FewArgs& A, hipStream_t s)
 {
-    return A.K % kChunk ? launch<Group, Up, Few, Ways, false, true>(S, A, s)
-                        : launch<Group, Up, Few, Ways, true, true>(S, A, s);
+    if constexpr (Group % kChunk != 0)  // K is a multiple of the group
+        if (A.K % kChunk) return launch<Group, Up, Few, Ways, false, true>(S, A, s);
+    return launch<Group, Up, Few, Ways, true, true>(S, A, s);
 }
 
 // Few ways over k leave more features to a block, which then share its rows' loads; many ways fit longer rows of

@@ -26,7 +26,11 @@
  *   w_down    [E][H][I]   Wd
  *
  * Every sum is held in fp32 and rounded once.  Results depend on the inputs
- * alone: no atomics, and an expert's result does not depend on the others.
+ * alone: no atomics.  With the same dims and inter, a row's result depends on
+ * that row and its expert's weights only, wherever the row lies and whatever
+ * the other rows are.  The dims choose the kernel's form, and with it the order
+ * in which a sum's terms are added: another number of tokens may round a row's
+ * result differently.  A sigmoid below 2^-126 may be taken as 0.
  *
  * On a plan with bad top-k ids every call writes nothing, as the calls of
  * moe_shuffle.h do.  With T = 0 forward calls write nothing and return

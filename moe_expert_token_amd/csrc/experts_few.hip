@@ -284,6 +284,7 @@ struct FewArgs {
     int across;            // blocks over N
 };
 
+// h is rounded because it is an operand of the next product (bf16 matrix instructions), y because it is a bf16 output.
 __device__ __forceinline__ unsigned short bf16_of(float v) { return (unsigned short)bf16_pack2(v, v); }
 
 // Keeps a row's pre-activation of feature n, the gate's (side 0) or the up projection's; 32 neighbouring lanes hold
@@ -459,8 +460,9 @@ hipError_t launch_w4_rows(const ExpertShape& S, const FewArgs& A, hipStream_t s)
 template <int Group, bool Up>
 hipError_t launch_w4_group(const ExpertShape& S, const FewArgs& A, hipStream_t s)
 {
-    // 12: at 16 rows on average half of the experts have a second tile of 16 (77 and 87 us in larger tiles, 89 and 77 in
-    // these, for 32 experts of 2048 x 2048 and 8 of 4096 x 4096)
+    // Tiles of 16 rows against higher ones, us, groups of 128, for 32 experts of 2048 x 2048, 8 of 4096 x 4096 and 64 of
+    // 1024 x 2048: 8 rows on average 52 / 53, 50 / 63, 55 / 60; 12 rows 77 / 62, 54 / 69, 76 / 69; 16 rows 88 / 69, 75 / 82,
+    // 85 / 76.  More experts, more of them with a second tile of 16: 12 lies between.
     return few_each(S, 12) ? launch_w4_rows<Group, Up, true>(S, A, s) : launch_w4_rows<Group, Up, false>(S, A, s);
 }
 
@@ -480,9 +482,10 @@ hipError_t launch_bf16(const ExpertShape& S, const FewArgs& A, hipStream_t s)
 
 }  // namespace
 
-// Up to 8 rows on average the streams win (at 8: 175 us against 206, 8 experts of 4096 x 4096; 181 against 214, 32 of
-// 2048 x 2048); at 16, where many experts have more than a tile of 16, the tiles of experts_ffn do (215 against 207, 225
-// against 213).
+// The streams against the tiles of experts_ffn, us, for 32 experts of 2048 x 2048, 8 of 4096 x 4096 and 64 of 1024 x
+// 2048: 8 rows on average 173 / 200, 171 / 203, 160 / 159; 10 rows 174 / 199, 172 / 203, 203 / 160; 12 rows 227 / 200,
+// 173 / 203, 206 / 161; 16 rows 216 / 199, 209 / 203, 214 / 162.  The host knows the mean alone: all of 80 tokens on one
+// of 8 experts of 4096 x 4096 take 101 us in streams, which read its weights five times, and 75 in tiles.
 bool ffn_is_few(const ExpertShape& S) { return few_each(S, 10); }
 
 hipError_t launch_few_up(const ExpertShape& S, const void* xe, const void* w_gate_up, void* h, SavedActs saved,

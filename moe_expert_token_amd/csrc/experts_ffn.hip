@@ -103,7 +103,8 @@ __device__ __forceinline__ void row_slots(KContiguous& r, const char* first, int
 
 // ---- the kernels ----
 // The accumulators go to memory through LDS, packed to bf16, so that whole rows of a tile are written (256 or 512
-// contiguous bytes a row) rather than the 8 bytes a lane holds.
+// contiguous bytes a row) rather than the 8 bytes a lane holds.  h, dg and du are rounded to bf16 there because they are
+// operands of the next products, whose matrix instructions take bf16; y and the gradients because they are bf16 outputs.
 
 // Largest magnitude over the 32 features that the four lanes of a row hold in a and b; infinity if any is not
 // finite.  Features past the width (`past`) count as zero.
@@ -122,9 +123,12 @@ __device__ __forceinline__ float group_top(f32x4 a, f32x4 b, bool past_a, bool p
     return fmaxf(top, __shfl_xor(top, 32, kWave));
 }
 
-// Rows an expert has on average, up to which tiles of 64 rows with two blocks a CU win: forward and backward pass, 32
-// experts of 2048 x 2048, 48 rows each on average, 650 us against 675; 48 experts of 1160 x 520 with uneven rows, 49 on
-// average, 209 against 254 (the sum of the kernels).  At 64 half of the experts have a second such tile (739 against 704).
+// Rows an expert has on average, up to which tiles of 64 rows with two blocks a CU are taken.  Forward and backward pass
+// in such tiles against higher ones, us, for 32 experts of 2048 x 2048, 8 of 4096 x 4096 and 48 of 1160 x 520:
+//   even routing          40 rows  642 / 666, 725 / 728, 172 / 174    56 rows  738 / 682, 734 / 749, 214 / 187
+//   popular experts       40 rows  677 / 775, 718 / 763, 200 / 244    56 rows  692 / 807, 689 / 796, 211 / 258
+// From 48 rows on some of evenly loaded experts have a second tile, but with popular experts (Zipf, 1.2) the low tiles
+// still win at 64 (707 / 791, 690 / 821, 221 / 271).  The host knows the mean alone; 56 lies between.
 constexpr int kSmallRows = 56;
 constexpr int kCUs = 256;
 constexpr int kUpFeatures = kTileFeatures / 2;  // of h: each of them takes a gate and an up feature

@@ -1,5 +1,6 @@
 // experts_w4.hip -- the making of 4-bit weights: step = max |w| / 7 of a group, rounded to bf16, q = rne(w / step) + 8.
-// Done once for a set of weights; not timed.
+// Done once for a set of weights.  Bound by its access: a lane reads a whole group, so a wave's loads lie a group apart.
+// 8 experts' [8192][4096]: 245 us with groups of 32 (2.8 TB/s), 1454 with groups of 128 (0.46 TB/s).
 #include "experts.h"
 
 namespace ms {

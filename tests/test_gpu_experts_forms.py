@@ -298,6 +298,45 @@ def test_subnormal_rows_with_4_bit_weights(counts):
         inside(f"expert {e}", ye, lo, hi, r, [0.0, 0.0])
 
 
+# ---- a row's own result ----
+
+@pytest.mark.parametrize("T", [8, 120, 400], ids=["streams", "small-tiles", "tiles"])
+def test_a_row_depends_on_itself_and_its_experts_weights(T):
+    """The same row as expert 0's only one, as one in the middle and as its last of T: the same bits in ye, in what is
+    saved, in grad_xe and with 4-bit weights (the number of tokens and experts is the same, so is the form)."""
+    H, I, E = 328, 200, 4
+    row = grad = weights = None
+    seen = []
+    for counts in ([1, T - 3, 1, 1], [T // 2 + 1, 0, T - T // 2 - 1, 0], [T, 0, 0, 0]):
+        c = Case(inputs.ids(counts), H, I, E, 2, seed=sum(counts[:2]))
+        if row is None:
+            row, grad, weights = c.xe[0].clone(), c.gy[0].clone(), (c.w1, c.w2)
+        at = {1: 0, T: T - 1}.get(counts[0], T // 4)
+        c.xe[at], c.gy[at], (c.w1, c.w2) = row, grad, weights
+        ye, saved, scale = c.forward(1, "int8")
+        got = c.backward(saved, scale, 1, want=("grad_xe",))["grad_xe"]
+        seen.append([t[at].clone() for t in (ye, saved, scale, got)])
+    for other in seen[1:]:
+        for a, b in zip(seen[0], other):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("T", [8, 120], ids=["few", "many"])
+def test_a_row_with_4_bit_weights_depends_on_itself(T):
+    H, I, group = 544, 256, 32
+    row = weights = None
+    seen = []
+    for counts in ([1, T - 3, 1, 1], [T // 2 + 1, 0, T - T // 2 - 1, 0], [T, 0, 0, 0]):
+        c = Block(counts, H, I, 4)
+        x = inputs.rows("dense", T, H, I, c.gen, "cuda")
+        if row is None:
+            row, weights = x[0].clone(), inputs.w4("dense", 4, H, I, group, c.gen, "cuda")
+        at = {1: 0, T: T - 1}.get(counts[0], T // 4)
+        x[at] = row
+        seen.append(c.w4(x, weights, group)[at].clone())
+    assert torch.equal(seen[0], seen[1]) and torch.equal(seen[0], seen[2])
+
+
 # ---- offsets past 2^31 bytes ----
 
 @pytest.mark.parametrize("rows", [3, 20, 70], ids=["streams", "small-tiles", "tiles"])

@@ -26,10 +26,14 @@
 // (two v_permlane32_swap, two v_permlane16_swap) deals them out so that each
 // matrix instruction covers 32 neighbouring k, and so one group.
 //
-// Kernel times: four tokens that hit 5 bf16 experts of 4096 x 14336, 199 + 141
-// us (1.76 GB, 5.2 TB/s); 4-bit weights in groups of 128, 256 experts of 7168 x 2048, one token 25
-// + 16 us (182 MB of weights, 4.4 TB/s).  With 4-bit weights and 48 tokens the
-// matrix pipes are 15 % busy and waves wait 45 % of their cycles.
+// Kernel times: four tokens that hit 5 bf16 experts of 4096 x 14336, 197 + 140
+// us (1.76 GB, 5.2 TB/s); 4-bit weights in groups of 128, 256 experts of 7168 x
+// 2048, one token 25 + 16 us (182 MB of weights, 4.4 TB/s); 48 tokens 633 + 311
+// us (4.7 GB, 5.0 TB/s), the matrix pipes 16 % busy, waves waiting for data 45 %
+// of their cycles.  With 203 tokens on 8 experts of 4096 x 14336, groups of 32,
+// weights are read about once (0.58 and 0.36 GB) and the memory is not the
+// limit: two waves a SIMD wait 47 % of their cycles for an instruction to issue
+// and 27 % for data.
 #include <type_traits>
 
 #include "experts.h"

@@ -7,10 +7,11 @@
 //   ffn_wgrad   [dg du]^T x and grad_y^T h
 //
 // Bound by the matrix pipes with hundreds of rows an expert, by the weights' bytes below.  On the Mixtral-like batch
-// (8 experts, 1024 rows each, 4096 x 14336) and on 32 experts of 7168 x 2048 with 1024 rows: up 1.15 and 1.21
-// PFLOP/s, down 1.15 and 1.12, grad_x 1.11 and 1.15, dh 0.84 and 0.93, weight gradients 1.00 and 1.02; one large
+// (8 experts, 1024 rows each, 4096 x 14336) and on 32 experts of 7168 x 2048 with 1024 rows: up 1.15 and 1.20
+// PFLOP/s, down 1.17 and 1.12, grad_x 1.14 and 1.17, dh 0.86 and 0.95, weight gradients 1.02 and 1.02; one large
 // library product reaches 1.57 (k-contiguous operands) and 1.30-1.36 (one k-strided).  dh has the lowest rate: its
-// epilogue also moves g, u, dg, du and h, 1.2 GB in bf16 on the Mixtral-like batch, 0.18 ms at the rate of a copy.
+// epilogue also moves g, u, dg, du and h, 1.2 GB in bf16 on the Mixtral-like batch.  At the rate of a copy that is 0.18 of
+// the 0.28 ms by which it is slower than the other products; the rest is not explained (waves wait 37 % of their cycles).
 #include <math.h>
 
 #include <type_traits>

@@ -125,7 +125,7 @@ def moe_experts_ffn_forward(plan: Plan, xe, w_gate_up, w_down, ye, workspace, sa
             _at(f, "w_down", w_down, (E, H, inter), 2), inter, int(act), _at(f, "ye", ye, (P, H), 2), held, scale, ws,
             ws_bytes)
     _on_gpu(f, stream, xe=xe, w_gate_up=w_gate_up, w_down=w_down, ye=ye, saved=saved, saved_scale=saved_scale,
-            workspace=workspace)
+            workspace=workspace, plan=plan.workspace)
     _check(f, _load().moe_experts_ffn_forward(plan.handle, *args, _stream(stream)))
 
 
@@ -142,7 +142,7 @@ def moe_experts_ffn_backward(plan: Plan, grad_ye, xe, w_gate_up, w_down, saved, 
             _at(f, "grad_w_gate_up", grad_w_gate_up, up, 2), _at(f, "grad_w_down", grad_w_down, down, 2), ws, ws_bytes)
     _on_gpu(f, stream, grad_ye=grad_ye, xe=xe, w_gate_up=w_gate_up, w_down=w_down, saved=saved,
             saved_scale=saved_scale, grad_xe=grad_xe, grad_w_gate_up=grad_w_gate_up, grad_w_down=grad_w_down,
-            workspace=workspace)
+            workspace=workspace, plan=plan.workspace)
     _check(f, _load().moe_experts_ffn_backward(plan.handle, *args, _stream(stream)))
 
 
@@ -159,7 +159,7 @@ def moe_experts_ffn_w4_forward(plan: Plan, xe, q_gate_up, s_gate_up, q_down, s_d
             _at(f, "q_down", q_down, (E, H, inter // 2), 1), _at(f, "s_down", s_down, (E, H, inter // group), 2), inter,
             int(group), int(act), _at(f, "ye", ye, (P, H), 2), ws, ws_bytes)
     _on_gpu(f, stream, xe=xe, q_gate_up=q_gate_up, s_gate_up=s_gate_up, q_down=q_down, s_down=s_down, ye=ye,
-            workspace=workspace)
+            workspace=workspace, plan=plan.workspace)
     _check(f, _load().moe_experts_ffn_w4_forward(plan.handle, *args, _stream(stream)))
 
 

@@ -45,6 +45,42 @@ def calls(ms):
     }
 
 
+class Elsewhere:
+    """What a tensor on another GPU says of itself."""
+    is_cuda, device = True, "cuda:1"
+
+    def get_device(self):
+        return 1
+
+
+class Stream:
+    device_index = 0
+
+
+def test_tensors_and_plans_of_another_device_are_refused():
+    ms = _ms()
+    from moe_expert_token_amd import experts
+    with pytest.raises(ms.MoeShuffleError) as e:
+        experts._on_gpu("f", Stream(), xe=None, ye=Elsewhere())
+    assert e.value.code == ms.E_INVALID_ARG and "ye" in str(e.value) and "cuda:1" in str(e.value)
+    stream = Stream()
+    stream.device_index = 1
+    experts._on_gpu("f", stream, ye=Elsewhere(), none=None)  # the stream's device, whatever the current one is
+
+
+@pytest.mark.parametrize("name", ["forward", "backward", "w4"])
+def test_the_plans_workspace_is_held_to_the_same_device(name, monkeypatch):
+    ms = _ms()
+    from moe_expert_token_amd import experts
+    seen = {}
+    monkeypatch.setattr(experts, "_on_gpu", lambda func, stream, **tensors: seen.update(tensors))
+    monkeypatch.setattr(experts, "_stream", lambda stream: None)
+    f, args = calls(ms)[name]
+    args["plan"].workspace = torch.empty(8, dtype=torch.uint8)
+    refusal(ms, f, args)  # by the library: the handle is null
+    assert any(t is args["plan"].workspace for t in seen.values())
+
+
 NAMES = ["forward", "backward", "w4", "quantize", "pack", "unpack"]
 
 

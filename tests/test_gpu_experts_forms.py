@@ -173,21 +173,22 @@ def test_w4_sum_beside_a_large_element(counts, group):
     assert torch.equal(ye[:c.P], small[:c.P])
 
 
+@pytest.mark.parametrize("top", [122, 124])
 @pytest.mark.parametrize("counts", [[5, 9], [40, 30]], ids=["few", "many"])
-def test_w4_of_large_finite_rows(counts):
-    """Elements of 2^122 with weights of 1 to 7 steps of 2^-124 (q 9 to 15): g and u are of order 1, and 15 * 2^122 is
-    inside fp32."""
+def test_w4_of_large_finite_rows(counts, top):
+    """Elements of 2^top with weights of 1 to 7 steps of 2^-(top + 2) (q 9 to 15): g and u are of order 1, and 15 * 2^top
+    is inside fp32, for 124 just so (2^128 / 15 is 1.07 * 2^124)."""
     H, I, group = 256, 128, 64
     c = Block(counts, H, I, 3)
     q1, s1, q2, s2 = inputs.w4("dense", c.E, H, I, group, c.gen, "cuda")
     q1 |= 0x88
     q1 = torch.where((q1 & 15) == 8, q1 + 1, q1)
     q1 = torch.where((q1 >> 4) == 8, q1 + 16, q1)
-    s1 = torch.full_like(s1, 2.0 ** -124)
+    s1 = torch.full_like(s1, 2.0 ** -(top + 2))
     x = torch.zeros((c.P, H), dtype=torch.bfloat16, device="cuda")
     # one element a group; the fourth group has none
     for i in range(3):
-        x[torch.arange(c.P, device="cuda"), 64 * i + (torch.arange(c.P, device="cuda") * 7 + 3 * i) % 64] = 2.0 ** 122
+        x[torch.arange(c.P, device="cuda"), 64 * i + (torch.arange(c.P, device="cuda") * 7 + 3 * i) % 64] = 2.0 ** top
     ye = c.w4(x, (q1, s1, q2, s2), group)
     worst = [0.0, 0.0]
     for e, lo, hi in c.segments():

@@ -23,3 +23,6 @@ from .experts import (  # noqa: F401
     moe_experts_ffn_w4_forward, moe_experts_ffn_workspace_size, moe_experts_pack8, moe_experts_unpack8,
     moe_experts_w4_quantize,
 )
+from .optim import (  # noqa: F401
+    GROUP_STATE, OPTIM_EXPORTS, AdamwTensors, moe_adamw_pack, moe_adamw_step, moe_adamw_unpack,
+)

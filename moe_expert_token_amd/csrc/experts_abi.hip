@@ -2,40 +2,19 @@
 // checks, workspace layout and launches.
 #include <hip/hip_runtime.h>
 
-#include <initializer_list>
-
+#include "checks.h"
 #include "experts.h"
-#include "internal.h"
 
 namespace {
 
+using ms::Span;
+using ms::align256;
+using ms::misaligned;
+using ms::overlaps;
+using ms::status_of;
+
 constexpr int kTileRoom = 1024;
 constexpr int kMaxWidth = 1 << 20;  // H and I below this: offsets inside a tile stay below 2^31
-
-bool misaligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) != 0; }
-size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
-
-struct Span {
-    const void* p;
-    size_t bytes;
-};
-
-// Whether any of `outs` overlaps another of them or any of `ins`.
-bool overlaps(std::initializer_list<Span> outs, std::initializer_list<Span> ins)
-{
-    const auto hit = [](const Span& a, const Span& b) {
-        if (!a.p || !b.p || !a.bytes || !b.bytes) return false;
-        const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
-        return x < y + b.bytes && y < x + a.bytes;
-    };
-    for (auto o = outs.begin(); o != outs.end(); ++o) {
-        for (auto q = o + 1; q != outs.end(); ++q)
-            if (hit(*o, *q)) return true;
-        for (const Span& i : ins)
-            if (hit(*o, i)) return true;
-    }
-    return false;
-}
 
 int check_inter(const moe_shuffle_dims& d, int32_t inter)
 {
@@ -93,8 +72,6 @@ size_t scale_bytes(const ms::ExpertShape& S) { return (size_t)S.P * 2 * ((S.I + 
 
 // The plan's own workspace, which nothing may write.
 Span plan_span(moe_shuffle_plan_t plan) { return Span{plan->ws, plan->L.total}; }
-
-int status_of(hipError_t e) { return e == hipSuccess ? MOE_SHUFFLE_OK : ms::hip_fail(e); }
 
 }  // namespace
 

@@ -23,6 +23,10 @@ from .experts import (  # noqa: F401
     moe_experts_ffn_w4_forward, moe_experts_ffn_workspace_size, moe_experts_pack8, moe_experts_unpack8,
     moe_experts_w4_quantize,
 )
+from .layer import (  # noqa: F401
+    LAYER_EXPORTS, LAYER_MAX_PAIRS, LAYER_MAX_TOKENS, SCORE_SIGMOID, SCORE_SOFTMAX, RouterRule, moe_layer_forward,
+    moe_layer_w4_forward, moe_layer_workspace_size,
+)
 from .optim import (  # noqa: F401
     GROUP_STATE, OPTIM_EXPORTS, AdamwTensors, moe_adamw_pack, moe_adamw_step, moe_adamw_unpack,
 )

@@ -1,0 +1,137 @@
+// layer.h -- what the router's and the layer's files share (library-internal;
+// the ABI is include/moe_layer.h): the routing rule, keys in 64 bits, and the
+// choice of the largest by one wave.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "experts.h"
+#include "moe_layer.h"
+
+namespace ms {
+
+constexpr int kLayerTokens = MOE_LAYER_MAX_TOKENS, kLayerPairs = MOE_LAYER_MAX_PAIRS;
+
+struct Rule {
+    int sigmoid, normalize;
+    float scale;
+    const float* bias;  // [E], sigmoid only
+};
+
+struct RouterShape {
+    int T, H, E, k;
+};
+
+// A layer's call, and where its workspace keeps what.
+struct LayerShape {
+    int T, H, E, k, I, P;    // P = T k
+    float c0, c1;            // the gate's sigmoid argument: c0 g + c1 g^3
+    unsigned long long* key;  // [T][E], ordered_key of each expert's key
+    float* logit;             // [T][E]
+    unsigned long long* tokens;  // [E] bit t: token t goes to this expert
+    int* first;               // [E] the first row of an expert, rows in the order of experts, then tokens
+    int* tile;                // [<= P] expert | part << 16
+    int* tiles;               // [1] how many
+    int* row_of;              // [P] the row of (token, slot)
+    float* gate;              // [P]
+    int* arrived;             // [ceil(H / 64)]
+    char* h;                  // [P][I] bf16
+    float* y;                 // [P][H]
+};
+
+size_t layer_workspace(LayerShape* S, char* base);
+
+struct LayerCall {
+    const void *x, *w_router, *up, *up_scale, *down, *down_scale, *residual;
+    void* out;
+    int32_t* topk_idx;
+    float* topk_w;
+    int group;  // 0: bf16 weights
+};
+
+hipError_t launch_layer(const LayerShape& S, const Rule& rule, const LayerCall& C, hipStream_t s);
+
+size_t router_workspace(const RouterShape& S, bool backward);
+hipError_t launch_router_forward(const RouterShape& S, const Rule& rule, const void* x, const void* w, int32_t* idx,
+                                 float* gate, float* logits, char* ws, hipStream_t s);
+hipError_t launch_router_backward(const RouterShape& S, const Rule& rule, const float* grad_gate, const float* logits,
+                                  const int32_t* idx, const void* x, const void* w, const float* grad_logits,
+                                  const void* grad_x_in, void* grad_x, void* grad_w, char* ws, hipStream_t s);
+
+// ---- device helpers ----
+
+// Keys as unsigned numbers of the same order; NaN as minus infinity, -0 as 0.  All are above 0, which stands for none.
+__device__ __forceinline__ unsigned long long ordered_key(double v)
+{
+    if (v != v) v = -__builtin_inf();
+    v += 0.0;
+    const unsigned long long u = (unsigned long long)__double_as_longlong(v);
+    return u >> 63 ? ~u : u | 1ull << 63;
+}
+
+__device__ __forceinline__ double score64(double l) { return 1.0 / (1.0 + exp(-l)); }
+
+template <int Ctrl, int Rows>
+__device__ __forceinline__ unsigned dpp_max(unsigned v)
+{
+    return max(v, (unsigned)__builtin_amdgcn_update_dpp(0, (int)v, Ctrl, Rows, 0xf, false));
+}
+
+// The largest of the wave's values (the same in every lane): within sixteens, then across them, without LDS.
+__device__ __forceinline__ unsigned wave_max(unsigned v)
+{
+    v = dpp_max<0x111, 0xf>(v);  // row_shr 1, 2, 4, 8: lane 15 of each row has the row's
+    v = dpp_max<0x112, 0xf>(v);
+    v = dpp_max<0x114, 0xf>(v);
+    v = dpp_max<0x118, 0xf>(v);
+    v = dpp_max<0x142, 0xa>(v);  // row_bcast 15 and 31
+    v = dpp_max<0x143, 0xc>(v);
+    return (unsigned)__builtin_amdgcn_readlane((int)v, 63);
+}
+
+__device__ __forceinline__ float wave_max(float v)
+{
+#pragma unroll
+    for (int d = 1; d < kWave; d <<= 1) v = fmaxf(v, __shfl_xor(v, d, kWave));
+    return v;
+}
+
+__device__ __forceinline__ float wave_total(float v)
+{
+#pragma unroll
+    for (int d = 1; d < kWave; d <<= 1) v += __shfl_xor(v, d, kWave);
+    return v;
+}
+
+// The place of the wave's largest of `key` (one a lane, with its index `at`); of equal ones the lowest index.
+__device__ __forceinline__ int wave_argmax(unsigned long long key, int at)
+{
+    const unsigned hi = (unsigned)(key >> 32), lo = (unsigned)key;
+    const unsigned top = wave_max(hi);
+    unsigned long long m = __ballot(hi == top);
+    if ((m & (m - 1)) == 0) return __builtin_amdgcn_readlane(at, __builtin_ctzll(m));
+    const unsigned low = wave_max(hi == top ? lo : 0u);
+    const bool one = hi == top && lo == low;
+    m = __ballot(one);
+    if ((m & (m - 1)) == 0) return __builtin_amdgcn_readlane(at, __builtin_ctzll(m));
+    return (int)~wave_max(one ? ~(unsigned)at : 0u);
+}
+
+// exp(v) for v <= 0, by the hardware's exponential.
+__device__ __forceinline__ float exp_of(float v) { return __builtin_amdgcn_exp2f(1.442695041f * v); }
+
+// The gates of a token: lane j < k has the logit l of slot j; `most` is the row's largest logit and `all` the sum of
+// exp(logit - most) over the row, which softmax without normalization needs.
+__device__ __forceinline__ float gate_of(const Rule& rule, int k, float l, float most, float all)
+{
+    const bool in = lane_id() < k;
+    float s;
+    if (rule.sigmoid) s = 1.0f / (1.0f + expf(-l));
+    else s = expf(l - most) / (rule.normalize ? 1.0f : all);
+    if (!in) s = 0.0f;
+    if (rule.normalize) s = s / (wave_total(s) + 1e-20f);
+    return rule.scale * s;
+}
+
+}  // namespace ms

@@ -1,0 +1,63 @@
+"""The routing rule and the layer in 64 bits, with bounds of each result (CPU
+or GPU tensors; test infrastructure)."""
+
+from __future__ import annotations
+
+import torch
+
+import experts_bounds as bounds
+from experts_ref import TINY, U
+
+STEP = 2.0 ** -24  # half an fp32 step, relative
+
+
+def logits(x, w):
+    return x.double() @ w.double().T
+
+
+def scores(l, sigmoid: bool):
+    if sigmoid:
+        return 1 / (1 + torch.exp(-l))
+    e = torch.exp(l - l.amax(1, keepdim=True))
+    return e / e.sum(1, keepdim=True)
+
+
+def choose(l, k: int, sigmoid: bool, bias=None):
+    """Ids by falling key, ties to the lowest index, NaN as minus infinity."""
+    key = l if bias is None else scores(l, True) + bias.double()
+    key = torch.where(key.isnan(), -torch.inf, key)
+    return torch.sort(key, dim=1, descending=True, stable=True).indices[:, :k]
+
+
+def gates(l, idx, sigmoid: bool, normalize: bool, scale: float):
+    """Gates of chosen experts, and a bound of the fp32 ones' relative error: a logit rounds once (worth |l| STEP of its
+    exponential, and the largest's as much), the difference once more, the exponential 2 STEP, a sum over E and one
+    over k (their terms' errors, and a step for each addition in a tree of the wave), and six more roundings."""
+    s = scores(l, sigmoid).gather(1, idx)
+    w = s / (s.sum(1, keepdim=True) + 1e-20) if normalize else s
+    most = l.abs().amax(1, keepdim=True).clamp(max=1e4)
+    return scale * w, (8 * most + 2 * (6 + l.shape[1] / 64) + 24) * STEP
+
+
+def layer(x, idx, w, rel, up, down, act, residual=None):
+    """The layer's output and element bounds.  up(e), down(e): an expert's weights as pairs (value, error matrix) of
+    experts_bounds; idx, w, rel: ids, gates and their relative error."""
+    T, k = idx.shape
+    H = x.shape[1]
+    y = torch.zeros((T, k, H), dtype=torch.float64, device=x.device)
+    ey = torch.zeros_like(y)
+    for e in sorted(set(idx.flatten().tolist())):
+        t, j = (idx == e).nonzero(as_tuple=True)
+        r = bounds.forward(x[t].double(), up(e), down(e), act)
+        y[t, j] = r["y"]
+        # the bound there counts y's rounding to bf16, which is left out here
+        ey[t, j] = ((r["e_y"] - TINY) - U * r["y"].abs()) / (1 + U) + TINY
+    terms = w[:, :, None] * y
+    out = terms.sum(1)
+    err = (w.abs()[:, :, None] * (1 + rel[:, :, None]) * ey).sum(1) + (rel[:, :, None] * terms.abs()).sum(1)
+    size = terms.abs().sum(1)
+    if residual is not None:
+        out = out + residual.double()
+        size = size + residual.double().abs()
+    err = err + (k + 1) * STEP * (size + err)
+    return out, err + U * (out.abs() + err) + TINY

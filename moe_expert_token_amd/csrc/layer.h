@@ -104,6 +104,17 @@ __device__ __forceinline__ float wave_total(float v)
     return v;
 }
 
+// Inclusive scan over the wave, likewise.
+__device__ __forceinline__ int wave_scan(int v)
+{
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);
+    return v + __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);
+}
+
 // The place of the wave's largest of `key` (one a lane, with its index `at`); of equal ones the lowest index.
 __device__ __forceinline__ int wave_argmax(unsigned long long key, int at)
 {
@@ -117,9 +128,6 @@ __device__ __forceinline__ int wave_argmax(unsigned long long key, int at)
     if ((m & (m - 1)) == 0) return __builtin_amdgcn_readlane(at, __builtin_ctzll(m));
     return (int)~wave_max(one ? ~(unsigned)at : 0u);
 }
-
-// exp(v) for v <= 0, by the hardware's exponential.
-__device__ __forceinline__ float exp_of(float v) { return __builtin_amdgcn_exp2f(1.442695041f * v); }
 
 // The gates of a token: lane j < k has the logit l of slot j; `most` is the row's largest logit and `all` the sum of
 // exp(logit - most) over the row, which softmax without normalization needs.

@@ -23,53 +23,85 @@ namespace {
 
 using namespace stream;
 
-constexpr int kScoreThreads = 256;
-constexpr int kScoreTokens = 8;  // of a block
-
 __device__ __forceinline__ double as_double(unsigned bits) { return (double)__uint_as_float(bits); }
 
-// One expert a block, up to eight tokens; the four waves share H.
-__global__ __launch_bounds__(kScoreThreads) void layer_scores_kernel(LayerShape S, Rule rule, const u32x4* x,
+// The wave's sums of N values a lane (a power of two, up to 32): each exchange halves the values that a lane is left
+// with, so that N + 5 or so of them do it and not 6 N.  Leaves one sum; returns which.
+template <int N, int D = kWave / 2>
+__device__ __forceinline__ int wave_sums(double (&v)[N], double* sum)
+{
+    if constexpr (N == 1) {
+        *sum = v[0];
+#pragma unroll
+        for (int d = D; d > 0; d >>= 1) *sum += __shfl_xor(*sum, d, kWave);
+        return 0;
+    } else {
+        const bool upper = lane_id() & D;
+        double half[N / 2];
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+            const double keep = upper ? v[i + N / 2] : v[i], give = upper ? v[i] : v[i + N / 2];
+            half[i] = keep + __shfl_xor(give, D, kWave);
+        }
+        return (upper ? N / 2 : 0) + wave_sums<N / 2, D / 2>(half, sum);
+    }
+}
+
+// Experts [Experts blockIdx.x, ...) and Tokens tokens a block; its waves share H.  What a number costs is its way
+// to 64 bits, so with many tokens four experts share it (48 tokens, 256 experts, H = 7168: see the file's head).
+template <int Tokens, int Experts, int Threads>
+__global__ __launch_bounds__(Threads) void layer_scores_kernel(LayerShape S, Rule rule, const u32x4* x,
                                                                      const u32x4* w, int columns)
 {
-    __shared__ double part[kScoreThreads / kWave][kScoreTokens];
-    const int e = blockIdx.x, t0 = blockIdx.y * kScoreTokens, n = min(kScoreTokens, S.T - t0), V = S.H / 8;
-    if (e == 0 && t0 == 0)
-        for (int i = threadIdx.x; i < columns; i += kScoreThreads) S.arrived[i] = 0;
-    double sum[kScoreTokens] = {};
-    for (int v = threadIdx.x; v < V; v += kScoreThreads) {
-        const u32x4 a = w[(int64_t)e * V + v];
-        double wd[8];
+    constexpr int kParts = Threads / kWave, kSums = Tokens * Experts;
+    __shared__ double part[kParts][kSums];
+    const int e0 = blockIdx.x * Experts, t0 = blockIdx.y * Tokens, V = S.H / 8;
+    if (e0 == 0 && t0 == 0)
+        for (int i = threadIdx.x; i < columns; i += Threads) S.arrived[i] = 0;
+    double sum[kSums] = {};  // [Experts][Tokens]
+#pragma unroll 1
+    for (int v = threadIdx.x; v < V; v += Threads) {
+        u32x4 a[Experts], b[Tokens];  // tokens and experts past the last repeat it
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            wd[2 * c] = as_double(a[c] << 16);
-            wd[2 * c + 1] = as_double(a[c] & 0xffff0000u);
-        }
+        for (int i = 0; i < Experts; ++i) a[i] = w[(int64_t)min(e0 + i, S.E - 1) * V + v];
 #pragma unroll
-        for (int t = 0; t < kScoreTokens; ++t) {
-            if (t >= n) break;
-            const u32x4 b = x[(int64_t)(t0 + t) * V + v];
+        for (int t = 0; t < Tokens; ++t) b[t] = x[(int64_t)min(t0 + t, S.T - 1) * V + v];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                sum[t] = fma(wd[2 * c], as_double(b[c] << 16), sum[t]);
-                sum[t] = fma(wd[2 * c + 1], as_double(b[c] & 0xffff0000u), sum[t]);
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                double wd[Experts];
+#pragma unroll
+                for (int i = 0; i < Experts; ++i) wd[i] = as_double(h ? a[i][c] & 0xffff0000u : a[i][c] << 16);
+#pragma unroll
+                for (int t = 0; t < Tokens; ++t) {
+                    const double xd = as_double(h ? b[t][c] & 0xffff0000u : b[t][c] << 16);
+#pragma unroll
+                    for (int i = 0; i < Experts; ++i) sum[i * Tokens + t] = fma(wd[i], xd, sum[i * Tokens + t]);
+                }
             }
-        }
     }
-#pragma unroll
-    for (int t = 0; t < kScoreTokens; ++t) {
-        if (t >= n) break;
-#pragma unroll
-        for (int d = 1; d < kWave; d <<= 1) sum[t] += __shfl_xor(sum[t], d, kWave);
-        if (lane_id() == 0) part[wave_id()][t] = sum[t];
-    }
+    double mine;
+    const int which = wave_sums(sum, &mine);
+    if ((lane_id() & (kWave / kSums - 1)) == 0) part[wave_id()][which] = mine;
     __syncthreads();
-    if ((int)threadIdx.x >= n) return;
-    const int t = threadIdx.x;
-    const double l = (part[0][t] + part[1][t]) + (part[2][t] + part[3][t]);
-    const int64_t at = (int64_t)(t0 + t) * S.E + e;
+    const int t = t0 + (int)threadIdx.x % Tokens, e = e0 + (int)threadIdx.x / Tokens;
+    if ((int)threadIdx.x >= kSums || t >= S.T || e >= S.E) return;
+    double l = 0;
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) l += part[i][threadIdx.x];
+    const int64_t at = (int64_t)t * S.E + e;
     S.logit[at] = (float)l;
     S.key[at] = ordered_key(rule.bias ? score64(l) + (double)rule.bias[e] : l);
+}
+
+template <int Tokens, int Experts, int Threads>
+hipError_t launch_scores(const LayerShape& S, const Rule& rule, const LayerCall& C, hipStream_t s)
+{
+    const dim3 grid((S.E + Experts - 1) / Experts, (S.T + Tokens - 1) / Tokens);
+    layer_scores_kernel<Tokens, Experts, Threads><<<grid, Threads, 0, s>>>(S, rule, (const u32x4*)C.x,
+                                                                           (const u32x4*)C.w_router, (S.H + 63) / 64);
+    return hipGetLastError();
 }
 
 // How a block's eight waves share its work, as stream::Split, for tiles of Rows rows.
@@ -94,46 +126,64 @@ struct Choice {
     int tiles;
 };
 
-// Chooses the experts of all tokens and lists the tiles of up to `rows` rows.  The keys of a wave's token are kept in
-// `keys` (E of them a wave).  The first block writes the choice down for the kernel that follows and for the user.
-__device__ __forceinline__ void choose(const LayerShape& S, const Rule& rule, int rows, unsigned long long* keys,
-                                       Choice& C, int32_t* topk_idx, float* topk_w)
+// The k largest of a token's E keys, by one wave with Each keys a lane: its bit in the experts' words, and lane j's
+// expert of slot j.
+template <int Each>
+__device__ __forceinline__ int choose_token(const LayerShape& S, int t, Choice& C)
+{
+    const int lane = lane_id();
+    unsigned long long key[Each];
+#pragma unroll
+    for (int i = 0; i < Each; ++i) {
+        const int e = lane + i * kWave;
+        key[i] = e < S.E ? S.key[(int64_t)t * S.E + e] : 0;
+    }
+    int chosen = 0;
+    for (int j = 0; j < S.k; ++j) {
+        unsigned long long best = key[0];
+        int at = lane;
+#pragma unroll
+        for (int i = 1; i < Each; ++i)
+            if (key[i] > best) { best = key[i]; at = lane + i * kWave; }
+        const int e = wave_argmax(best, at);
+        if (lane == j) chosen = e;
+#pragma unroll
+        for (int i = 0; i < Each; ++i)
+            if (lane + i * kWave == e) key[i] = 0;
+        if (lane == 0) atomicOr(&C.tokens[e], 1ull << t);
+    }
+    return chosen;
+}
+
+// Chooses the experts of all tokens and lists the tiles of up to `rows` rows.  The first block writes the choice down,
+// for the kernel that follows and for the user.  (A block more that does nothing else is a round more where the others
+// fill the card: 37.5 us against 31.8, one token, 256 4-bit experts of 7168 x 2048.)
+__device__ __forceinline__ void choose(const LayerShape& S, const Rule& rule, int rows, Choice& C, int32_t* topk_idx,
+                                       float* topk_w)
 {
     const int lane = lane_id(), wave = wave_id(), E = S.E, k = S.k;
     const bool write = blockIdx.x == 0;
     for (int e = threadIdx.x; e < E; e += kThreads) C.tokens[e] = 0;
     __syncthreads();
-    unsigned long long* const mine = keys + wave * E;
     for (int t = wave; t < S.T; t += kWaves) {
-        for (int e = lane; e < E; e += kWave) mine[e] = S.key[(int64_t)t * E + e];
+        const int chosen = E <= 64 ? choose_token<1>(S, t, C) : E <= 256 ? choose_token<4>(S, t, C) : choose_token<16>(S, t, C);
+        if (!write) continue;
+        const float* const l = S.logit + (int64_t)t * E;
         float most = -__builtin_inff(), all = 0;
-        if (!rule.sigmoid && write) {
-            for (int e = lane; e < E; e += kWave) most = fmaxf(most, S.logit[(int64_t)t * E + e]);
+        if (!rule.sigmoid) {
+            for (int e = lane; e < E; e += kWave) most = fmaxf(most, l[e]);
             most = wave_max(most);
             if (!rule.normalize) {
-                for (int e = lane; e < E; e += kWave) all += expf(S.logit[(int64_t)t * E + e] - most);
+                for (int e = lane; e < E; e += kWave) all += expf(l[e] - most);
                 all = wave_total(all);
             }
         }
-        int chosen = 0;  // lane j's: slot j's expert
-        for (int j = 0; j < k; ++j) {
-            unsigned long long best = 0;
-            int at = E;
-            for (int e = lane; e < E; e += kWave)
-                if (mine[e] > best) { best = mine[e]; at = e; }
-            const int e = wave_argmax(best, at);
-            if (lane == j) chosen = e;
-            if (lane == (e & (kWave - 1))) mine[e] = 0;
-            if (lane == 0) atomicOr(&C.tokens[e], 1ull << t);
-        }
-        if (write) {
-            const float w = gate_of(rule, k, S.logit[(int64_t)t * E + chosen], most, all);
-            if (lane < k) {
-                S.gate[t * k + lane] = w;
-                if (topk_idx) topk_idx[t * k + lane] = chosen;
-                if (topk_w) topk_w[t * k + lane] = w;
-                S.row_of[t * k + lane] = chosen;  // its row, once the first rows are known
-            }
+        const float w = gate_of(rule, k, l[chosen], most, all);
+        if (lane < k) {
+            S.gate[t * k + lane] = w;
+            if (topk_idx) topk_idx[t * k + lane] = chosen;
+            if (topk_w) topk_w[t * k + lane] = w;
+            S.row_of[t * k + lane] = chosen;  // its row, once the first rows are known
         }
     }
     __syncthreads();
@@ -145,7 +195,7 @@ __device__ __forceinline__ void choose(const LayerShape& S, const Rule& rule, in
         count[i] = n | (n + rows - 1) / rows << 16;
         sum += count[i];
     }
-    const int upto = wave_inclusive_scan(sum);
+    const int upto = wave_scan(sum);
     if (lane == kWave - 1) C.wave_sum[wave] = upto;
     __syncthreads();
     int before = upto - sum, total = 0;
@@ -188,14 +238,14 @@ __device__ __forceinline__ int tile_rows(unsigned long long tokens, int rows, in
 }
 
 template <int Group, int Rows, int Ways, bool Whole, bool Staged>
-__global__ __launch_bounds__(kThreads) void layer_up_kernel(LayerShape S, Rule rule, const char* x, Weights A,
+__global__ __launch_bounds__(kThreads, Rows == 16 ? 4 : 2) void layer_up_kernel(LayerShape S, Rule rule, const char* x, Weights A,
                                                             int32_t* topk_idx, float* topk_w)
 {
     typedef LayerSplit<Rows, Ways> P;
     constexpr int kOut = 32;  // output features of a wave
-    __shared__ __align__(16) char lds[P::kStage];
+    __shared__ __align__(16) char lds[Staged ? P::kStage : P::kSums];
     __shared__ Choice C;
-    choose(S, rule, Rows, (unsigned long long*)lds, C, topk_idx, topk_w);
+    choose(S, rule, Rows, C, topk_idx, topk_w);
     const int ks = wave_id() % P::KS, fs = wave_id() / P::KS, K = S.H, N = S.I;
     const int items = C.tiles * A.across;
     for (int item = blockIdx.x; item < items; item += gridDim.x) {
@@ -243,16 +293,34 @@ __global__ __launch_bounds__(kThreads) void layer_up_kernel(LayerShape S, Rule r
     }
 }
 
+// y goes to memory and comes from there, not from an L2 that is one of eight (sc1, agent scope): so a block's y is there
+// for every other one as soon as its stores are done, which a wait for them shows.  Fences would do the same by writing
+// back and dropping the whole L2, for each tile (890 us against 311 without any, 48 tokens, 256 experts of 2048 to 7168).
+constexpr int kAgent = 16;
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_of(const float* y, int64_t bytes)
+{
+    const uint64_t a = (uint64_t)y;
+    const uint64_t p = (unsigned)__builtin_amdgcn_readfirstlane((int)a) |
+                       (uint64_t)(unsigned)__builtin_amdgcn_readfirstlane((int)(a >> 32)) << 32;
+    return __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, __builtin_amdgcn_readfirstlane((int)(unsigned)bytes),
+                                             0x00020000);
+}
+
 // Columns [n0, n0 + width) of out: the rows' y, weighted and added in the order of the slots.
-__device__ __forceinline__ void combine(const LayerShape& S, const void* residual, void* out, int n0, int width)
+__device__ __forceinline__ void combine(const LayerShape& S, const int* row_of, const float* gate, const void* residual,
+                                        void* out, int n0, int width)
 {
     const int quads = (min(width, S.H - n0) + 3) / 4;
+    const __amdgpu_buffer_rsrc_t rows = rows_of(S.y, (int64_t)S.P * S.H * 4);
     for (int i = threadIdx.x; i < S.T * quads; i += kThreads) {
         const int t = i / quads, n = n0 + 4 * (i - t * quads);
         f32x4 sum = {0, 0, 0, 0};
+#pragma unroll 8
         for (int j = 0; j < S.k; ++j) {
-            const float w = S.gate[t * S.k + j];
-            const f32x4 y = *(const f32x4*)(S.y + (int64_t)S.row_of[t * S.k + j] * S.H + n);
+            const float w = gate[t * S.k + j];
+            const unsigned at = ((unsigned)row_of[t * S.k + j] * S.H + n) * 4;
+            const f32x4 y = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rows, at, 0, kAgent));
 #pragma unroll
             for (int c = 0; c < 4; ++c) sum[c] = fmaf(w, y[c], sum[c]);
         }
@@ -269,12 +337,17 @@ __device__ __forceinline__ void combine(const LayerShape& S, const void* residua
 }
 
 template <int Group, int Rows, int Ways, bool Whole, bool Staged>
-__global__ __launch_bounds__(kThreads) void layer_down_kernel(LayerShape S, Weights A, const void* residual, void* out)
+__global__ __launch_bounds__(kThreads, Rows == 16 ? 4 : 2) void layer_down_kernel(LayerShape S, Weights A, const void* residual, void* out)
 {
     typedef LayerSplit<Rows, Ways> P;
     constexpr int kOut = 64;
     __shared__ __align__(16) char lds[Staged ? P::kStage : P::kSums];
-    __shared__ int last;
+    __shared__ int last, row_of[kLayerPairs];
+    __shared__ float gate[kLayerPairs];
+    for (int p = threadIdx.x; p < S.P; p += kThreads) {  // a barrier comes before they are read
+        row_of[p] = S.row_of[p];
+        gate[p] = S.gate[p];
+    }
     const int ks = wave_id() % P::KS, fs = wave_id() / P::KS, K = S.I, N = S.H;
     const int tiles = *S.tiles, items = tiles * A.across;
     for (int item = blockIdx.x; item < items; item += gridDim.x) {
@@ -295,23 +368,22 @@ __global__ __launch_bounds__(kThreads) void layer_down_kernel(LayerShape S, Weig
         if constexpr (Staged) stage_scales<P>(lds, from, ks, fs);
         const auto run = [&](auto tiles) {
             const auto total = sum_up<Group, P, decltype(tiles)::value, Whole, Staged>(lds, from, ks, fs);
+            const __amdgpu_buffer_rsrc_t rows = rows_of(S.y + row0 * N, (int64_t)nr * N * 4);
             for (int i = ks * kWave + lane_id(); i < nr * kOut; i += P::KS * kWave) {
                 const int r = i / kOut, f = i % kOut, n = n0 + f;
                 const float v = total(f >> 4, r, f);
-                if (n < N) S.y[(row0 + r) * N + n] = v;
+                if (n < N) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), rows, (r * N + n) * 4, 0, kAgent);
             }
         };
         if (Rows == 16 || nr <= 16) run(std::integral_constant<int, 1>());
         else run(std::integral_constant<int, 2>());
-        // this block's y before its arrival; the last to arrive sees them all
-        __threadfence();
+        // every wave's y is in memory before the block's arrival; the last to arrive finds them all there
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         __syncthreads();
-        if (threadIdx.x == 0) last = atomicAdd(S.arrived + place, 1) == tiles - 1;
+        if (threadIdx.x == 0)
+            last = __hip_atomic_fetch_add(S.arrived + place, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == tiles - 1;
         __syncthreads();
-        if (last) {
-            __threadfence();
-            combine(S, residual, out, place * P::FS * kOut, P::FS * kOut);
-        }
+        if (last) combine(S, row_of, gate, residual, out, place * P::FS * kOut, P::FS * kOut);
     }
 }
 
@@ -323,7 +395,8 @@ hipError_t launch_up(const LayerShape& S, const Rule& rule, const LayerCall& C, 
     constexpr int kOut = 32 * LayerSplit<Rows, Ways>::FS;
     const Weights A{(const char*)C.up, (const char*)C.up_scale, (S.I + kOut - 1) / kOut};
     const int64_t items = (int64_t)((S.P < S.E ? S.P : S.E) + S.P / Rows) * A.across;
-    layer_up_kernel<Group, Rows, Ways, Whole, Staged><<<(int)(items < kResident ? items : kResident), kThreads, 0, s>>>(
+    const int grid = (int)(items < kResident ? items : kResident);
+    layer_up_kernel<Group, Rows, Ways, Whole, Staged><<<grid, kThreads, 0, s>>>(
         S, rule, (const char*)C.x, A, C.topk_idx, C.topk_w);
     return hipGetLastError();
 }
@@ -401,9 +474,9 @@ size_t layer_workspace(LayerShape* S, char* base)
 
 hipError_t launch_layer(const LayerShape& S, const Rule& rule, const LayerCall& C, hipStream_t s)
 {
-    layer_scores_kernel<<<dim3(S.E, (S.T + kScoreTokens - 1) / kScoreTokens), kScoreThreads, 0, s>>>(
-        S, rule, (const u32x4*)C.x, (const u32x4*)C.w_router, (S.H + 63) / 64);
-    const hipError_t e = hipGetLastError();
+    const hipError_t e = S.T == 1 ? launch_scores<1, 1, 1024>(S, rule, C, s)
+                         : S.T <= 4 ? launch_scores<4, 1, 512>(S, rule, C, s)
+                                    : launch_scores<8, 4, 512>(S, rule, C, s);
     if (e != hipSuccess) return e;
     switch (C.group) {
         case 32: return launch_rows<32>(S, rule, C, s);

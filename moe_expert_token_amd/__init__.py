@@ -25,7 +25,8 @@ from .experts import (  # noqa: F401
 )
 from .layer import (  # noqa: F401
     LAYER_EXPORTS, LAYER_MAX_PAIRS, LAYER_MAX_TOKENS, SCORE_SIGMOID, SCORE_SOFTMAX, RouterRule, moe_layer_forward,
-    moe_layer_w4_forward, moe_layer_workspace_size,
+    moe_layer_w4_forward, moe_layer_workspace_size, moe_router_backward, moe_router_forward,
+    moe_router_workspace_size,
 )
 from .optim import (  # noqa: F401
     GROUP_STATE, OPTIM_EXPORTS, AdamwTensors, moe_adamw_pack, moe_adamw_step, moe_adamw_unpack,

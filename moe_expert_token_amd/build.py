@@ -17,7 +17,7 @@ LIB = os.path.join(PKG, "libmoe_shuffle.so")
 SOURCES = [os.path.join(CSRC, f) for f in ("abi.hip", "plan.hip", "rows.hip", "reduce.hip", "combine_bwd.hip", "copy_ref.hip",
                                                "experts_abi.hip", "experts_ffn.hip", "experts_few.hip",
                                                "experts_w4.hip", "experts_pack.hip", "optim.hip", "layer_abi.hip",
-                                               "layer.hip")]
+                                               "layer.hip", "router.hip")]
 ARCH = os.environ.get("MOE_SHUFFLE_ARCH", "gfx950")
 
 HIPCC_FLAGS = [

@@ -204,9 +204,17 @@ __device__ __forceinline__ int row_of(int m)
 }
 __device__ __forceinline__ int feature_of(int n) { return (n >> 1) * 128 + 32 * (wave_id() & 3) + 16 * (n & 1); }
 
-// The tile's product.  `lds`: Lds<Small>::kBytes.  Ends with a barrier: LDS is free.
-template <bool Small, int MF, class R, class F>
-__device__ __forceinline__ void tile_product(const R& r, const F& f, int K, char* lds, Acc<MF>& acc)
+// What a product shows of its operands on the way: nothing.
+struct Unseen {
+    template <int N>
+    __device__ __forceinline__ void rows(int, int, const bf16x8 (&)[N][2]) const {}
+    __device__ __forceinline__ void features(int, const bf16x8 (&)[2][2], const bf16x8 (&)[2][2]) const {}
+};
+
+// The tile's product.  `lds`: Lds<Small>::kBytes.  Ends with a barrier: LDS is free.  `see` is shown each tile of k's
+// fragments, rows(kt, first row fragment, ...) and features(kt, F0's, F1's), once they are in registers.
+template <bool Small, int MF, class R, class F, class See = Unseen>
+__device__ __forceinline__ void tile_product(const R& r, const F& f, int K, char* lds, Acc<MF>& acc, See&& see = See())
 {
     constexpr int A = low_rows(MF), B = MF - A;  // row fragments of a wave in R0 and R1
     constexpr int kTile = Lds<Small>::kTile, kFeatures = Lds<Small>::kFeatures;
@@ -266,8 +274,11 @@ __device__ __forceinline__ void tile_product(const R& r, const F& f, int K, char
               [&] { load_f(0, kt + 2); }, MS_INT(2 * a + b + 6));
         phase(MS_INT(A), MS_INT(0), MS_INT(1), r0, f1, MS_INT(2 * B), [&](int i) { read_r1(kt, i); },
               [&] { load_f(1, kt + 2); }, MS_INT(a + b + 8));
+        see.rows(kt, 0, r0);
+        see.features(kt, f0, f1);
         phase(MS_INT(B), MS_INT(A), MS_INT(1), r1, f1, MS_INT(2 * A), [&](int i) { read_r0(kt + 1, i); },
               [&] { load_r(1, kt + 2); }, MS_INT(a + 2 * b + 6));
+        if constexpr (B > 0) see.rows(kt, A, r1);
         phase(MS_INT(B), MS_INT(A), MS_INT(0), r1, f0, MS_INT(4), [&](int i) { read_f(f1, 0, kt + 1, i); },
               [&] { load_r(0, kt + 3); }, MS_INT(2 * a + 2 * b + 4));
     };

@@ -81,9 +81,96 @@ int layer(const moe_shuffle_dims* dims, const moe_router_rule* rule, int32_t int
     return status_of(ms::launch_layer(S, q, C, (hipStream_t)stream));
 }
 
+int check_router(const moe_shuffle_dims* d, bool backward)
+{
+    const int rc = ms::check_dims(d);
+    if (rc) return rc;
+    const int64_t T = d->num_tokens, lim = (int64_t)1 << 40;
+    if (d->hidden >= kMaxWidth || T * d->num_experts >= lim || T * d->hidden >= lim || (backward && T >= 1 << 30))
+        return MOE_SHUFFLE_E_OVERFLOW;
+    return MOE_SHUFFLE_OK;
+}
+
+ms::RouterShape router_shape(const moe_shuffle_dims& d)
+{
+    return ms::RouterShape{d.num_tokens, d.hidden, d.num_experts, d.top_k};
+}
+
+int check_workspace(const void* workspace, size_t bytes, size_t need)
+{
+    if (!workspace) return MOE_SHUFFLE_E_INVALID_ARG;
+    if (misaligned(workspace, 256)) return MOE_SHUFFLE_E_ALIGN;
+    return bytes < need ? MOE_SHUFFLE_E_WORKSPACE : MOE_SHUFFLE_OK;
+}
+
 }  // namespace
 
 extern "C" {
+
+int moe_router_workspace_size(const moe_shuffle_dims* dims, int32_t backward, size_t* bytes)
+{
+    const int rc = check_router(dims, backward != 0);
+    if (rc) return rc;
+    if (!bytes) return MOE_SHUFFLE_E_INVALID_ARG;
+    *bytes = ms::router_workspace(router_shape(*dims), backward != 0);
+    return MOE_SHUFFLE_OK;
+}
+
+int moe_router_forward(const moe_shuffle_dims* dims, const moe_router_rule* rule, const void* x, const void* w_router,
+                       int32_t* topk_idx, float* topk_w, float* logits, void* workspace, size_t workspace_bytes,
+                       void* stream)
+{
+    int rc = check_router(dims, false);
+    ms::Rule q;
+    if (!rc) rc = check_rule(rule, &q);
+    if (rc) return rc;
+    const ms::RouterShape S = router_shape(*dims);
+    if (S.T == 0) return MOE_SHUFFLE_OK;
+    if (!x || !w_router || !topk_idx || !topk_w) return MOE_SHUFFLE_E_INVALID_ARG;
+    if (misaligned(x, 16) || misaligned(w_router, 16) || misaligned(topk_idx, 4) || misaligned(topk_w, 4) ||
+        misaligned(logits, 4))
+        return MOE_SHUFFLE_E_ALIGN;
+    const size_t need = ms::router_workspace(S, false), pairs = (size_t)S.T * S.k * 4;
+    rc = check_workspace(workspace, workspace_bytes, need);
+    if (rc) return rc;
+    if (overlaps({{topk_idx, pairs}, {topk_w, pairs}, {logits, (size_t)S.T * S.E * 4}, {workspace, need}},
+                 {{x, (size_t)S.T * S.H * 2}, {w_router, (size_t)S.E * S.H * 2}, {q.bias, (size_t)S.E * 4}}))
+        return MOE_SHUFFLE_E_INVALID_ARG;
+    return status_of(ms::launch_router_forward(S, q, x, w_router, topk_idx, topk_w, logits, (char*)workspace,
+                                               (hipStream_t)stream));
+}
+
+int moe_router_backward(const moe_shuffle_dims* dims, const moe_router_rule* rule, const float* grad_topk_w,
+                        const float* logits, const int32_t* topk_idx, const void* x, const void* w_router,
+                        const float* grad_logits, const void* grad_x_in, void* grad_x, void* grad_w_router,
+                        void* workspace, size_t workspace_bytes, void* stream)
+{
+    int rc = check_router(dims, true);
+    ms::Rule q;
+    if (!rc) rc = check_rule(rule, &q);
+    if (rc) return rc;
+    const ms::RouterShape S = router_shape(*dims);
+    // with no rows only the (zero) weights' gradient is written, and nothing is read
+    if (S.T > 0 && (!grad_topk_w || !logits || !topk_idx || (grad_x && !w_router) || (grad_w_router && !x)))
+        return MOE_SHUFFLE_E_INVALID_ARG;
+    if (grad_x_in && !grad_x) return MOE_SHUFFLE_E_INVALID_ARG;
+    if (misaligned(x, 16) || misaligned(w_router, 16) || misaligned(grad_x_in, 16) || misaligned(grad_x, 16) ||
+        misaligned(grad_w_router, 16) || misaligned(grad_topk_w, 4) || misaligned(logits, 4) ||
+        misaligned(topk_idx, 4) || misaligned(grad_logits, 4))
+        return MOE_SHUFFLE_E_ALIGN;
+    const size_t need = ms::router_workspace(S, true), pairs = (size_t)S.T * S.k * 4;
+    rc = check_workspace(workspace, workspace_bytes, need);
+    if (rc) return rc;
+    const size_t rows = (size_t)S.T * S.H * 2, weights = (size_t)S.E * S.H * 2, table = (size_t)S.T * S.E * 4;
+    if (overlaps({{grad_x, rows}, {grad_w_router, weights}, {workspace, need}},
+                 {{x, rows}, {w_router, weights}, {grad_topk_w, pairs}, {logits, table}, {topk_idx, pairs},
+                  {grad_logits, table}, {grad_x_in == grad_x ? nullptr : grad_x_in, rows}}))
+        return MOE_SHUFFLE_E_INVALID_ARG;
+    if (!grad_x && !grad_w_router) return MOE_SHUFFLE_OK;
+    return status_of(ms::launch_router_backward(S, q, grad_topk_w, logits, topk_idx, x, w_router, grad_logits,
+                                                grad_x_in, grad_x, grad_w_router, (char*)workspace,
+                                                (hipStream_t)stream));
+}
 
 int moe_layer_workspace_size(const moe_shuffle_dims* dims, int32_t inter, size_t* bytes)
 {

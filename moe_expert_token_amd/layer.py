@@ -17,7 +17,8 @@ SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 LAYER_MAX_TOKENS, LAYER_MAX_PAIRS = 64, 512
 
 # Every function moe_layer.h declares.
-LAYER_EXPORTS = ("moe_layer_workspace_size", "moe_layer_forward", "moe_layer_w4_forward")
+LAYER_EXPORTS = ("moe_router_workspace_size", "moe_router_forward", "moe_router_backward", "moe_layer_workspace_size",
+                 "moe_layer_forward", "moe_layer_w4_forward")
 
 _vp, _i32, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
 
@@ -27,6 +28,9 @@ class _Rule(ctypes.Structure):
 
 
 _SIGNATURES = {
+    "moe_router_workspace_size": [ctypes.POINTER(Dims), _i32, ctypes.POINTER(_sz)],
+    "moe_router_forward": [ctypes.POINTER(Dims), ctypes.POINTER(_Rule), _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp],
+    "moe_router_backward": [ctypes.POINTER(Dims), ctypes.POINTER(_Rule)] + [_vp] * 10 + [_sz, _vp],
     "moe_layer_workspace_size": [ctypes.POINTER(Dims), _i32, ctypes.POINTER(_sz)],
     "moe_layer_forward": [ctypes.POINTER(Dims), ctypes.POINTER(_Rule), _vp, _vp, _vp, _vp, _i32, _i32, _vp, _vp, _vp,
                           _vp, _vp, _sz, _vp],
@@ -79,6 +83,45 @@ def _ids(func: str, t, shape):
 def _bias(func: str, rule: RouterRule, E: int):
     if rule.bias is not None and (rule.bias.numel() != E or not rule.bias.is_contiguous()):
         _refuse(func, f"the rule's bias must be contiguous [{E}], not {list(rule.bias.shape)}")
+
+
+def moe_router_workspace_size(dims: Dims, backward: bool = False) -> int:
+    n = _sz(0)
+    _check("moe_router_workspace_size",
+           _load().moe_router_workspace_size(ctypes.byref(dims), int(bool(backward)), ctypes.byref(n)))
+    return n.value
+
+
+def moe_router_forward(dims: Dims, rule: RouterRule, x, w_router, topk_idx, topk_w, workspace, logits=None, stream=None):
+    """Ids and gates of the rows x by the rule; `logits` (fp32 [T, E]) receives what moe_router_backward needs."""
+    f = "moe_router_forward"
+    T, H, E, k = dims.num_tokens, dims.hidden, dims.num_experts, dims.top_k
+    _bias(f, rule, E)
+    ws, ws_bytes = _workspace(f, workspace)
+    args = (_at(f, "x", x, (T, H), 2), _at(f, "w_router", w_router, (E, H), 2), _ids(f, topk_idx, (T, k)),
+            _f32(f, "topk_w", topk_w, (T, k)), _f32(f, "logits", logits, (T, E)))
+    _on_gpu(f, stream, x=x, w_router=w_router, topk_idx=topk_idx, topk_w=topk_w, logits=logits, workspace=workspace,
+            bias=rule.bias)
+    _check(f, _load().moe_router_forward(ctypes.byref(dims), ctypes.byref(rule.struct), *args, ws, ws_bytes,
+                                         _stream(stream)))
+
+
+def moe_router_backward(dims: Dims, rule: RouterRule, grad_topk_w, logits, topk_idx, x, w_router, grad_x,
+                        grad_w_router, workspace, grad_x_in=None, grad_logits=None, stream=None):
+    """Gradients of rows and router's weights from the gates' (and, with grad_logits, the logits' own); grad_x_in, which
+    may be grad_x, is added to grad_x.  Each of grad_x and grad_w_router may be None."""
+    f = "moe_router_backward"
+    T, H, E, k = dims.num_tokens, dims.hidden, dims.num_experts, dims.top_k
+    ws, ws_bytes = _workspace(f, workspace)
+    args = (_f32(f, "grad_topk_w", grad_topk_w, (T, k)), _f32(f, "logits", logits, (T, E)), _ids(f, topk_idx, (T, k)),
+            _at(f, "x", x, (T, H), 2), _at(f, "w_router", w_router, (E, H), 2),
+            _f32(f, "grad_logits", grad_logits, (T, E)), _at(f, "grad_x_in", grad_x_in, (T, H), 2),
+            _at(f, "grad_x", grad_x, (T, H), 2), _at(f, "grad_w_router", grad_w_router, (E, H), 2))
+    _on_gpu(f, stream, grad_topk_w=grad_topk_w, logits=logits, topk_idx=topk_idx, x=x, w_router=w_router,
+            grad_logits=grad_logits, grad_x_in=grad_x_in, grad_x=grad_x, grad_w_router=grad_w_router,
+            workspace=workspace)
+    _check(f, _load().moe_router_backward(ctypes.byref(dims), ctypes.byref(rule.struct), *args, ws, ws_bytes,
+                                          _stream(stream)))
 
 
 def moe_layer_workspace_size(dims: Dims, inter: int) -> int:

@@ -61,3 +61,39 @@ def layer(x, idx, w, rel, up, down, act, residual=None):
         size = size + residual.double().abs()
     err = err + (k + 1) * STEP * (size + err)
     return out, err + U * (out.abs() + err) + TINY
+
+
+def score_gradient(l, idx, grad, sigmoid: bool, normalize: bool, scale: float):
+    """dl, and a bound of the error of one computed in fp32 from the same logits.
+
+    A score's relative error: the logit's difference to the largest rounds (|l| STEP each), the exponential, the sum over
+    E and the division a few steps more; D and the sum over the k chosen have as much again, and each further product
+    or difference rounds its terms once."""
+    s = scores(l, sigmoid)
+    at, g = s.gather(1, idx), scale * grad.double()
+    size = g.abs()
+    if normalize:
+        total = at.sum(1, keepdim=True) + 1e-20
+        size = (g.abs() + (g.abs() * at).sum(1, keepdim=True) / total) / total
+        g = (g - (g * at).sum(1, keepdim=True) / total) / total
+    wide, wide_size = torch.zeros_like(s).scatter_(1, idx, g), torch.zeros_like(s).scatter_(1, idx, size)
+    rel = (16 * l.abs().amax(1, keepdim=True).clamp(max=1e4) + 4 * (6 + l.shape[1] / 64) + 64) * STEP
+    if sigmoid:
+        # 1 - s loses what s rounds
+        return wide * s * (1 - s), rel * wide_size * s
+    mean, mean_size = (g * at).sum(1, keepdim=True), (size * at).sum(1, keepdim=True)
+    return s * (wide - mean), rel * s * (wide_size + mean_size)
+
+
+def router_backward(x, w, dl, e_dl, grad_x_in=None):
+    """grad_x and grad_w_router of a bf16-rounded dl, with element bounds."""
+    from experts_ref import GAMMA
+    x, w = x.double(), w.double()
+    err = e_dl + U * (dl.abs() + e_dl) + TINY
+    size = dl.abs() + err
+    gx, ex = dl @ w, err @ w.abs() + GAMMA(w.shape[0]) * (size @ w.abs())
+    if grad_x_in is not None:
+        gx = gx + grad_x_in.double()
+        ex = ex + 2 * STEP * (gx.abs() + ex)
+    gw, ew = dl.T @ x, err.T @ x.abs() + GAMMA(x.shape[0] + 32) * (size.T @ x.abs())
+    return gx, ex + U * (gx.abs() + ex) + TINY, gw, ew + U * (gw.abs() + ew) + TINY

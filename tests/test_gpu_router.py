@@ -1,0 +1,367 @@
+"""The router of many rows on the MI355X against its 64-bit definition: sizes
+around each border, ties and near ties, rows that are zero, tiny, huge or not
+finite, the backward pass, graphs, streams, and a training step through it."""
+
+import pytest
+import torch
+
+import layer_ref as ref
+from experts_ref import GAMMA
+
+pytestmark = pytest.mark.gpu
+
+SENTINEL = -12345.0
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import moe_expert_token_amd
+    moe_expert_token_amd.load()
+
+
+def ms():
+    import moe_expert_token_amd
+    return moe_expert_token_amd
+
+
+def bf16(gen, *shape, std=1.0):
+    return torch.empty(shape, dtype=torch.bfloat16, device="cuda").normal_(0, std, generator=gen)
+
+
+def guarded(rows, cols, dtype, value):
+    whole = torch.full((rows + 1, cols), value, dtype=dtype, device="cuda")
+    return whole, whole[:rows]
+
+
+class Router:
+    def __init__(self, T, H, E, k, sigmoid=False, norm=True, bias=False, scale=1.0, seed=0):
+        m = ms()
+        self.T, self.H, self.E, self.k = T, H, E, k
+        self.sigmoid, self.norm, self.scale = sigmoid, norm, scale
+        gen = self.gen = torch.Generator(device="cuda").manual_seed(seed)
+        self.x = bf16(gen, T, H)
+        self.w = bf16(gen, E, H, std=H ** -0.5)
+        self.bias = torch.empty(E, device="cuda").normal_(0, 0.1, generator=gen) if bias else None
+        self.grad = torch.empty(T, k, device="cuda").normal_(0, 1, generator=gen)
+        self.dims = m.dims_of(T, H, E, k, 1)
+        self.ws = torch.empty(m.moe_router_workspace_size(self.dims, True), dtype=torch.uint8, device="cuda")
+        self.ws.fill_(0xff)
+
+    def rule(self):
+        m = ms()
+        return m.RouterRule(m.SCORE_SIGMOID if self.sigmoid else m.SCORE_SOFTMAX, self.norm, self.scale, self.bias)
+
+    def forward(self, logits=True, **kw):
+        self.wholes = [guarded(self.T, self.k, torch.int32, -77), guarded(self.T, self.k, torch.float32, SENTINEL),
+                       guarded(self.T, self.E, torch.float32, SENTINEL)]
+        self.idx, self.gates, self.logits = (t[1] for t in self.wholes)
+        ms().moe_router_forward(self.dims, self.rule(), self.x, self.w, self.idx, self.gates, self.ws,
+                                logits=self.logits if logits else None, **kw)
+        return self
+
+    def guards_hold(self):
+        for whole, _ in self.wholes:
+            assert bool((whole[-1] == (-77 if whole.dtype == torch.int32 else SENTINEL)).all())
+
+    def check(self, rows=None):
+        """The forward call's results (of some rows)."""
+        r = slice(None) if rows is None else rows
+        x, w = self.x[r].double(), self.w.double()
+        l = x @ w.T
+        el = GAMMA(self.H) * (x.abs() @ w.abs().T) + ref.TINY
+        far = (self.logits[r].double() - l).abs()
+        assert bool((far <= el).all()), f"logits: {float((far / el).max()):.3g}"
+        idx = ref.choose(l, self.k, self.sigmoid, self.bias)
+        assert torch.equal(self.idx[r].long(), idx), f"{int((self.idx[r].long() != idx).any(1).sum())} rows' ids"
+        gates, rel = ref.gates(l, idx, self.sigmoid, self.norm, self.scale)
+        rel = rel + 4 * el.amax(1, keepdim=True)
+        off = (self.gates[r].double() - gates).abs()
+        assert bool((off <= rel * gates.abs() + 1e-37).all()), f"gates: {float((off / (rel * gates.abs() + 1e-37)).max())}"
+
+    def backward(self, want=("grad_x", "grad_w"), grad_x_in=None, grad_logits=None, **kw):
+        gx, gw = guarded(self.T, self.H, torch.bfloat16, SENTINEL), guarded(self.E, self.H, torch.bfloat16, SENTINEL)
+        ms().moe_router_backward(self.dims, self.rule(), self.grad, self.logits, self.idx, self.x, self.w,
+                                 gx[1] if "grad_x" in want else None, gw[1] if "grad_w" in want else None, self.ws,
+                                 grad_x_in=grad_x_in, grad_logits=grad_logits, **kw)
+        assert bool((gx[0][-1] == SENTINEL).all()) and bool((gw[0][-1] == SENTINEL).all())
+        for name, t in (("grad_x", gx), ("grad_w", gw)):
+            assert name in want or bool((t[0] == SENTINEL).all())
+        return gx[1], gw[1]
+
+    def check_backward(self, gx, gw, grad_x_in=None, grad_logits=None):
+        dl, e_dl = ref.score_gradient(self.logits.double(), self.idx.long(), self.grad, self.sigmoid, self.norm, self.scale)
+        if grad_logits is not None:
+            dl = dl + grad_logits.double()
+            e_dl = e_dl + ref.STEP * (dl.abs() + grad_logits.double().abs())
+        wx, ex, ww, ew = ref.router_backward(self.x, self.w, dl, e_dl, grad_x_in)
+        for got, want, err, name in ((gx, wx, ex, "grad_x"), (gw, ww, ew, "grad_w")):
+            far = (got.double() - want).abs()
+            assert bool((far <= err).all()), f"{name}: {float((far / err).max()):.3g} of the bound"
+
+
+SHAPES = [  # T, H, E, k
+    (1, 8, 1, 1), (1, 4096, 8, 2), (3, 72, 2, 2), (63, 64, 3, 2), (64, 520, 40, 6), (65, 1544, 64, 8), (200, 136, 65, 5),
+    (257, 2048, 128, 8), (1000, 264, 130, 3), (300, 7168, 256, 8), (129, 512, 257, 8), (70, 520, 1023, 64), (4100, 128, 16, 4),
+]
+RULES = [dict(), dict(sigmoid=True, bias=True, scale=2.5), dict(norm=False, scale=0.5), dict(sigmoid=True, norm=False)]
+NAMES = ["softmax", "bias", "plain", "sigmoid"]
+
+
+@pytest.mark.parametrize("rule", RULES, ids=NAMES)
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "-".join(map(str, s)))
+def test_both_ways(shape, rule):
+    c = Router(*shape, seed=sum(shape), **rule).forward()
+    c.check()
+    c.guards_hold()
+    first = [c.idx.clone(), c.gates.clone()]
+    add = bf16(c.gen, c.T, c.H, std=0.1)
+    extra = torch.empty(c.T, c.E, device="cuda").normal_(0, 0.05, generator=c.gen)
+    gx, gw = c.backward()
+    c.check_backward(gx, gw)
+    gx2, gw2 = c.backward(grad_x_in=add, grad_logits=extra)
+    c.check_backward(gx2, gw2, add, extra)
+    # each alone, and in place: the same bits
+    assert torch.equal(c.backward(want=("grad_x",), grad_x_in=add, grad_logits=extra)[0], gx2)
+    assert torch.equal(c.backward(want=("grad_w",), grad_logits=extra)[1], gw2)
+    same = add.clone()
+    ms().moe_router_backward(c.dims, c.rule(), c.grad, c.logits, c.idx, c.x, c.w, same, None, c.ws, grad_x_in=same,
+                             grad_logits=extra)
+    assert torch.equal(same, gx2)
+    # without logits, and again
+    c.forward(logits=False)
+    assert torch.equal(c.idx, first[0]) and torch.equal(c.gates, first[1])
+    assert bool((c.logits == SENTINEL).all())
+
+
+@pytest.mark.parametrize("rule", RULES[:2], ids=NAMES[:2])
+def test_large_batch(rule):
+    """The DeepSeek-V3-like batch: every row's ids."""
+    c = Router(8192, 7168, 256, 8, seed=1, **rule).forward()
+    for lo in range(0, 8192, 1024):
+        c.check(slice(lo, lo + 1024))
+
+
+def near_ties(c, size):
+    """Rows whose keys differ by little: all experts share a row but for one element, where x is small."""
+    c.w[:] = c.w[:1].clone()
+    n = min(c.E, c.H)
+    c.x[:, :n] = (torch.randn(c.T, n, device="cuda", generator=c.gen) * size).to(torch.bfloat16)
+    at = torch.arange(n)
+    c.w[at, at] = torch.randn(n, device="cuda", generator=c.gen).to(torch.bfloat16)
+
+
+@pytest.mark.parametrize("size", [2.0 ** -6, 2.0 ** -12, 2.0 ** -18])
+@pytest.mark.parametrize("E", [16, 200])
+@pytest.mark.parametrize("rule", [dict(), dict(sigmoid=True, bias=True)], ids=["softmax", "bias"])
+def test_keys_that_nearly_tie(size, E, rule):
+    """From a few that 32 bits cannot order to more of them than a wave's lanes."""
+    c = Router(300, 2048, E, 8, seed=E, **rule)
+    near_ties(c, size)
+    if c.bias is not None:
+        c.bias.normal_(0, size, generator=c.gen)
+    c.forward().check()
+
+
+def test_ids_do_not_depend_on_the_batch():
+    c = Router(2000, 1024, 96, 6, sigmoid=True, bias=True, seed=3)
+    near_ties(c, 2.0 ** -10)
+    c.x[1000:] = bf16(c.gen, 1000, 1024)
+    ids = c.forward().idx.clone()
+    m = ms()
+    for lo, n in ((0, 1), (990, 50), (1990, 10), (500, 700)):
+        d = Router(n, 1024, 96, 6, sigmoid=True, seed=4)
+        d.x, d.w, d.bias = c.x[lo:lo + n].contiguous(), c.w, c.bias
+        assert torch.equal(d.forward().idx, ids[lo:lo + n])
+        if n <= 64:  # and the layer's
+            dims = m.dims_of(n, 1024, 96, 6, 1)
+            ws = torch.empty(m.moe_layer_workspace_size(dims, 8), dtype=torch.uint8, device="cuda")
+            w1, w2 = bf16(c.gen, 96, 16, 1024), bf16(c.gen, 96, 1024, 8)
+            out, idx = torch.empty_like(d.x), torch.empty(n, 6, dtype=torch.int32, device="cuda")
+            m.moe_layer_forward(dims, d.rule(), d.x, c.w, w1, w2, out, ws, topk_idx=idx)
+            assert torch.equal(idx, ids[lo:lo + n])
+
+
+@pytest.mark.parametrize("rule", RULES, ids=NAMES)
+def test_ties_and_zero_rows(rule):
+    c = Router(130, 256, 100, 5, seed=5, **rule)
+    c.w[1::2] = c.w[0::2]  # pairs of equal experts
+    c.x[7] = 0
+    c.x[64:100] = 0
+    c.forward().check()
+    if c.bias is None:
+        assert c.idx[7].tolist() == [0, 1, 2, 3, 4]
+    c.bias = torch.zeros(100, device="cuda") if c.bias is not None else None
+    c.forward().check()
+    c.w.zero_()
+    c.forward().check()
+    gx, gw = c.backward()
+    c.check_backward(gx, gw)
+
+
+@pytest.mark.parametrize("size", [1e-30, 1e-18, 1e15, 1e25])
+def test_rows_of_extreme_size(size):
+    """Norms whose squares leave fp32 (down to products that do not): the choice is still that of exact sums."""
+    c = Router(70, 512, 48, 6, seed=6)
+    c.x[3:40] = (c.x[3:40].float() * size).to(torch.bfloat16)
+    c.forward()
+    l = c.x.double() @ c.w.double().T
+    assert torch.equal(c.idx.long(), ref.choose(l, 6, False))
+
+
+def test_rows_that_are_not_finite():
+    c = Router(100, 256, 20, 4, seed=7)
+    clean = c.forward()
+    ids, gates = clean.idx.clone(), clean.gates.clone()
+    c.x[5, 3] = float("nan")
+    c.x[6, 4] = float("inf")
+    c.forward()
+    others = torch.ones(100, dtype=torch.bool, device="cuda")
+    others[5:7] = False
+    assert torch.equal(c.idx[others], ids[others]) and torch.equal(c.gates[others], gates[others])
+    assert c.idx[5].tolist() == [0, 1, 2, 3]
+    for t in (5, 6):
+        row = c.idx[t].tolist()
+        assert len(set(row)) == 4 and min(row) >= 0 and max(row) < 20
+    # a bias of minus infinity takes an expert out; all but three: the others follow by index
+    s = Router(50, 64, 30, 5, sigmoid=True, bias=True, seed=8)
+    s.bias[:] = float("-inf")
+    s.bias[[4, 9, 17]] = 0.0
+    s.forward()
+    assert bool((s.idx[:, 3:] == torch.tensor([0, 1], device="cuda")).all())
+    assert torch.equal(s.idx.long(), ref.choose(s.x.double() @ s.w.double().T, 5, True, s.bias))
+
+
+def test_bad_ids_touch_nothing_else():
+    c = Router(40, 128, 12, 3, seed=9).forward()
+    good = c.backward()[0].clone()
+    c.idx[7] = torch.tensor([-1, 12, 1 << 30], dtype=torch.int32, device="cuda")
+    gx, gw = c.backward()
+    others = torch.arange(40, device="cuda") != 7
+    assert torch.equal(gx[others], good[others])
+    assert bool((gx[7] == 0).all())  # nothing was chosen
+
+
+def test_no_rows():
+    m = ms()
+    c = Router(4, 64, 8, 2, seed=10)
+    dims = m.dims_of(0, 64, 8, 2, 1)
+    ws = torch.empty(m.moe_router_workspace_size(dims, True), dtype=torch.uint8, device="cuda")
+    i, f, l = (torch.empty(0, n, dtype=d, device="cuda") for n, d in ((2, torch.int32), (2, torch.float32), (8, torch.float32)))
+    m.moe_router_forward(dims, c.rule(), c.x[:0], c.w, i, f, ws, logits=l)
+    gw = torch.full((8, 64), 3.0, dtype=torch.bfloat16, device="cuda")
+    m.moe_router_backward(dims, c.rule(), f, l, i, c.x[:0], c.w, c.x[:0].clone(), gw, ws)
+    assert bool((gw == 0).all())
+
+
+def test_graph_replays():
+    """Forward and backward in one graph, new rows and weights between replays, eager work between them."""
+    c = Router(500, 520, 40, 6, sigmoid=True, bias=True, seed=11)
+    m, rule = ms(), c.rule()
+    out = [torch.empty(500, 6, dtype=torch.int32, device="cuda"), torch.empty(500, 6, device="cuda"),
+           torch.empty(500, 40, device="cuda"), torch.empty_like(c.x), torch.empty_like(c.w)]
+    eager_ws = torch.empty_like(c.ws)
+
+    def go(out, ws):
+        m.moe_router_forward(c.dims, rule, c.x, c.w, out[0], out[1], ws, logits=out[2])
+        m.moe_router_backward(c.dims, rule, c.grad, out[2], out[0], c.x, c.w, out[3], out[4], ws)
+
+    go(out, c.ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        go(out, c.ws)
+    for i in range(5):
+        c.x.normal_(0, 1, generator=c.gen)
+        c.w.normal_(0, 0.05, generator=c.gen)
+        c.bias.normal_(0, 0.1, generator=c.gen)
+        graph.replay()
+        torch.cuda.synchronize()
+        eager = [torch.empty_like(t) for t in out]
+        go(eager, eager_ws)
+        for a, b in zip(out, eager):
+            assert torch.equal(a, b)
+    c.idx, c.gates, c.logits = out[:3]
+    c.check()
+    c.check_backward(out[3], out[4])
+
+
+def test_two_streams_at_once():
+    a, b = Router(700, 1024, 64, 4, seed=12), Router(300, 2048, 128, 8, sigmoid=True, bias=True, seed=13)
+    want = []
+    for c in (a, b):
+        c.forward()
+        want.append([c.idx.clone(), c.gates.clone()] + [t.clone() for t in c.backward()])
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(8):
+        got = []
+        for s in streams:
+            s.wait_stream(torch.cuda.current_stream())
+        for c, s in zip((a, b), streams):
+            with torch.cuda.stream(s):
+                c.forward()
+                got.append([c.idx, c.gates] + list(c.backward()))
+        for s in streams:
+            torch.cuda.current_stream().wait_stream(s)
+        for g, w in zip(got, want):
+            for x, y in zip(g, w):
+                assert torch.equal(x, y)
+
+
+def test_a_training_step():
+    """Router, plan, dispatch, block, combine, and back; the gradients of x and of the router's weights against 64-bit
+    autograd, then AdamW on all weights.  Each path has at most six bf16 roundings of 2^-8 of what they round (xe is
+    exact): a gradient's error is held to 6 2^-8 of its norm."""
+    m = ms()
+    T, H, E, k, R, I = 300, 256, 8, 2, 4, 128
+    c = Router(T, H, E, k, sigmoid=True, bias=True, seed=14)
+    gen = c.gen
+    w1, w2 = bf16(gen, E, 2 * I, H, std=H ** -0.5), bf16(gen, E, H, I, std=I ** -0.5)
+    grad_out = bf16(gen, T, H)
+    dims = m.dims_of(T, H, E, k, R)
+    c.forward()
+    plan_ws = torch.empty(m.moe_shuffle_workspace_size(dims), dtype=torch.uint8, device="cuda")
+    plan = m.moe_shuffle_plan(dims, c.idx, plan_ws)
+    P = T * k
+    rows = {n: torch.empty(P, H, dtype=torch.bfloat16, device="cuda") for n in ("xr", "xe", "ye", "gye", "gxe", "gxr")}
+    saved = torch.empty(P, 2 * I, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(m.moe_experts_ffn_workspace_size(dims, I, True), dtype=torch.uint8, device="cuda")
+    out, gx = torch.empty(T, H, dtype=torch.bfloat16, device="cuda"), torch.empty(T, H, dtype=torch.bfloat16, device="cuda")
+    gw = torch.empty(T, k, device="cuda")
+    gw1, gw2, gwr = torch.empty_like(w1), torch.empty_like(w2), torch.empty_like(c.w)
+    m.moe_shuffle_dispatch(plan, c.x, rows["xr"], rows["xe"])
+    m.moe_experts_ffn_forward(plan, rows["xe"], w1, w2, rows["ye"], ws, saved=saved)
+    m.moe_shuffle_combine(plan, rows["ye"], c.gates, out)
+    m.moe_shuffle_combine_backward(plan, grad_out, rows["ye"], c.gates, rows["gye"], gw)
+    m.moe_experts_ffn_backward(plan, rows["gye"], rows["xe"], w1, w2, saved, rows["gxe"], gw1, gw2, ws)
+    m.moe_shuffle_dispatch_backward(plan, rows["gxe"], rows["gxr"], gx)
+    m.moe_router_backward(c.dims, c.rule(), gw, c.logits, c.idx, c.x, c.w, gx, gwr, c.ws, grad_x_in=gx)
+    # 64 bits on the CPU
+    x, wr, a, b = (t.double().cpu().requires_grad_(True) for t in (c.x, c.w, w1, w2))
+    s = torch.sigmoid(x @ wr.T)
+    idx = c.idx.long().cpu()
+    at = s.gather(1, idx)
+    gates = at / (at.sum(1, keepdim=True) + 1e-20)
+    total = torch.zeros(T, H, dtype=torch.float64)
+    for e in range(E):
+        t, j = (idx == e).nonzero(as_tuple=True)
+        pre = x[t] @ a[e].T
+        y = (torch.nn.functional.silu(pre[:, :I]) * pre[:, I:]) @ b[e].T
+        total = total.index_add(0, t, gates[t, j][:, None] * y)
+    want = torch.autograd.grad(total, (x, wr, a, b), grad_out.double().cpu())
+    for got, w, name in zip((gx, gwr, gw1, gw2), want, ("x", "w_router", "w_gate_up", "w_down")):
+        far = float((got.double().cpu() - w).norm() / w.norm())
+        assert far <= 6 * 2.0 ** -8, f"{name}: {far}"
+    tensors, before = [], []
+    for p, g in ((w1, gw1), (w2, gw2), (c.w, gwr)):
+        master = p.float()
+        tensors.append(dict(p=master, copy=p, g=g, m=torch.zeros_like(master), v=torch.zeros_like(master)))
+        before.append(master.clone())
+    m.moe_adamw_step(m.AdamwTensors(tensors), 1, 1e-2, weight_decay=0.0)
+    for t, old in zip(tensors, before):
+        # the first step is lr times the gradient's sign, wherever the gradient is far above eps
+        far = t["g"].float().abs() > 1e-4
+        move = (t["p"] - old)[far]
+        assert bool(((move + 1e-2 * t["g"].float().sign()[far]).abs() <= 1e-2 * 1.1e-4 + 2.0 ** -23 * old[far].abs()).all())
+        assert torch.equal(t["copy"], t["p"].to(torch.bfloat16))

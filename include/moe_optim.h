@@ -38,8 +38,8 @@
  * scale NaN: all of it reads back as NaN.  All-zero states (codes and
  * scales) are those of a first step.
  *
- * Limits: count >= 0, 0 <= n < 2^40 each, pointers 16-byte aligned (scales 4),
- * chunks of 8192 elements below 2^31 in all.  The tensors of a call must not
+ * Limits: count >= 0, 0 <= n < 2^40 each, pointers 16-byte aligned (scales 4).
+ * The tensors of a call must not
  * overlap each other; within one of them that is checked.
  */
 #ifndef MOE_OPTIM_H

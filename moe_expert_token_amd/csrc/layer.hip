@@ -443,8 +443,11 @@ hipError_t launch_both(const LayerShape& S, const Rule& rule, const LayerCall& C
 template <int Group>
 hipError_t launch_rows(const LayerShape& S, const Rule& rule, const LayerCall& C, hipStream_t s)
 {
-    // up to 16 tokens no expert has more rows
-    return S.T <= 16 ? launch_both<Group, 16>(S, rule, C, s) : launch_both<Group, 32>(S, rule, C, s);
+#ifndef MS_ROWS
+#define MS_ROWS 12
+#endif
+    return S.P <= (int64_t)MS_ROWS * (S.P < S.E ? S.P : S.E) ? launch_both<Group, 16>(S, rule, C, s)
+                                                             : launch_both<Group, 32>(S, rule, C, s);
 }
 
 }  // namespace

@@ -2,12 +2,18 @@
 // and the formats), and the way between 8-bit states and their values.
 //
 // Every element is read and written once, so the bytes are the bound: 28 an element with fp32 states, fp32
-// parameters, their bf16 copy and bf16 gradients, 16.1 with 8-bit states.  A lane has eight neighbouring elements
-// (16 or 32 bytes of each kind), sixteen neighbouring lanes a group of 128, whose largest magnitudes four exchanges
-// within the sixteen find.  A block takes 8192 elements of one tensor; the tensors' addresses come with the kernel's
-// arguments, 40 a launch, so that nothing has to be copied to the device first.
+// parameters, their bf16 copy and bf16 gradients, 16.1 with 8-bit states.  What reaches the memory's rate is small
+// blocks in the order of memory: with four neighbouring elements a lane (16 contiguous bytes of fp32) and 1024 a block,
+// 197 M parameters with fp32 states take 910 us (6.1 TB/s, a large copy 6.5); 1028 with 8192 a block, 1128 with 8192 in
+// lanes of eight.  8-bit states, 1.4 G parameters: 3.81 ms (6.0 TB/s) with 1024 a block of two waves, 4.07 of four, 4.27
+// with 8192.  Unpacking moves fewer bytes an element and likes lanes of eight: 1.37 ms against 1.57 (6.2 TB/s).
+//
+// A group of 128 is 32 or 16 neighbouring lanes, which find its largest magnitudes by five or four exchanges.  The
+// tensors' addresses come with the kernel's arguments, 40 a launch, so that nothing has to be copied to the device first.
 #include <hip/hip_runtime.h>
 #include <math.h>
+
+#include <type_traits>
 
 #include "checks.h"
 #include "device_common.h"
@@ -17,15 +23,21 @@
 namespace ms {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kEach = 8;                    // elements of a lane
-constexpr int kTurn = kThreads * kEach;     // elements a block has at once
-constexpr int kChunk = 4 * kTurn;           // of a block
-constexpr int kTensors = 40;                // of a launch
+constexpr int kTensors = 40;  // of a launch
 constexpr int kGroup = MOE_ADAMW_GROUP;
 // Group steps are the largest magnitudes times these: the largest becomes 448 = 1.75 2^8 or 8064 = 63 2^7.
 constexpr float kPerM = 1.0f / 448.0f, kPerS = 1.0f / 8064.0f;
-static_assert(kGroup == 16 * kEach, "sixteen lanes a group");
+
+// A kernel's blocks: Threads lanes of Each elements, Turns times.
+template <int EACH, int THREADS, int TURNS>
+struct Shape {
+    static constexpr int kEach = EACH, kThreads = THREADS, kTurns = TURNS;
+    static constexpr int kTurn = kEach * kThreads, kChunk = kTurn * kTurns;
+    static constexpr int kLanes = kGroup / kEach;  // of a group
+};
+typedef Shape<4, 256, 1> StepWide;
+typedef Shape<4, 128, 2> StepEight;
+typedef Shape<8, 256, 1> Convert;
 
 struct Tensor {
     char *p, *copy;
@@ -79,84 +91,109 @@ __host__ __device__ inline Rates rates_of(const Hyper& h, double lr, int64_t ste
     return r;
 }
 
-// ---- a lane's eight elements at i, of which `n` exist; the others read as zero ----
+// ---- a lane's N elements (4 or 8) at i, of which `n` exist; the others read as zero ----
 
-template <bool Half>
-__device__ __forceinline__ void read8(const char* from, int64_t i, int n, float (&f)[kEach])
+template <bool Half, int N>
+__device__ __forceinline__ void read(const char* from, int64_t i, int n, float (&f)[N])
 {
-    if (n >= kEach) {
+    if (n >= N) {
         if constexpr (Half) {
-            const u32x4 d = __builtin_nontemporal_load((const u32x4*)(from + i * 2));
+            typedef unsigned vec __attribute__((ext_vector_type(N / 2)));
+            const vec d = __builtin_nontemporal_load((const vec*)(from + i * 2));
 #pragma unroll
-            for (int c = 0; c < 4; ++c) { f[2 * c] = bf16_lo(d[c]); f[2 * c + 1] = bf16_hi(d[c]); }
+            for (int c = 0; c < N / 2; ++c) { f[2 * c] = bf16_lo(d[c]); f[2 * c + 1] = bf16_hi(d[c]); }
         } else {
-            const u32x4 a = __builtin_nontemporal_load((const u32x4*)(from + i * 4));
-            const u32x4 b = __builtin_nontemporal_load((const u32x4*)(from + i * 4) + 1);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) { f[c] = __uint_as_float(a[c]); f[4 + c] = __uint_as_float(b[c]); }
+            for (int h = 0; h < N / 4; ++h) {
+                const u32x4 a = __builtin_nontemporal_load((const u32x4*)(from + i * 4) + h);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) f[4 * h + c] = __uint_as_float(a[c]);
+            }
         }
         return;
     }
 #pragma unroll
-    for (int c = 0; c < kEach; ++c)
+    for (int c = 0; c < N; ++c)
         f[c] = c >= n ? 0.0f
                : Half ? __uint_as_float((unsigned)((const unsigned short*)from)[i + c] << 16)
                       : ((const float*)from)[i + c];
 }
 
-template <bool Half>
-__device__ __forceinline__ void write8(char* to, int64_t i, int n, const float (&f)[kEach])
+template <bool Half, int N>
+__device__ __forceinline__ void write(char* to, int64_t i, int n, const float (&f)[N])
 {
-    if (n >= kEach) {
+    if (n >= N) {
         if constexpr (Half) {
-            const u32x4 d = {bf16_pack2(f[0], f[1]), bf16_pack2(f[2], f[3]), bf16_pack2(f[4], f[5]),
-                             bf16_pack2(f[6], f[7])};
-            __builtin_nontemporal_store(d, (u32x4*)(to + i * 2));
-        } else {
-            u32x4 a, b;
+            typedef unsigned vec __attribute__((ext_vector_type(N / 2)));
+            vec d;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) { a[c] = __float_as_uint(f[c]); b[c] = __float_as_uint(f[4 + c]); }
-            __builtin_nontemporal_store(a, (u32x4*)(to + i * 4));
-            __builtin_nontemporal_store(b, (u32x4*)(to + i * 4) + 1);
+            for (int c = 0; c < N / 2; ++c) d[c] = bf16_pack2(f[2 * c], f[2 * c + 1]);
+            __builtin_nontemporal_store(d, (vec*)(to + i * 2));
+        } else {
+#pragma unroll
+            for (int h = 0; h < N / 4; ++h) {
+                u32x4 a;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) a[c] = __float_as_uint(f[4 * h + c]);
+                __builtin_nontemporal_store(a, (u32x4*)(to + i * 4) + h);
+            }
         }
         return;
     }
 #pragma unroll
-    for (int c = 0; c < kEach; ++c)
+    for (int c = 0; c < N; ++c)
         if (c < n) {
             if (Half) ((unsigned short*)to)[i + c] = (unsigned short)bf16_pack2(f[c], f[c]);
             else ((float*)to)[i + c] = f[c];
         }
 }
 
-__device__ __forceinline__ u32x2 read_codes(const char* from, int64_t i, int n)
-{
-    if (n >= kEach) return __builtin_nontemporal_load((const u32x2*)(from + i));
-    u32x2 d = {0, 0};
-#pragma unroll
-    for (int c = 0; c < kEach; ++c)
-        if (c < n) d[c >> 2] |= (unsigned)((const unsigned char*)from)[i + c] << (8 * (c & 3));
-    return d;
-}
+// N codes, four a register.
+template <int N>
+struct Codes {
+    typedef unsigned vec __attribute__((ext_vector_type(N / 4 == 1 ? 2 : N / 4)));
+    unsigned d[N / 4];
 
-__device__ __forceinline__ void write_codes(char* to, int64_t i, int n, u32x2 d)
-{
-    if (n >= kEach) {
-        __builtin_nontemporal_store(d, (u32x2*)(to + i));
-        return;
-    }
+    __device__ __forceinline__ void read(const char* from, int64_t i, int n)
+    {
+        if (n >= N) {
+            if constexpr (N == 4) {
+                d[0] = __builtin_nontemporal_load((const unsigned*)(from + i));
+            } else {
+                const vec v = __builtin_nontemporal_load((const vec*)(from + i));
+                d[0] = v[0];
+                d[1] = v[1];
+            }
+            return;
+        }
 #pragma unroll
-    for (int c = 0; c < kEach; ++c)
-        if (c < n) to[i + c] = (char)(d[c >> 2] >> (8 * (c & 3)));
-}
+        for (int h = 0; h < N / 4; ++h) d[h] = 0;
+#pragma unroll
+        for (int c = 0; c < N; ++c)
+            if (c < n) d[c >> 2] |= (unsigned)((const unsigned char*)from)[i + c] << (8 * (c & 3));
+    }
+
+    __device__ __forceinline__ void write(char* to, int64_t i, int n) const
+    {
+        if (n >= N) {
+            if constexpr (N == 4) __builtin_nontemporal_store(d[0], (unsigned*)(to + i));
+            else __builtin_nontemporal_store(vec{d[0], d[1]}, (vec*)(to + i));
+            return;
+        }
+#pragma unroll
+        for (int c = 0; c < N; ++c)
+            if (c < n) to[i + c] = (char)(d[c >> 2] >> (8 * (c & 3)));
+    }
+};
 
 // ---- 8-bit states ----
 
-__device__ __forceinline__ void values_m(u32x2 d, float step, float (&f)[kEach])
+template <int N>
+__device__ __forceinline__ void values_m(const Codes<N>& q, float step, float (&f)[N])
 {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const auto a = __builtin_amdgcn_cvt_pk_f32_fp8(d[h], false), b = __builtin_amdgcn_cvt_pk_f32_fp8(d[h], true);
+    for (int h = 0; h < N / 4; ++h) {
+        const auto a = __builtin_amdgcn_cvt_pk_f32_fp8(q.d[h], false), b = __builtin_amdgcn_cvt_pk_f32_fp8(q.d[h], true);
         f[4 * h] = a[0] * step;
         f[4 * h + 1] = a[1] * step;
         f[4 * h + 2] = b[0] * step;
@@ -167,59 +204,63 @@ __device__ __forceinline__ void values_m(u32x2 d, float step, float (&f)[kEach])
 // Codes c > 0 of s: as the upper bits of a float, 32 2^(c / 32) has the exponent 5 + c / 32.
 constexpr int kBaseS = 132 << 5;
 
-__device__ __forceinline__ void values_s(u32x2 d, float step, float (&f)[kEach])
+template <int N>
+__device__ __forceinline__ void values_s(const Codes<N>& q, float step, float (&f)[N])
 {
 #pragma unroll
-    for (int c = 0; c < kEach; ++c) {
-        const unsigned code = (d[c >> 2] >> (8 * (c & 3))) & 255u;
+    for (int c = 0; c < N; ++c) {
+        const unsigned code = (q.d[c >> 2] >> (8 * (c & 3))) & 255u;
         f[c] = (code ? __uint_as_float((code + kBaseS) << 18) : 0.0f) * step;
     }
 }
 
 // The step of a group: its largest magnitude times `per`, at least 2^-126; NaN where one is not finite.
-__device__ __forceinline__ float group_step(const float (&f)[kEach], float per)
+template <int N>
+__device__ __forceinline__ float group_step(const float (&f)[N], float per)
 {
     float most = 0;
     bool bad = false;
 #pragma unroll
-    for (int c = 0; c < kEach; ++c) {
+    for (int c = 0; c < N; ++c) {
         const float a = fabsf(f[c]);
         bad |= !(a <= 3.40282347e38f);
         most = fmaxf(most, a);
     }
     if (bad) most = __uint_as_float(0x7f800000u);
 #pragma unroll
-    for (int d = 1; d < 16; d <<= 1) most = fmaxf(most, __shfl_xor(most, d, kWave));
+    for (int d = 1; d < kGroup / N; d <<= 1) most = fmaxf(most, __shfl_xor(most, d, kWave));
     return most <= 3.40282347e38f ? fmaxf(most * per, 1.17549435e-38f) : __uint_as_float(0x7fc00000u);
 }
 
 // v_cvt_pk_fp8_f32: e4m3, to the nearest, the even one of two.  |f inv| is at most 448 (1 + 2^-23), which is 448.
-__device__ __forceinline__ u32x2 codes_m(const float (&f)[kEach], float step)
+template <int N>
+__device__ __forceinline__ Codes<N> codes_m(const float (&f)[N], float step)
 {
-    if (step != step) return u32x2{0, 0};
+    Codes<N> q = {};
+    if (step != step) return q;
     const float inv = 1.0f / step;
-    u32x2 d;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < N / 4; ++h) {
         int v = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * h] * inv, f[4 * h + 1] * inv, 0, false);
         v = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * h + 2] * inv, f[4 * h + 3] * inv, v, true);
-        d[h] = (unsigned)v;
+        q.d[h] = (unsigned)v;
     }
-    return d;
+    return q;
 }
 
-__device__ __forceinline__ u32x2 codes_s(const float (&f)[kEach], float step)
+template <int N>
+__device__ __forceinline__ Codes<N> codes_s(const float (&f)[N], float step)
 {
-    if (step != step) return u32x2{0, 0};
+    Codes<N> q = {};
+    if (step != step) return q;
     const float inv = 1.0f / step;
-    u32x2 d = {0, 0};
 #pragma unroll
-    for (int c = 0; c < kEach; ++c) {
+    for (int c = 0; c < N; ++c) {
         const int u = __float_as_int(f[c] * inv);
         const int code = min(max(((u + 0x1ffff + ((u >> 18) & 1)) >> 18) - kBaseS, 1), 255);
-        d[c >> 2] |= (f[c] > 0.0f ? (unsigned)code : 0u) << (8 * (c & 3));
+        q.d[c >> 2] |= (f[c] > 0.0f ? (unsigned)code : 0u) << (8 * (c & 3));
     }
-    return d;
+    return q;
 }
 
 // ---- the kernels ----
@@ -231,23 +272,46 @@ __device__ __forceinline__ int tensor_of(const Tensors& A, int chunk)
     return __builtin_ctzll(__ballot(lane < A.count && A.first[min(lane, kTensors - 1) + 1] > chunk));
 }
 
-// Calls f(i, n) for a block's turns: this lane's eight elements at i, n of them in the tensor (at least one in some
-// lane of each wave that is called).
-template <class F>
+// Calls f(i, n) for a block's turns: this lane's elements at i, n of them in the tensor (at least one in some lane of
+// each wave that is called).
+template <class B, class F>
 __device__ __forceinline__ void turns(int64_t n, int chunk, F&& f)
 {
-    const int64_t at = (int64_t)chunk * kChunk + threadIdx.x * kEach;
-#pragma unroll 1
-    for (int turn = 0; turn < kChunk / kTurn; ++turn) {
-        const int64_t i = at + turn * kTurn, left = n - i;
-        if (n - (i - lane_id() * kEach) <= 0) return;  // the same in every lane
-        f(i, (int)(left < 0 ? 0 : left < kEach ? left : kEach));
+    const int64_t at = (int64_t)chunk * B::kChunk + threadIdx.x * B::kEach;
+#pragma unroll
+    for (int turn = 0; turn < B::kTurns; ++turn) {
+        const int64_t i = at + turn * B::kTurn, left = n - i;
+        if (n - (i - lane_id() * B::kEach) <= 0) return;  // the same in every lane
+        f(i, (int)(left < 0 ? 0 : left < B::kEach ? left : B::kEach));
     }
 }
 
-template <bool HalfP, bool HalfG, bool Eight>
-__global__ __launch_bounds__(kThreads) void adamw_kernel(Tensors A, Rates fixed, Hyper h)
+// The group of the lane's elements at i.
+template <class B>
+__device__ __forceinline__ int64_t group_of(int64_t i)
 {
+    return (i - (lane_id() & (B::kLanes - 1)) * B::kEach) / kGroup;
+}
+
+// Packs a lane's elements of states; every lane of a group calls it.
+template <class B>
+__device__ __forceinline__ void pack(const Tensor& t, int64_t i, int n, const float (&m)[B::kEach],
+                                     const float (&s)[B::kEach])
+{
+    const float step_m = group_step(m, kPerM), step_s = group_step(s, kPerS);
+    codes_m(m, step_m).write(t.m, i, n);
+    codes_s(s, step_s).write(t.v, i, n);
+    if ((lane_id() & (B::kLanes - 1)) == 0 && n > 0) {
+        const int64_t group = group_of<B>(i);
+        t.m_scale[group] = step_m;
+        t.v_scale[group] = step_s;
+    }
+}
+
+template <bool HalfP, bool HalfG, bool Eight, class B>
+__global__ __launch_bounds__(B::kThreads) void adamw_kernel(Tensors A, Rates fixed, Hyper h)
+{
+    constexpr int N = B::kEach;
     const int which = tensor_of(A, blockIdx.x);
     const Tensor t = A.t[which];
     const int chunk = blockIdx.x - A.first[which];
@@ -257,96 +321,87 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(Tensors A, Rates fixed,
         r = rates_of(h, h.lr_device ? (double)*h.lr_device : h.lr, step < 1 ? 1 : step);
     }
     const float scale = h.grad_scale ? *h.grad_scale : 1.0f;
-    turns(t.n, chunk, [&](int64_t i, int n) {
-        float g[kEach], m[kEach], s[kEach], p[kEach];
-        read8<HalfG>(t.g, i, n, g);
-        read8<HalfP>(t.p, i, n, p);
+    turns<B>(t.n, chunk, [&](int64_t i, int n) {
+        float g[N], m[N], s[N], p[N];
+        read<HalfG>(t.g, i, n, g);
+        read<HalfP>(t.p, i, n, p);
         if constexpr (Eight) {
-            const int64_t group = (i - (lane_id() & 15) * kEach) / kGroup;
+            const int64_t group = group_of<B>(i);
             const bool any = group * kGroup < t.n;
-            values_m(read_codes(t.m, i, n), any ? t.m_scale[group] : 0.0f, m);
-            values_s(read_codes(t.v, i, n), any ? t.v_scale[group] : 0.0f, s);
+            Codes<N> qm, qs;
+            qm.read(t.m, i, n);
+            qs.read(t.v, i, n);
+            values_m(qm, any ? t.m_scale[group] : 0.0f, m);
+            values_s(qs, any ? t.v_scale[group] : 0.0f, s);
 #pragma unroll
-            for (int c = 0; c < kEach; ++c) s[c] *= s[c];
+            for (int c = 0; c < N; ++c) s[c] *= s[c];
         } else {
-            read8<false>(t.m, i, n, m);
-            read8<false>(t.v, i, n, s);
+            read<false>(t.m, i, n, m);
+            read<false>(t.v, i, n, s);
         }
-        float v[kEach];
+        float v[N];
 #pragma unroll
-        for (int c = 0; c < kEach; ++c) {
+        for (int c = 0; c < N; ++c) {
             const float d = g[c] * scale;
             m[c] = m[c] * r.b1 + d * r.a1;
             v[c] = s[c] * r.b2 + d * d * r.a2;
             s[c] = sqrtf(v[c]);
             p[c] = p[c] * r.keep - r.gain * m[c] / (s[c] * r.root + r.eps);
         }
-        write8<HalfP>(t.p, i, n, p);
-        if (!HalfP && t.copy) write8<true>(t.copy, i, n, p);
+        write<HalfP>(t.p, i, n, p);
+        if (!HalfP && t.copy) write<true>(t.copy, i, n, p);
         if constexpr (Eight) {
-            const int64_t group = (i - (lane_id() & 15) * kEach) / kGroup;
-            if (n < kEach) {  // what is not there counts as zero (a gradient of zero leaves 0 unless eps is 0)
+            if (n < N) {  // what is not there counts as zero
 #pragma unroll
-                for (int c = 0; c < kEach; ++c)
+                for (int c = 0; c < N; ++c)
                     if (c >= n) m[c] = s[c] = 0.0f;
             }
-            const float step_m = group_step(m, kPerM), step_s = group_step(s, kPerS);
-            write_codes(t.m, i, n, codes_m(m, step_m));
-            write_codes(t.v, i, n, codes_s(s, step_s));
-            if ((lane_id() & 15) == 0 && n > 0) {
-                t.m_scale[group] = step_m;
-                t.v_scale[group] = step_s;
-            }
+            pack<B>(t, i, n, m, s);
         } else {
-            write8<false>(t.m, i, n, m);
-            write8<false>(t.v, i, n, v);
+            write<false>(t.m, i, n, m);
+            write<false>(t.v, i, n, v);
         }
     });
 }
 
 // p and copy hold m_out and v_out.
-__global__ __launch_bounds__(kThreads) void adamw_pack_kernel(Tensors A)
+template <class B>
+__global__ __launch_bounds__(B::kThreads) void adamw_pack_kernel(Tensors A)
 {
     const int which = tensor_of(A, blockIdx.x);
     const Tensor t = A.t[which];
-    turns(t.n, blockIdx.x - A.first[which], [&](int64_t i, int n) {
-        float m[kEach], s[kEach];
-        read8<false>(t.p, i, n, m);
-        read8<false>(t.copy, i, n, s);
+    turns<B>(t.n, blockIdx.x - A.first[which], [&](int64_t i, int n) {
+        float m[B::kEach], s[B::kEach];
+        read<false>(t.p, i, n, m);
+        read<false>(t.copy, i, n, s);
 #pragma unroll
-        for (int c = 0; c < kEach; ++c) s[c] = s[c] < 0.0f ? 0.0f : sqrtf(s[c]);
-        const int64_t group = (i - (lane_id() & 15) * kEach) / kGroup;
-        const float step_m = group_step(m, kPerM), step_s = group_step(s, kPerS);
-        write_codes(t.m, i, n, codes_m(m, step_m));
-        write_codes(t.v, i, n, codes_s(s, step_s));
-        if ((lane_id() & 15) == 0 && n > 0) {
-            t.m_scale[group] = step_m;
-            t.v_scale[group] = step_s;
-        }
+        for (int c = 0; c < B::kEach; ++c) s[c] = s[c] < 0.0f ? 0.0f : sqrtf(s[c]);
+        pack<B>(t, i, n, m, s);
     });
 }
 
-template <bool Half>
-__global__ __launch_bounds__(kThreads) void adamw_unpack_kernel(Tensors A)
+template <bool Half, class B>
+__global__ __launch_bounds__(B::kThreads) void adamw_unpack_kernel(Tensors A)
 {
     const int which = tensor_of(A, blockIdx.x);
     const Tensor t = A.t[which];
-    turns(t.n, blockIdx.x - A.first[which], [&](int64_t i, int n) {
+    turns<B>(t.n, blockIdx.x - A.first[which], [&](int64_t i, int n) {
         if (n <= 0) return;
-        float m[kEach], s[kEach];
+        float m[B::kEach], s[B::kEach];
         const int64_t group = i / kGroup;
-        values_m(read_codes(t.m, i, n), t.m_scale[group], m);
-        values_s(read_codes(t.v, i, n), t.v_scale[group], s);
+        Codes<B::kEach> qm, qs;
+        qm.read(t.m, i, n);
+        qs.read(t.v, i, n);
+        values_m(qm, t.m_scale[group], m);
+        values_s(qs, t.v_scale[group], s);
 #pragma unroll
-        for (int c = 0; c < kEach; ++c) s[c] *= s[c];
-        write8<Half>(t.p, i, n, m);
-        write8<Half>(t.copy, i, n, s);
+        for (int c = 0; c < B::kEach; ++c) s[c] *= s[c];
+        write<Half>(t.p, i, n, m);
+        write<Half>(t.copy, i, n, s);
     });
 }
 
 // ---- the boundary ----
-
-int64_t chunks_of(int64_t n) { return (n + kChunk - 1) / kChunk; }
 
 size_t scale_bytes(int64_t n) { return (size_t)((n + kGroup - 1) / kGroup) * 4; }
 
@@ -356,11 +411,10 @@ enum class Call { Step, Pack, Unpack };
 int check_tensors(const moe_adamw_tensor* tensors, int32_t count, Call call, size_t p_size, size_t g_size, bool eight)
 {
     if (count < 0 || (count > 0 && !tensors)) return MOE_SHUFFLE_E_INVALID_ARG;
-    int64_t chunks = 0;
     for (int i = 0; i < count; ++i) {
         const moe_adamw_tensor& t = tensors[i];
         if (t.n < 0) return MOE_SHUFFLE_E_INVALID_ARG;
-        if (t.n >= (int64_t)1 << 40 || (chunks += chunks_of(t.n)) >= (int64_t)1 << 31) return MOE_SHUFFLE_E_OVERFLOW;
+        if (t.n >= (int64_t)1 << 40) return MOE_SHUFFLE_E_OVERFLOW;
         if (t.n == 0) continue;
         const bool step = call == Call::Step;
         const void* const a = step ? t.p : t.m_out;
@@ -382,10 +436,19 @@ int check_tensors(const moe_adamw_tensor* tensors, int32_t count, Call call, siz
     return MOE_SHUFFLE_OK;
 }
 
-// launch(grid, tensors) for every 40 tensors that have an element.
-template <class F>
-hipError_t launch_tensors(const moe_adamw_tensor* tensors, int32_t count, bool step, F&& launch)
+// Bytes an element of what a call's kernel finds in a Tensor.
+struct Sizes {
+    int p, copy, g, state;
+};
+
+// launch(grid, tensors) for every 40 tensors that have an element; of one with very many, pieces of 2^32.
+template <class B, class F>
+hipError_t launch_tensors(const moe_adamw_tensor* tensors, int32_t count, bool step, const Sizes& size, F&& launch)
 {
+    constexpr int64_t kPiece = (int64_t)1 << 32;
+    static_assert(kPiece % B::kChunk == 0 && kPiece % kGroup == 0, "pieces of whole chunks and groups");
+    // one dispatch carries fewer than 2^32 work-items
+    static_assert(kPiece / B::kChunk * B::kThreads < (int64_t)1 << 32, "a piece fits a dispatch");
     Tensors A;
     A.count = 0;
     int64_t chunks = 0;
@@ -398,17 +461,22 @@ hipError_t launch_tensors(const moe_adamw_tensor* tensors, int32_t count, bool s
     };
     for (int i = 0; i < count; ++i) {
         const moe_adamw_tensor& t = tensors[i];
-        if (t.n == 0) continue;
-        // one dispatch carries fewer than 2^32 work-items
-        if (A.count == kTensors || (chunks + chunks_of(t.n)) * kThreads >= (int64_t)1 << 32) {
-            const hipError_t e = go();
-            if (e != hipSuccess) return e;
+        for (int64_t at = 0; at < t.n; at += kPiece) {
+            const int64_t n = t.n - at < kPiece ? t.n - at : kPiece, more = (n + B::kChunk - 1) / B::kChunk;
+            if (A.count == kTensors || (chunks + more) * B::kThreads >= (int64_t)1 << 32) {
+                const hipError_t e = go();
+                if (e != hipSuccess) return e;
+            }
+            const auto from = [&](const void* p, int bytes) { return p ? (char*)p + at * bytes : nullptr; };
+            const auto scales = [&](float* p) { return p ? p + at / kGroup : nullptr; };
+            A.t[A.count] = Tensor{from(step ? t.p : t.m_out, size.p),    from(step ? t.copy : t.v_out, size.copy),
+                                  from(t.g, size.g),                     from(t.m, size.state),
+                                  from(t.v, size.state),                 scales(t.m_scale),
+                                  scales(t.v_scale),                     n};
+            A.first[A.count++] = (int)chunks;
+            chunks += more;
+            A.first[A.count] = (int)chunks;
         }
-        A.t[A.count] = Tensor{(char*)(step ? t.p : t.m_out), (char*)(step ? t.copy : t.v_out), (const char*)t.g,
-                              (char*)t.m, (char*)t.v, t.m_scale, t.v_scale, t.n};
-        A.first[A.count++] = (int)chunks;
-        chunks += chunks_of(t.n);
-        A.first[A.count] = (int)chunks;
     }
     return go();
 }
@@ -442,29 +510,29 @@ int moe_adamw_step(const moe_adamw_tensor* tensors, int32_t count, const moe_ada
                   q->grad_scale};
     const Rates r = rates_of(h, h.lr, h.step < 1 ? 1 : h.step);
     hipStream_t s = (hipStream_t)stream;
-    return status_of(launch_tensors(tensors, count, true, [&](dim3 grid, const Tensors& A) {
-        const auto go = [&](auto p, auto g, auto e) {
-            adamw_kernel<decltype(p)::value, decltype(g)::value, decltype(e)::value><<<grid, kThreads, 0, s>>>(A, r, h);
-        };
-        const auto with_state = [&](auto p, auto g) {
-            if (eight) go(p, g, std::true_type());
-            else go(p, g, std::false_type());
-        };
-        const auto with_grad = [&](auto p) {
-            if (half_g) with_state(p, std::true_type());
-            else with_state(p, std::false_type());
-        };
-        if (half_p) with_grad(std::true_type());
-        else with_grad(std::false_type());
-    }));
+    const Sizes size{half_p ? 2 : 4, 2, half_g ? 2 : 4, eight ? 1 : 4};
+    const auto run = [&](auto p, auto g, auto e) {
+        typedef std::conditional_t<decltype(e)::value, StepEight, StepWide> B;
+        return status_of(launch_tensors<B>(tensors, count, true, size, [&](dim3 grid, const Tensors& A) {
+            adamw_kernel<decltype(p)::value, decltype(g)::value, decltype(e)::value, B>
+                <<<grid, B::kThreads, 0, s>>>(A, r, h);
+        }));
+    };
+    const auto with_state = [&](auto p, auto g) {
+        return eight ? run(p, g, std::true_type()) : run(p, g, std::false_type());
+    };
+    const auto with_grad = [&](auto p) {
+        return half_g ? with_state(p, std::true_type()) : with_state(p, std::false_type());
+    };
+    return half_p ? with_grad(std::true_type()) : with_grad(std::false_type());
 }
 
 int moe_adamw_pack(const moe_adamw_tensor* tensors, int32_t count, void* stream)
 {
     const int rc = check_tensors(tensors, count, Call::Pack, 4, 4, true);
     if (rc) return rc;
-    return status_of(launch_tensors(tensors, count, false, [&](dim3 grid, const Tensors& A) {
-        adamw_pack_kernel<<<grid, kThreads, 0, (hipStream_t)stream>>>(A);
+    return status_of(launch_tensors<Convert>(tensors, count, false, Sizes{4, 4, 0, 1}, [&](dim3 grid, const Tensors& A) {
+        adamw_pack_kernel<Convert><<<grid, Convert::kThreads, 0, (hipStream_t)stream>>>(A);
     }));
 }
 
@@ -474,9 +542,10 @@ int moe_adamw_unpack(const moe_adamw_tensor* tensors, int32_t count, int32_t val
     const bool half = values == MOE_ADAMW_BF16;
     const int rc = check_tensors(tensors, count, Call::Unpack, half ? 2 : 4, 4, true);
     if (rc) return rc;
-    return status_of(launch_tensors(tensors, count, false, [&](dim3 grid, const Tensors& A) {
-        if (half) adamw_unpack_kernel<true><<<grid, kThreads, 0, (hipStream_t)stream>>>(A);
-        else adamw_unpack_kernel<false><<<grid, kThreads, 0, (hipStream_t)stream>>>(A);
+    const Sizes size{half ? 2 : 4, half ? 2 : 4, 0, 1};
+    return status_of(launch_tensors<Convert>(tensors, count, false, size, [&](dim3 grid, const Tensors& A) {
+        if (half) adamw_unpack_kernel<true, Convert><<<grid, Convert::kThreads, 0, (hipStream_t)stream>>>(A);
+        else adamw_unpack_kernel<false, Convert><<<grid, Convert::kThreads, 0, (hipStream_t)stream>>>(A);
     }));
 }
 

@@ -20,16 +20,16 @@
 namespace ms {
 namespace {
 
-constexpr int kTokens = 64;  // rows of a logits tile
-
 // How the logits' product is split: `splits` parts of `each` elements of H (a multiple of the tile's 64).
 struct Cut {
+    int tokens;            // rows of a tile
     int splits, each, ld;  // ld: a row of partial sums, E rounded up to 4
     float gamma;           // a logit is off by at most gamma ||x|| ||w||
 };
 
 struct Partial {
-    float *sum, *x2, *w2;  // [splits][T][ld], [splits][T] and [splits][E]: parts of logits and of squared norms
+    float *sum, *x2, *w2;  // [splits][T][ld], [splits][T]: parts of logits and of squared norms; [splits][expert tiles]:
+                           // the largest of a tile's experts' squared norms
 };
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
@@ -74,11 +74,14 @@ __device__ __forceinline__ float over_k(float v)
     return v + __shfl_xor(v, 32, kWave);
 }
 
-__global__ __launch_bounds__(kGemmThreads, 4) void router_logits_kernel(RouterShape S, Cut cut, Partial P, const char* x,
-                                                                        const char* w, int tiles, GridSpan span)
+template <int MF>
+__global__ __launch_bounds__(kGemmThreads, MF <= 2 ? 4 : 2) void router_logits_kernel(RouterShape S, Cut cut, Partial P,
+                                                                                      const char* x, const char* w,
+                                                                                      int tiles, int across, GridSpan span)
 {
-    __shared__ __align__(1024) char lds[Lds<true>::kBytes];
-    constexpr int MF = 2;
+    constexpr bool kSmall = MF <= 2;
+    constexpr int kTokens = 32 * MF;
+    __shared__ __align__(1024) char lds[Lds<kSmall>::kBytes];
     // the parts of H vary fastest: with 1, 2, 4 or 8 of them an XCD's L2 holds one part of the weights, not all
     const int b = span_block(span), part = b % cut.splits, at = b / cut.splits, tile = at % tiles;
     const int t0 = tile * kTokens, e0 = at / tiles * kTileFeatures, k0 = part * cut.each;
@@ -93,7 +96,7 @@ __global__ __launch_bounds__(kGemmThreads, 4) void router_logits_kernel(RouterSh
     }
     Squares<MF> see = {};
     Acc<MF> acc;
-    tile_product<true, MF>(r, f, K, lds, acc, see);
+    tile_product<kSmall, MF>(r, f, K, lds, acc, see);
     float* const to = P.sum + ((int64_t)part * S.T + t0) * cut.ld + e0;
 #pragma unroll
     for (int m = 0; m < MF; ++m)
@@ -119,28 +122,57 @@ __global__ __launch_bounds__(kGemmThreads, 4) void router_logits_kernel(RouterSh
     const int i = threadIdx.x;
     if (i < nr && e0 == 0)
         P.x2[(int64_t)part * S.T + t0 + i] = (rows[i] + rows[kTokens + i]) + (rows[2 * kTokens + i] + rows[3 * kTokens + i]);
-    if (tile == 0 && i < kTileFeatures && e0 + i < S.E) P.w2[part * S.E + e0 + i] = features[i] + features[kTileFeatures + i];
+    if (tile != 0) return;
+    if (i < kTileFeatures) {  // experts past the last have none
+        const float v = features[i] + features[kTileFeatures + i], top = wave_max(v != v ? __builtin_inff() : v);
+        if (lane == 0) rows[4 * kTokens + 2 * kTileFeatures + wave] = top;
+    }
+    __syncthreads();
+    if (i == 0) {
+        const float* const t = rows + 4 * kTokens + 2 * kTileFeatures;
+        P.w2[part * across + e0 / kTileFeatures] = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+    }
 }
 
 // ---- the choice ----
 
 constexpr int kChooseWaves = 4;
 
-// x . w[e] in 64 bits, the same in every lane.
-__device__ __forceinline__ double exact_logit(const u32x4* x, const u32x4* w, int V)
+// Vectors [from, to) of x . w[e] in 64 bits for two experts, the same in every lane.
+__device__ __forceinline__ void exact_logits(const u32x4* x, const u32x4* w, int e0, int e1, int V, int from, int to,
+                                             double (&out)[2])
 {
-    double sum = 0;
-    for (int v = lane_id(); v < V; v += kWave) {
-        const u32x4 a = x[v], b = w[v];
+    constexpr int kAhead = 4;
+    const u32x4 *const w0 = w + (int64_t)e0 * V, *const w1 = w + (int64_t)e1 * V;
+    double sum[2] = {};
+#pragma unroll 1
+    for (int v0 = from + lane_id(); v0 < to; v0 += kAhead * kWave) {
+        u32x4 a[kAhead], b[2][kAhead];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            sum = fma((double)bf16_lo(a[c]), (double)bf16_lo(b[c]), sum);
-            sum = fma((double)bf16_hi(a[c]), (double)bf16_hi(b[c]), sum);
+        for (int i = 0; i < kAhead; ++i) {  // past the end the last vector, which is left out below
+            const unsigned v = min(v0 + i * kWave, to - 1);
+            a[i] = x[v];
+            b[0][i] = w0[v];
+            b[1][i] = w1[v];
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            if (v0 + i * kWave >= to) break;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const double lo = (double)bf16_lo(a[i][c]), hi = (double)bf16_hi(a[i][c]);
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+                    sum[n] = fma(hi, (double)bf16_hi(b[n][i][c]), fma(lo, (double)bf16_lo(b[n][i][c]), sum[n]));
+            }
         }
     }
 #pragma unroll
-    for (int d = 1; d < kWave; d <<= 1) sum += __shfl_xor(sum, d, kWave);
-    return sum;
+    for (int n = 0; n < 2; ++n) {
+#pragma unroll
+        for (int d = 1; d < kWave; d <<= 1) sum[n] += __shfl_xor(sum[n], d, kWave);
+        out[n] = sum[n];
+    }
 }
 
 // As ordered_key, of fp32 keys.
@@ -169,9 +201,11 @@ __device__ __forceinline__ int choose_exact(const RouterShape& S, const Rule& ru
         double l = 0;  // lane i's: expert e0 + i
         if (!zero)
 #pragma unroll 1
-            for (int i = 0; i < kWave && e0 + i < S.E; ++i) {
-                const double d = exact_logit(x, w + (int64_t)(e0 + i) * V, V);
-                if (lane == i) l = d;
+            for (int i = 0; i < kWave && e0 + i < S.E; i += 2) {
+                double d[2];
+                exact_logits(x, w, e0 + i, min(e0 + i + 1, S.E - 1), V, 0, V, d);
+                if (lane == i) l = d[0];
+                if (lane == i + 1) l = d[1];
             }
         const int e = e0 + lane;
         if (e < S.E) keys[e] = ordered_key(rule.bias ? score64(l) + (double)rule.bias[e] : l);
@@ -190,80 +224,125 @@ __device__ __forceinline__ int choose_exact(const RouterShape& S, const Rule& ru
     return chosen;
 }
 
+// Sorts two keys with their experts: the larger first, of equal ones the lower expert.
+__device__ __forceinline__ void order(unsigned& a, unsigned& b, int& ea, int& eb)
+{
+    const bool swap = b > a || (b == a && eb < ea);
+    const unsigned k = swap ? b : a;
+    const int e = swap ? eb : ea;
+    b = swap ? a : b;
+    eb = swap ? ea : eb;
+    a = k;
+    ea = e;
+}
+
+constexpr int kAgain = 16;  // candidates of a row that are summed again, at most; with more, all its experts are
+
 // A wave a row; Each logits a lane.
 template <int Each>
-__global__ __launch_bounds__(kChooseWaves * kWave) void router_choose_kernel(RouterShape S, Rule rule, Cut cut, Partial P,
+__global__ __launch_bounds__(kChooseWaves * kWave, Each <= 4 ? 8 : 1) void router_choose_kernel(RouterShape S, Rule rule, Cut cut, Partial P,
                                                                              ChooseArgs A, GridSpan span)
 {
     __shared__ unsigned long long keys[kChooseWaves][Each * kWave];
-    const int lane = lane_id(), E = S.E, k = S.k, V = S.H / 8;
-    const int64_t t = (int64_t)span_block(span) * kChooseWaves + wave_id();
-    if (t >= S.T) return;
-    float l[Each], w2 = 0;
-    float x2 = 0;
-    for (int s = 0; s < cut.splits; ++s) x2 += P.x2[(int64_t)s * S.T + t];
-    const float* const sums = P.sum + t * cut.ld;
+    __shared__ double part[kChooseWaves][kAgain][kChooseWaves];  // of a row's candidates, by the wave that summed it
+    __shared__ int again_of[kChooseWaves][kAgain], agains[kChooseWaves];
+    const int lane = lane_id(), wave = wave_id(), E = S.E, k = S.k, V = S.H / 8;
+    const int64_t t = (int64_t)span_block(span) * kChooseWaves + wave;
+    const bool row = t < S.T;
+    const float* const sums = P.sum + (row ? t : 0) * cut.ld;
     const int64_t next = (int64_t)S.T * cut.ld;
+    float l[Each] = {}, widest = 0, off = 0, rounds = 0;
+    bool exact = false, zero = false;
+    // lane j's: the j-th largest key and its expert, k of them and those that may be as large as the k-th
+    int mine = 0, m = 0;
+    unsigned my_key = 0;
+    unsigned long long again = 0;
+    if (row) {
+        float x2 = 0, w2 = 0;
+        const int across = (E + kTileFeatures - 1) / kTileFeatures;
+#pragma unroll 4
+        for (int s = 0; s < cut.splits; ++s) {
+            const float* const from = sums + s * next;
 #pragma unroll
-    for (int i = 0; i < Each; ++i) {
-        const int e = lane + i * kWave;
-        l[i] = 0;
-        float n = 0;
-        if (e < E)
-            for (int s = 0; s < cut.splits; ++s) {
-                l[i] += sums[s * next + e];
-                n += P.w2[s * E + e];
+            for (int i = 0; i < Each; ++i) {
+                const unsigned e = lane + i * kWave;
+                if (e < (unsigned)E) l[i] += from[e];
             }
-        if (e < E && A.logits) A.logits[t * E + e] = l[i];
-        w2 = n != n || n > w2 ? n : w2;  // a NaN stays
-        if (w2 != w2) w2 = __builtin_inff();
-    }
-    w2 = wave_max(w2);
-    // how far a key may be off.  Squares that underflow say nothing, unless all is zero
-    const bool tiny = x2 < 8e-25f || w2 < 8e-25f;
-    bool exact = !(x2 <= 1e38f && w2 <= 1e38f), zero = w2 == 0.0f;
-    if (!exact && tiny && !zero) {
-        unsigned any = 0;
-        for (int v = lane; v < V; v += kWave) {
-            const u32x4 a = A.x[t * V + v];
-            any |= (a[0] | a[1] | a[2] | a[3]) & 0x7fff7fffu;
+            x2 += P.x2[(int64_t)s * S.T + t];
+            float most = P.w2[s * across];
+            for (int c = 1; c < across; ++c) most = fmaxf(most, P.w2[s * across + c]);
+            w2 += most;
         }
-        zero = __ballot(any != 0) == 0;
-        exact = !zero;
-    }
-    float slack = zero ? 0.0f : cut.gamma * sqrtf(x2) * sqrtf(w2) * 1.01f;
-    float bias[Each], most_bias = 0;
-    if (rule.bias) {
+        if (A.logits) {
+            float* const to = A.logits + t * E;
 #pragma unroll
-        for (int i = 0; i < Each; ++i) {
-            const int e = lane + i * kWave;
-            bias[i] = e < E ? rule.bias[e] : 0.0f;
-            if (fabsf(bias[i]) <= 3.4e38f) most_bias = fmaxf(most_bias, fabsf(bias[i]));
+            for (int i = 0; i < Each; ++i) {
+                const unsigned e = lane + i * kWave;
+                if (e < (unsigned)E) to[e] = l[i];
+            }
         }
-        // a sigmoid's slope is a quarter at most; its own roundings and the sum's in fp32
-        slack = 0.25f * slack + 4.8e-7f * (1.0f + wave_max(most_bias));
+        // how far a key may be off.  Squares that underflow say nothing, unless all is zero
+        const bool tiny = x2 < 8e-25f || w2 < 8e-25f;
+        exact = !(x2 <= 1e38f && w2 <= 1e38f);
+        zero = w2 == 0.0f;
+        if (!exact && tiny && !zero) {
+            unsigned any = 0;
+            for (int v = lane; v < V; v += kWave) {
+                const u32x4 a = A.x[t * V + v];
+                any |= (a[0] | a[1] | a[2] | a[3]) & 0x7fff7fffu;
+            }
+            zero = __ballot(any != 0) == 0;
+            exact = !zero;
+        }
+        off = zero ? 0.0f : cut.gamma * sqrtf(x2) * sqrtf(w2) * 1.01f;
     }
-    int chosen = 0;  // lane j's: the expert of slot j
-    if (!exact) {
+    if (row && !exact) {
         unsigned key[Each];
+        int expert[Each];
+        float v[Each];
+#pragma unroll
+        for (int i = 0; i < Each; ++i) v[i] = l[i];
+        if (rule.bias) {
+            float most_bias = 0;
+#pragma unroll
+            for (int i = 0; i < Each; ++i) {
+                const unsigned e = lane + i * kWave;
+                const float b = e < (unsigned)E ? rule.bias[e] : 0.0f;
+                if (fabsf(b) <= 3.4e38f) most_bias = fmaxf(most_bias, fabsf(b));
+                // the hardware's exponential and reciprocal: with the argument's rounding under 8e-7 of a sigmoid
+                v[i] = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.442695041f * l[i])) + b;
+            }
+            rounds = 1e-6f * (1.0f + wave_max(most_bias));  // those and the sum's in fp32
+        }
+        // of a key: a sigmoid's slope is s (1 - s), and changes by less than a tenth of what the logit does
+        widest = rule.bias ? 0.25f * off + rounds : off;
 #pragma unroll
         for (int i = 0; i < Each; ++i) {
-            const int e = lane + i * kWave;
-            key[i] = e < E ? ordered_key32(rule.bias ? 1.0f / (1.0f + expf(-l[i])) + bias[i] : l[i]) : 0;
+            expert[i] = lane + i * kWave;
+            key[i] = expert[i] < E ? ordered_key32(v[i]) : 0;
         }
-        // lane j's: the j-th largest key and its expert, k of them and those that may be as large as the k-th
-        int mine = 0, m = 0;
-        unsigned my_key = 0;
-        float least = 0;
+        // a lane's keys in order, so that only the first of each is looked at
+        if constexpr (Each == 2) order(key[0], key[1], expert[0], expert[1]);
+        if constexpr (Each == 4) {
+            order(key[0], key[1], expert[0], expert[1]);
+            order(key[2], key[3], expert[2], expert[3]);
+            order(key[0], key[2], expert[0], expert[2]);
+            order(key[1], key[3], expert[1], expert[3]);
+            order(key[1], key[2], expert[1], expert[2]);
+        }
+        float least = 0;  // what may still be as large as the k-th
+#pragma unroll 1
         for (;;) {
             unsigned best = key[0];
-            int at = lane;
+            int at = expert[0];
+            if constexpr (Each > 4) {
 #pragma unroll
-            for (int i = 1; i < Each; ++i)
-                if (key[i] > best) { best = key[i]; at = lane + i * kWave; }
+                for (int i = 1; i < Each; ++i)
+                    if (key[i] > best) { best = key[i]; at = expert[i]; }
+            }
             const unsigned top = wave_max(best);
             if (top == 0) break;  // all experts are listed
-            if (m >= k && (slack == 0 || !(key_value(top) >= least - 2 * slack))) break;
+            if (m >= k && (widest == 0 || !(key_value(top) >= least))) break;
             if (m == kWave) { exact = true; break; }
             const unsigned long long tie = __ballot(best == top);
             const int e = (tie & (tie - 1)) == 0 ? __builtin_amdgcn_readlane(at, __builtin_ctzll(tie))
@@ -272,44 +351,83 @@ __global__ __launch_bounds__(kChooseWaves * kWave) void router_choose_kernel(Rou
                 mine = e;
                 my_key = top;
             }
+            if constexpr (Each > 4) {
 #pragma unroll
-            for (int i = 0; i < Each; ++i)
-                if (lane + i * kWave == e) key[i] = 0;
-            if (++m == k) least = key_value(top);
+                for (int i = 0; i < Each; ++i)
+                    if (expert[i] == e) key[i] = 0;
+            } else {
+                const bool pop = at == e;
+#pragma unroll
+                for (int i = 0; i < Each; ++i) {
+                    key[i] = pop ? (i + 1 < Each ? key[i + 1 < Each ? i + 1 : i] : 0u) : key[i];
+                    expert[i] = pop ? (i + 1 < Each ? expert[i + 1 < Each ? i + 1 : i] : -1) : expert[i];
+                }
+            }
+            if (++m == k) least = key_value(top) - 2 * widest;
         }
         if (!exact) {
             const float v = key_value(my_key);
-            const float after = __shfl_down(v, 1, kWave);
-            // the slack is 0 where all keys are exact: equal ones are listed in the order of their indexes
-            const bool near = slack > 0 && lane + 1 < m && v - after <= 2 * slack;
-            unsigned long long again = __ballot(near);
+            float slack = off;
+            if (rule.bias) {
+                const float s = v - rule.bias[mine];
+                slack = off * fminf(fabsf(s * (1.0f - s)) + 0.1f * off + 1e-6f, 0.25f) + rounds;
+                if (!(slack >= 0.0f)) slack = widest;  // beside an infinite bias
+            }
+            const float after = __shfl_down(v, 1, kWave), both = slack + __shfl_down(slack, 1, kWave);
+            // nothing is off where all keys are exact: equal ones are listed in the order of their indexes
+            again = __ballot(widest > 0 && lane + 1 < m && v - after <= both);
             again |= again << 1;
-            if (again == 0) {
-                chosen = mine;
-            } else {
-                double key64 = (double)v;
-                for (unsigned long long left = again; left; left &= left - 1) {
-                    const int i = __builtin_ctzll(left), e = __builtin_amdgcn_readlane(mine, i);
-                    const double d = zero ? 0.0 : exact_logit(A.x + t * V, A.w + (int64_t)e * V, V);
-                    const double kd = rule.bias ? score64(d) + (double)rule.bias[e] : d;
-                    if (lane == i) key64 = kd;
-                }
-                const unsigned long long u = lane < m ? ordered_key(key64) : 0;
-                int rank = 0;
-                for (int i = 0; i < m; ++i) {
-                    const unsigned long long o =
-                        (unsigned long long)(unsigned)__builtin_amdgcn_readlane((int)(u >> 32), i) << 32 |
-                        (unsigned)__builtin_amdgcn_readlane((int)(unsigned)u, i);
-                    const int e = __builtin_amdgcn_readlane(mine, i);
-                    rank += o > u || (o == u && e < mine);
-                }
-                // to the lane of its slot; lanes past the candidates rank behind them
-                if (lane >= m) rank = lane;
-                chosen = __builtin_amdgcn_ds_permute(rank * 4, mine);
+            if (__popcll(again) > kAgain) exact = true;
+        }
+    }
+    // rows of zeros have logits of exactly 0, and need no sum
+    const bool sum_again = again != 0 && !exact && !zero;
+    const int place = mbcnt(again);  // of this lane's candidate among those
+    if (sum_again && (again >> lane & 1)) again_of[wave][place] = mine;
+    if (lane == 0) agains[wave] = sum_again ? __popcll(again) : 0;
+    __syncthreads();
+    // the block's waves share such a row: a quarter of H each, two experts at a time (they come in pairs)
+    const int quarter = (V + kChooseWaves - 1) / kChooseWaves, from = min(wave * quarter, V), to = min(from + quarter, V);
+#pragma unroll 1
+    for (int r = 0; r < kChooseWaves; ++r) {
+        const int n = __builtin_amdgcn_readfirstlane(agains[r]);
+#pragma unroll 1
+        for (int i = 0; i < n; i += 2) {
+            const int j = min(i + 1, n - 1);
+            double d[2];
+            exact_logits(A.x + (t - wave + r) * V, A.w, __builtin_amdgcn_readfirstlane(again_of[r][i]),
+                         __builtin_amdgcn_readfirstlane(again_of[r][j]), V, from, to, d);
+            if (lane == 0) {
+                part[r][i][wave] = d[0];
+                part[r][j][wave] = d[j - i];
             }
         }
     }
-    if (exact) chosen = choose_exact(S, rule, zero, A.x + t * V, A.w, keys[wave_id()]);
+    __syncthreads();
+    if (!row) return;
+    int chosen = mine;  // lane j's: the expert of slot j
+    if (exact) {
+        chosen = choose_exact(S, rule, zero, A.x + t * V, A.w, keys[wave]);
+    } else if (again != 0) {
+        double key64 = (double)key_value(my_key);
+        if (again >> lane & 1) {
+            const double* const d = part[wave][place];
+            const double l64 = zero ? 0.0 : (d[0] + d[1]) + (d[2] + d[3]);
+            key64 = rule.bias ? score64(l64) + (double)rule.bias[mine] : l64;
+        }
+        const unsigned long long u = lane < m ? ordered_key(key64) : 0;
+        int rank = 0;
+#pragma unroll 1
+        for (int i = 0; i < m; ++i) {
+            const unsigned long long o = (unsigned long long)(unsigned)__builtin_amdgcn_readlane((int)(u >> 32), i) << 32 |
+                                         (unsigned)__builtin_amdgcn_readlane((int)(unsigned)u, i);
+            const int e = __builtin_amdgcn_readlane(mine, i);
+            rank += o > u || (o == u && e < mine);
+        }
+        // to the lane of its slot; lanes past the candidates rank behind them
+        if (lane >= m) rank = lane;
+        chosen = __builtin_amdgcn_ds_permute(rank * 4, mine);
+    }
     float most = -__builtin_inff(), all = 0;
     if (!rule.sigmoid) {
 #pragma unroll
@@ -323,9 +441,13 @@ __global__ __launch_bounds__(kChooseWaves * kWave) void router_choose_kernel(Rou
             all = wave_total(all);
         }
     }
-    float mine = 0;
-    for (int s = 0; s < cut.splits; ++s) mine += sums[s * next + chosen];
-    const float g = gate_of(rule, k, mine, most, all);
+    float its = 0;  // the logit of lane j's slot
+#pragma unroll
+    for (int i = 0; i < Each; ++i) {
+        const float v = __shfl(l[i], chosen & (kWave - 1), kWave);
+        if (chosen / kWave == i) its = v;
+    }
+    const float g = gate_of(rule, k, its, most, all);
     if (lane < k) {
         A.idx[t * k + lane] = chosen;
         A.gate[t * k + lane] = g;
@@ -488,18 +610,22 @@ __global__ __launch_bounds__(256) void router_join_kernel(const f32x4* parts, in
 
 // ---- sizes ----
 
-constexpr int kBlocks = 512;  // two small tiles a CU
 constexpr int kMaxSplits = 16;
 
 int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 Cut cut_of(const RouterShape& S)
 {
-    const int64_t tiles = up(S.T, kTokens) * up(S.E, kTileFeatures);
+#ifndef MS_MF
+#define MS_MF 4
+#endif
+    Cut c;
+    c.tokens = S.T >= 4096 ? 32 * MS_MF : 64;
+    const int64_t tiles = up(S.T, c.tokens) * up(S.E, kTileFeatures);
+    const int kBlocks = c.tokens > 64 ? 256 : 512;
     int splits = 1;
     // parts of at least four tiles of k, as long as there are fewer blocks than fill the card
     while (splits < kMaxSplits && tiles * splits * 2 <= kBlocks && S.H >= splits * 2 * 4 * kTileK) splits *= 2;
-    Cut c;
     c.each = (int)up(up(S.H, splits), kTileK) * kTileK;
     c.splits = (int)up(S.H, c.each);
     c.ld = (int)up(S.E, 4) * 4;
@@ -575,7 +701,7 @@ size_t router_workspace(const RouterShape& S, bool backward)
     if (S.T > 0) {
         const Cut c = cut_of(S);
         n = align256((size_t)c.splits * S.T * c.ld * 4) + align256((size_t)c.splits * S.T * 4) +
-            align256((size_t)c.splits * S.E * 4);
+            align256((size_t)c.splits * up(S.E, kTileFeatures) * 4);
     }
     if (backward && S.T > 0) {
         const GradCut g = grad_cut(S);
@@ -593,10 +719,14 @@ hipError_t launch_router_forward(const RouterShape& S, const Rule& rule, const v
     P.sum = (float*)ws;
     P.x2 = (float*)(ws + align256((size_t)cut.splits * S.T * cut.ld * 4));
     P.w2 = (float*)((char*)P.x2 + align256((size_t)cut.splits * S.T * 4));
-    const int tiles = (int)up(S.T, kTokens);
-    const int64_t grid = (int64_t)tiles * up(S.E, kTileFeatures) * cut.splits;
+    const int tiles = (int)up(S.T, cut.tokens);
+    const int across = (int)up(S.E, kTileFeatures);
+    const int64_t grid = (int64_t)tiles * across * cut.splits;
     const hipError_t e = launch_spans(grid, kGemmThreads, [&](dim3 blocks, GridSpan span) {
-        router_logits_kernel<<<blocks, kGemmThreads, 0, s>>>(S, cut, P, (const char*)x, (const char*)w, tiles, span);
+        if (cut.tokens == 64)
+            router_logits_kernel<2><<<blocks, kGemmThreads, 0, s>>>(S, cut, P, (const char*)x, (const char*)w, tiles, across, span);
+        else
+            router_logits_kernel<MS_MF><<<blocks, kGemmThreads, 0, s>>>(S, cut, P, (const char*)x, (const char*)w, tiles, across, span);
     });
     if (e != hipSuccess) return e;
     return by_experts<GoChoose>(S.E, S, rule, cut, P, ChooseArgs{(const u32x4*)x, (const u32x4*)w, idx, gate, logits}, s);
@@ -614,8 +744,11 @@ hipError_t launch_router_backward(const RouterShape& S, const Rule& rule, const 
     hipError_t e = by_experts<GoDlogits>(S.E, S, rule, grad_gate, logits, idx, grad_logits, dl, g.ld, s);
     if (e == hipSuccess && grad_x) {
         const int across = (int)up(S.H, kTileFeatures);
-        e = launch_spans(places(up(S.T, Lds<true>::kRows), across), kGemmThreads, [&](dim3 grid, GridSpan span) {
-            router_grad_x_kernel<true><<<grid, kGemmThreads, 0, s>>>(S, (const char*)dl, g.ld, (const char*)w,
+#ifndef MS_GXS
+#define MS_GXS true
+#endif
+        e = launch_spans(places(up(S.T, Lds<MS_GXS>::kRows), across), kGemmThreads, [&](dim3 grid, GridSpan span) {
+            router_grad_x_kernel<MS_GXS><<<grid, kGemmThreads, 0, s>>>(S, (const char*)dl, g.ld, (const char*)w,
                                                                      (const char*)grad_x_in, (char*)grad_x, across, span);
         });
     }

@@ -80,15 +80,6 @@ def test_what_a_step_refuses():
     assert step(tensor(optim, v_scale=BASE + (5 << 30) + 28), eight) == bad   # m_scale's last
 
 
-def test_chunks_of_all_tensors_are_counted():
-    ms, optim, lib = _ms()
-    n = (1 << 40) - 1
-    many = (optim._Tensor * 20)(*[tensor(optim, n, **{name: BASE + ((i * 16 + j) << 44) for j, name in enumerate(
-        ("p", "copy", "g", "m", "v"))}) for i in range(20)])
-    p = params(optim)
-    assert lib.moe_adamw_step(many, 20, ctypes.byref(p), None) == ms.E_OVERFLOW
-
-
 def test_what_pack_and_unpack_refuse():
     ms, optim, lib = _ms()
     calls = {"pack": lambda t, count=1: lib.moe_adamw_pack(ctypes.byref(t), count, None),

@@ -4,7 +4,8 @@
 //            blocks where there are few tiles (partial sums in fp32 in the workspace)
 //   choose   a wave a row: the partial sums' sum, the k largest keys, the gates
 //   dlogits  a wave a row: the gates' gradients to the logits', bf16
-//   grad_x   dl W by tiles, grad_x_in added in fp32 before the one rounding
+//   grad_x   grad_x_in + dl W, added in fp32 before the one rounding: by tiles, or, where dl has k numbers a row, a sum
+//            of k rows of W a row
 //   grad_w   dl^T x by tiles, T split over blocks, and the sum of their parts
 //
 // The choice has to be that of exact sums, and matrix instructions sum in fp32.  So `choose` knows how far a logit may
@@ -137,6 +138,7 @@ __global__ __launch_bounds__(kGemmThreads, MF <= 2 ? 4 : 2) void router_logits_k
 // ---- the choice ----
 
 constexpr int kChooseWaves = 4;
+constexpr int kAtOnce = 8;  // partial sums on their way
 
 // Vectors [from, to) of x . w[e] in 64 bits for two experts, the same in every lane.
 __device__ __forceinline__ void exact_logits(const u32x4* x, const u32x4* w, int e0, int e1, int V, int from, int to,
@@ -236,6 +238,15 @@ __device__ __forceinline__ void order(unsigned& a, unsigned& b, int& ea, int& eb
     ea = e;
 }
 
+// Which experts a lane has of a row: Each of them, four neighbours at a time (16 bytes of partial sums).
+template <int Each>
+struct Own {
+    static constexpr int kRun = Each < 4 ? Each : 4;
+    static __device__ __forceinline__ int expert(int i) { return (i / kRun * kWave + lane_id()) * kRun + i % kRun; }
+    static __device__ __forceinline__ int lane(int e) { return e / kRun & (kWave - 1); }
+    static __device__ __forceinline__ int place(int e) { return e / (kRun * kWave) * kRun + e % kRun; }
+};
+
 constexpr int kAgain = 16;  // candidates of a row that are summed again, at most; with more, all its experts are
 
 // A wave a row; Each logits a lane.
@@ -258,28 +269,38 @@ __global__ __launch_bounds__(kChooseWaves * kWave, Each <= 4 ? 8 : 1) void route
     unsigned my_key = 0;
     unsigned long long again = 0;
     if (row) {
-        float x2 = 0, w2 = 0;
+        // the parts of the norms a lane each, those of the logits eight at a time
         const int across = (E + kTileFeatures - 1) / kTileFeatures;
-#pragma unroll 4
+        float x2 = 0, w2 = 0;
+        if (lane < cut.splits) {
+            x2 = P.x2[(int64_t)lane * S.T + t];
+            for (int c = 0; c < across; ++c) w2 = fmaxf(w2, P.w2[lane * across + c]);
+        }
+        typedef float run_t __attribute__((ext_vector_type(Own<Each>::kRun == 1 ? 2 : Own<Each>::kRun)));
+        constexpr int kRun = Own<Each>::kRun;
+        // past the last expert there are zeros up to ld, a multiple of 4; past that the row's first again
+#pragma unroll kAtOnce
         for (int s = 0; s < cut.splits; ++s) {
             const float* const from = sums + s * next;
 #pragma unroll
-            for (int i = 0; i < Each; ++i) {
-                const unsigned e = lane + i * kWave;
-                if (e < (unsigned)E) l[i] += from[e];
+            for (int i = 0; i < Each; i += kRun) {
+                const int e = Own<Each>::expert(i), at = e < cut.ld ? e : 0;
+                if constexpr (kRun == 1) {
+                    l[i] += from[at];
+                } else {
+                    const run_t v = *(const run_t*)(from + at);
+#pragma unroll
+                    for (int c = 0; c < kRun; ++c) l[i + c] += v[c];
+                }
             }
-            x2 += P.x2[(int64_t)s * S.T + t];
-            float most = P.w2[s * across];
-            for (int c = 1; c < across; ++c) most = fmaxf(most, P.w2[s * across + c]);
-            w2 += most;
         }
+        x2 = wave_total(x2);
+        w2 = wave_total(w2);
         if (A.logits) {
             float* const to = A.logits + t * E;
 #pragma unroll
-            for (int i = 0; i < Each; ++i) {
-                const unsigned e = lane + i * kWave;
-                if (e < (unsigned)E) to[e] = l[i];
-            }
+            for (int i = 0; i < Each; ++i)
+                if (Own<Each>::expert(i) < E) to[Own<Each>::expert(i)] = l[i];
         }
         // how far a key may be off.  Squares that underflow say nothing, unless all is zero
         const bool tiny = x2 < 8e-25f || w2 < 8e-25f;
@@ -306,8 +327,8 @@ __global__ __launch_bounds__(kChooseWaves * kWave, Each <= 4 ? 8 : 1) void route
             float most_bias = 0;
 #pragma unroll
             for (int i = 0; i < Each; ++i) {
-                const unsigned e = lane + i * kWave;
-                const float b = e < (unsigned)E ? rule.bias[e] : 0.0f;
+                const int e = Own<Each>::expert(i);
+                const float b = e < E ? rule.bias[e] : 0.0f;
                 if (fabsf(b) <= 3.4e38f) most_bias = fmaxf(most_bias, fabsf(b));
                 // the hardware's exponential and reciprocal: with the argument's rounding under 8e-7 of a sigmoid
                 v[i] = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.442695041f * l[i])) + b;
@@ -318,7 +339,7 @@ __global__ __launch_bounds__(kChooseWaves * kWave, Each <= 4 ? 8 : 1) void route
         widest = rule.bias ? 0.25f * off + rounds : off;
 #pragma unroll
         for (int i = 0; i < Each; ++i) {
-            expert[i] = lane + i * kWave;
+            expert[i] = Own<Each>::expert(i);
             key[i] = expert[i] < E ? ordered_key32(v[i]) : 0;
         }
         // a lane's keys in order, so that only the first of each is looked at
@@ -432,20 +453,20 @@ __global__ __launch_bounds__(kChooseWaves * kWave, Each <= 4 ? 8 : 1) void route
     if (!rule.sigmoid) {
 #pragma unroll
         for (int i = 0; i < Each; ++i)
-            if (lane + i * kWave < E) most = fmaxf(most, l[i]);
+            if (Own<Each>::expert(i) < E) most = fmaxf(most, l[i]);
         most = wave_max(most);
         if (!rule.normalize) {
 #pragma unroll
             for (int i = 0; i < Each; ++i)
-                if (lane + i * kWave < E) all += expf(l[i] - most);
+                if (Own<Each>::expert(i) < E) all += expf(l[i] - most);
             all = wave_total(all);
         }
     }
     float its = 0;  // the logit of lane j's slot
 #pragma unroll
     for (int i = 0; i < Each; ++i) {
-        const float v = __shfl(l[i], chosen & (kWave - 1), kWave);
-        if (chosen / kWave == i) its = v;
+        const float v = __shfl(l[i], Own<Each>::lane(chosen), kWave);
+        if (Own<Each>::place(chosen) == i) its = v;
     }
     const float g = gate_of(rule, k, its, most, all);
     if (lane < k) {
@@ -456,13 +477,16 @@ __global__ __launch_bounds__(kChooseWaves * kWave, Each <= 4 ? 8 : 1) void route
 
 // ---- the backward pass ----
 
-// dl of a row, bf16, zeros from E to ld (a multiple of 8).
+// dl of a row as two bf16 numbers, the second what the first leaves: [2][T][ld], zeros from E to ld (a multiple of 8).
+// The products below take both, so that 16 bits of dl reach the gradients; with the first alone their error against 64
+// bits is 1.4 to 1.5 times that of rounding them to bf16.
 template <int Each>
 __global__ __launch_bounds__(kChooseWaves * kWave) void router_dlogits_kernel(RouterShape S, Rule rule,
                                                                               const float* grad_gate,
                                                                               const float* logits, const int32_t* idx,
                                                                               const float* grad_logits,
-                                                                              unsigned short* dl, int ld, GridSpan span)
+                                                                              unsigned short* dl, int ld, float* few,
+                                                                              GridSpan span)
 {
     __shared__ float ds[kChooseWaves][Each * kWave];
     const int lane = lane_id(), E = S.E, k = S.k;
@@ -495,7 +519,10 @@ __global__ __launch_bounds__(kChooseWaves * kWave) void router_dlogits_kernel(Ro
         g = (g - wave_total(g * s) / total) / total;
         if (!in) g = 0.0f;
     }
-    const float mean = rule.sigmoid ? 0.0f : wave_total(g * s);
+    // normalized, the chosen scores' sum does not change: the mean is 0, and so is dl of the others
+    const float mean = rule.sigmoid || rule.normalize ? 0.0f : wave_total(g * s);
+    if (few && lane < k) few[t * k + lane] = rule.sigmoid ? (in ? g * s * (1.0f - s) : 0.0f) : in ? s * g : 0.0f;
+    if (!dl) return;
     if (in) mine[e] = g;
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // this wave's own LDS
 #pragma unroll
@@ -511,12 +538,16 @@ __global__ __launch_bounds__(kChooseWaves * kWave) void router_dlogits_kernel(Ro
                     const float s = score(l[i]);
                     d = g * s * (1.0f - s);
                 }
-            } else {
+            } else if (g != mean) {
                 d = score(l[i]) * (g - mean);
             }
             if (grad_logits) d += grad_logits[t * E + e];
         }
-        dl[t * ld + e] = (unsigned short)bf16_pack2(d, d);
+        const unsigned first = bf16_pack2(d, d) & 0xffffu;
+        // beside an infinite or NaN first part the second would make a NaN of it
+        const float left = fabsf(d) <= 3.38e38f ? d - __uint_as_float(first << 16) : 0.0f;
+        dl[t * ld + e] = (unsigned short)first;
+        dl[((int64_t)S.T + t) * ld + e] = (unsigned short)bf16_pack2(left, left);
     }
 }
 
@@ -527,6 +558,21 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* p, int64_t 
                        (uint64_t)(unsigned)__builtin_amdgcn_readfirstlane((int)(a >> 32)) << 32;
     return __builtin_amdgcn_make_buffer_rsrc((void*)q, 0, __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000);
 }
+
+// An operand whose tiles of k come twice in a row, the second time `plane` bytes further on.
+template <class Base>
+struct Twice : Base {
+    int64_t plane;
+
+    template <int N>
+    __device__ __forceinline__ void load(int s, int kt, unsigned lds) const
+    {
+        Base b = *this;
+        b.p[s] += (kt & 1) * plane;
+        b.template load<N>(s, kt >> 1, lds);
+    }
+};
+__device__ __forceinline__ int twice(int K) { return (K + kTileK - 1) / kTileK * kTileK * 2; }
 
 // grad_x = grad_x_in + dl W, a tile of rows and 256 columns a block.
 template <bool Small>
@@ -539,16 +585,18 @@ __global__ __launch_bounds__(kGemmThreads, Small ? 4 : 2) void router_grad_x_ker
     const int row0 = at.tile * Lds<Small>::kRows, nr = min(Lds<Small>::kRows, S.T - row0);
     if (nr <= 0) return;
     const int n0 = at.across * kTileFeatures, H = S.H, valid = min(H - n0, kTileFeatures), lane = lane_id();
-    KContiguous r;
+    Twice<KContiguous> r;
     r.init(ld, ld);
-    KStrided f;
+    r.plane = (int64_t)S.T * ld * 2;
+    Twice<KStrided> f;
     f.init(H, S.E);
+    f.plane = 0;
     for (int i = 0; i < 2; ++i) f.slot(i, w + (n0 + 128 * i) * 2, H - n0 - 128 * i);
     with_rows<Small>(nr, [&](auto mf) {
         constexpr int MF = decltype(mf)::value;
         Acc<MF> acc;
         row_slots<MF>(r, dl + (int64_t)row0 * ld * 2, ld, nr);
-        tile_product<Small, MF>(r, f, S.E, lds, acc);
+        tile_product<Small, MF>(r, f, twice(S.E), lds, acc);
         const int64_t first = (int64_t)row0 * H + n0;
         const __amdgpu_buffer_rsrc_t add = buffer(in ? in + first * 2 : nullptr, in ? ((int64_t)nr * H - n0) * 2 : 0);
         write_tile<MF>(lds, nr, valid, out + first * 2, (int64_t)H * 2, [&](int m, int n) {
@@ -559,6 +607,53 @@ __global__ __launch_bounds__(kGemmThreads, Small ? 4 : 2) void router_grad_x_ker
             return pack4(f32x4{v[0] + bf16_lo(d[0]), v[1] + bf16_hi(d[0]), v[2] + bf16_lo(d[1]), v[3] + bf16_hi(d[1])});
         });
     });
+}
+
+// grad_x = grad_x_in + sum over j of few[t][j] W[idx[t][j]]: a wave makes 512 columns of a row.  W is read k times a row,
+// from the L2s: all blocks work on one piece of 512 columns before the next, so that each L2 holds the few hundred
+// kilobytes of W that are needed.  A row's ids and factors are a lane's each, and come back as scalars.
+__global__ __launch_bounds__(256) void router_gather_kernel(RouterShape S, const float* few, const int32_t* idx,
+                                                            const u32x4* w, const u32x4* in, u32x4* out, GridSpan span)
+{
+    const int t = span_block(span), lane = lane_id(), V = S.H / 8, k = S.k;
+    const unsigned v0 = (blockIdx.y * (256 / kWave) + wave_id()) * kWave, v = v0 + lane;
+    if (v0 >= (unsigned)V) return;
+    const unsigned at = min(v, (unsigned)V - 1);  // past the row's end its last vector
+    int id = 0;
+    float f = 0;
+    if (lane < k) {
+        const int e = idx[(int64_t)t * k + lane];
+        if ((unsigned)e < (unsigned)S.E) {  // a bad id counts as none
+            id = e;
+            f = few[(int64_t)t * k + lane];
+        }
+    }
+    u32x4 add = {0, 0, 0, 0};
+    if (in) add = load_row16<true>(in + (int64_t)t * V + at);
+    float sum[8] = {};
+    const auto some = [&](auto count, int j0) {
+        constexpr int N = decltype(count)::value;
+        u32x4 row[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) row[j] = (w + (int64_t)__builtin_amdgcn_readlane(id, j0 + j) * V)[at];
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const float d = __uint_as_float((unsigned)__builtin_amdgcn_readlane((int)__float_as_uint(f), j0 + j));
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                sum[2 * c] = fmaf(d, bf16_lo(row[j][c]), sum[2 * c]);
+                sum[2 * c + 1] = fmaf(d, bf16_hi(row[j][c]), sum[2 * c + 1]);
+            }
+        }
+    };
+    int j = 0;
+    for (; j + 8 <= k; j += 8) some(std::integral_constant<int, 8>(), j);
+    for (; j + 2 <= k; j += 2) some(std::integral_constant<int, 2>(), j);
+    if (j < k) some(std::integral_constant<int, 1>(), j);
+    u32x4 r;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) r[c] = bf16_pack2(sum[2 * c] + bf16_lo(add[c]), sum[2 * c + 1] + bf16_hi(add[c]));
+    if (v < (unsigned)V) store_row16<true>(r, out + (int64_t)t * V + v);
 }
 
 // Part `blockIdx / tiles` of dl^T x: rows [part * each, ...) of both, 256 experts by 256 columns a block, fp32.
@@ -572,15 +667,17 @@ __global__ __launch_bounds__(kGemmThreads, 2) void router_grad_w_kernel(RouterSh
     const int n0 = tile % across * kTileFeatures, H = S.H, E = S.E, lane = lane_id();
     const int64_t t0 = (int64_t)part * each;
     const int K = (int)min((int64_t)each, S.T - t0), nr = min(kTileRows, E - e0);
-    KStrided r, f;
+    Twice<KStrided> r, f;
     r.init(ld, K);
+    r.plane = (int64_t)S.T * ld * 2;
     f.init(H, K);
+    f.plane = 0;
     for (int i = 0; i < 2; ++i) f.slot(i, x + (t0 * H + n0 + 128 * i) * 2, H - n0 - 128 * i);
     with_rows<false>(nr, [&](auto mf) {
         constexpr int MF = decltype(mf)::value, kFirst = 32 * low_rows(MF);
         Acc<MF> acc;
         for (int i = 0; i < 2; ++i) r.slot(i, dl + (t0 * ld + e0 + kFirst * i) * 2, ld - e0 - kFirst * i);
-        tile_product<false, MF>(r, f, K, lds, acc);
+        tile_product<false, MF>(r, f, twice(K), lds, acc);
         // rows past the experts' last lie past the descriptor's end: nothing is written
         const __amdgpu_buffer_rsrc_t to = buffer(parts + ((int64_t)part * E + e0) * H + n0, ((int64_t)nr * H - n0) * 4);
 #pragma unroll
@@ -616,11 +713,10 @@ int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 Cut cut_of(const RouterShape& S)
 {
-#ifndef MS_MF
-#define MS_MF 4
-#endif
     Cut c;
-    c.tokens = S.T >= 4096 ? 32 * MS_MF : 64;
+    // tiles of 128 rows against 64, both kernels, us: H = 7168, 256 experts: 1024 rows 49 / 48, 2048 51 / 54, 8192 73 / 79;
+    // H = 4096, 128 experts: 2048 rows 37 / 37, 4096 34 / 35, 16384 69 / 75
+    c.tokens = S.T >= 2048 ? 128 : 64;
     const int64_t tiles = up(S.T, c.tokens) * up(S.E, kTileFeatures);
     const int kBlocks = c.tokens > 64 ? 256 : 512;
     int splits = 1;
@@ -684,11 +780,12 @@ struct GoChoose {
 template <int Each>
 struct GoDlogits {
     static hipError_t go(const RouterShape& S, const Rule& rule, const float* grad_gate, const float* logits,
-                         const int32_t* idx, const float* grad_logits, unsigned short* dl, int ld, hipStream_t s)
+                         const int32_t* idx, const float* grad_logits, unsigned short* dl, int ld, float* few,
+                         hipStream_t s)
     {
         return launch_spans(up(S.T, kChooseWaves), kChooseWaves * kWave, [&](dim3 grid, GridSpan span) {
             router_dlogits_kernel<Each><<<grid, kChooseWaves * kWave, 0, s>>>(S, rule, grad_gate, logits, idx, grad_logits,
-                                                                              dl, ld, span);
+                                                                              dl, ld, few, span);
         });
     }
 };
@@ -705,7 +802,8 @@ size_t router_workspace(const RouterShape& S, bool backward)
     }
     if (backward && S.T > 0) {
         const GradCut g = grad_cut(S);
-        const size_t b = align256((size_t)S.T * g.ld * 2) + align256((size_t)g.splits * S.E * S.H * 4);
+        const size_t b = align256((size_t)S.T * g.ld * 4) + align256((size_t)g.splits * S.E * S.H * 4) +
+                         align256((size_t)S.T * S.k * 4);
         if (b > n) n = b;
     }
     return n;
@@ -726,7 +824,7 @@ hipError_t launch_router_forward(const RouterShape& S, const Rule& rule, const v
         if (cut.tokens == 64)
             router_logits_kernel<2><<<blocks, kGemmThreads, 0, s>>>(S, cut, P, (const char*)x, (const char*)w, tiles, across, span);
         else
-            router_logits_kernel<MS_MF><<<blocks, kGemmThreads, 0, s>>>(S, cut, P, (const char*)x, (const char*)w, tiles, across, span);
+            router_logits_kernel<4><<<blocks, kGemmThreads, 0, s>>>(S, cut, P, (const char*)x, (const char*)w, tiles, across, span);
     });
     if (e != hipSuccess) return e;
     return by_experts<GoChoose>(S.E, S, rule, cut, P, ChooseArgs{(const u32x4*)x, (const u32x4*)w, idx, gate, logits}, s);
@@ -738,17 +836,23 @@ hipError_t launch_router_backward(const RouterShape& S, const Rule& rule, const 
 {
     const GradCut g = S.T ? grad_cut(S) : GradCut{};
     unsigned short* const dl = (unsigned short*)ws;
-    float* const parts = (float*)(ws + align256((size_t)S.T * g.ld * 2));
+    float* const parts = (float*)(ws + align256((size_t)S.T * g.ld * 4));
     if (S.T == 0)  // no part: zeros
         return grad_w ? join(parts, 0, S, grad_w, s) : hipSuccess;
-    hipError_t e = by_experts<GoDlogits>(S.E, S, rule, grad_gate, logits, idx, grad_logits, dl, g.ld, s);
-    if (e == hipSuccess && grad_x) {
+    const bool sparse = (rule.sigmoid || rule.normalize) && !grad_logits;
+    float* const few = sparse && grad_x ? (float*)((char*)parts + align256((size_t)g.splits * S.E * S.H * 4)) : nullptr;
+    hipError_t e = by_experts<GoDlogits>(S.E, S, rule, grad_gate, logits, idx, grad_logits,
+                                         grad_w || !few ? dl : nullptr, g.ld, few, s);
+    if (e == hipSuccess && few) {
+        const unsigned pieces = (unsigned)up(S.H / 8, 256);
+        e = launch_spans(S.T, 256, [&](dim3 grid, GridSpan span) {
+            router_gather_kernel<<<dim3(grid.x, pieces), 256, 0, s>>>(S, few, idx, (const u32x4*)w, (const u32x4*)grad_x_in,
+                                                                      (u32x4*)grad_x, span);
+        });
+    } else if (e == hipSuccess && grad_x) {
         const int across = (int)up(S.H, kTileFeatures);
-#ifndef MS_GXS
-#define MS_GXS true
-#endif
-        e = launch_spans(places(up(S.T, Lds<MS_GXS>::kRows), across), kGemmThreads, [&](dim3 grid, GridSpan span) {
-            router_grad_x_kernel<MS_GXS><<<grid, kGemmThreads, 0, s>>>(S, (const char*)dl, g.ld, (const char*)w,
+        e = launch_spans(places(up(S.T, Lds<true>::kRows), across), kGemmThreads, [&](dim3 grid, GridSpan span) {
+            router_grad_x_kernel<true><<<grid, kGemmThreads, 0, s>>>(S, (const char*)dl, g.ld, (const char*)w,
                                                                      (const char*)grad_x_in, (char*)grad_x, across, span);
         });
     }

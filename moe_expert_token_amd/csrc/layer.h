@@ -29,9 +29,7 @@ struct LayerShape {
     float c0, c1;            // the gate's sigmoid argument: c0 g + c1 g^3
     unsigned long long* key;  // [T][E], ordered_key of each expert's key
     float* logit;             // [T][E]
-    unsigned long long* tokens;  // [E] bit t: token t goes to this expert
-    int* first;               // [E] the first row of an expert, rows in the order of experts, then tokens
-    int* tile;                // [<= P] expert | part << 16
+    int4* tile;               // [<= P] expert, first row, rows; rows are in the order of experts, then tokens
     int* tiles;               // [1] how many
     int* row_of;              // [P] the row of (token, slot)
     float* gate;              // [P]

@@ -126,66 +126,154 @@ struct Choice {
     int tiles;
 };
 
-// The k largest of a token's E keys, by one wave with Each keys a lane: its bit in the experts' words, and lane j's
-// expert of slot j.
-template <int Each>
-__device__ __forceinline__ int choose_token(const LayerShape& S, int t, Choice& C)
+// Sorts two keys with their experts, the larger first; of equal ones the one that comes first stays first.
+__device__ __forceinline__ void order(unsigned long long& a, unsigned long long& b, int& ea, int& eb)
 {
-    const int lane = lane_id();
-    unsigned long long key[Each];
-#pragma unroll
-    for (int i = 0; i < Each; ++i) {
-        const int e = lane + i * kWave;
-        key[i] = e < S.E ? S.key[(int64_t)t * S.E + e] : 0;
-    }
-    int chosen = 0;
-    for (int j = 0; j < S.k; ++j) {
-        unsigned long long best = key[0];
-        int at = lane;
-#pragma unroll
-        for (int i = 1; i < Each; ++i)
-            if (key[i] > best) { best = key[i]; at = lane + i * kWave; }
-        const int e = wave_argmax(best, at);
-        if (lane == j) chosen = e;
-#pragma unroll
-        for (int i = 0; i < Each; ++i)
-            if (lane + i * kWave == e) key[i] = 0;
-        if (lane == 0) atomicOr(&C.tokens[e], 1ull << t);
-    }
-    return chosen;
+    const bool swap = b > a || (b == a && eb < ea);
+    const unsigned long long k = swap ? b : a;
+    const int e = swap ? eb : ea;
+    b = swap ? a : b;
+    eb = swap ? ea : eb;
+    a = k;
+    ea = e;
 }
 
-// Chooses the experts of all tokens and lists the tiles of up to `rows` rows.  The first block writes the choice down,
-// for the kernel that follows and for the user.  (A block more that does nothing else is a round more where the others
-// fill the card: 37.5 us against 31.8, one token, 256 4-bit experts of 7168 x 2048.)
+// The k largest of the E keys of N tokens, by one wave with Each keys of a token a lane: the tokens' bits in the experts'
+// words, and lane j's expert of slot j.  A choice is a chain of some twenty dependent steps, so two tokens go side by side.
+template <int Each, int N>
+__device__ __forceinline__ void choose_tokens(const LayerShape& S, const int (&t)[N], Choice& C, int (&chosen)[N])
+{
+    const int lane = lane_id();
+    unsigned long long key[N][Each];
+    int expert[N][Each];
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int i = 0; i < Each; ++i) {
+            const int e = lane + i * kWave;
+            expert[n][i] = e;
+            key[n][i] = S.key[(int64_t)t[n] * S.E + min(e, S.E - 1)];
+            if (e >= S.E) key[n][i] = 0;
+        }
+    if constexpr (Each == 4) {  // a lane's keys in order, so that only the first is looked at
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            order(key[n][0], key[n][1], expert[n][0], expert[n][1]);
+            order(key[n][2], key[n][3], expert[n][2], expert[n][3]);
+            order(key[n][0], key[n][2], expert[n][0], expert[n][2]);
+            order(key[n][1], key[n][3], expert[n][1], expert[n][3]);
+            order(key[n][1], key[n][2], expert[n][1], expert[n][2]);
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < N; ++n) chosen[n] = 0;
+#pragma unroll 1
+    for (int j = 0; j < S.k; ++j) {
+        unsigned long long best[N], tie[N];
+        unsigned top[N];
+        int at[N], e[N];
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            best[n] = key[n][0];
+            at[n] = expert[n][0];
+            if constexpr (Each > 4) {
+#pragma unroll
+                for (int i = 1; i < Each; ++i)
+                    if (key[n][i] > best[n]) { best[n] = key[n][i]; at[n] = expert[n][i]; }
+            }
+            top[n] = wave_max((unsigned)(best[n] >> 32));
+        }
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            tie[n] = __ballot((unsigned)(best[n] >> 32) == top[n]);
+            e[n] = __builtin_amdgcn_readlane(at[n], __builtin_ctzll(tie[n]));
+            if (tie[n] & (tie[n] - 1)) e[n] = wave_argmax(best[n], at[n]);
+            if (lane == j) chosen[n] = e[n];
+            if constexpr (Each > 4) {
+#pragma unroll
+                for (int i = 0; i < Each; ++i)
+                    if (expert[n][i] == e[n]) key[n][i] = 0;
+            } else {
+                const bool pop = at[n] == e[n];
+#pragma unroll
+                for (int i = 0; i < Each; ++i) {
+                    const int from = i + 1 < Each ? i + 1 : i;
+                    key[n][i] = pop ? (i + 1 < Each ? key[n][from] : 0) : key[n][i];
+                    expert[n][i] = pop ? (i + 1 < Each ? expert[n][from] : -1) : expert[n][i];
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+        if (lane < S.k) atomicOr(&C.tokens[chosen[n]], 1ull << t[n]);
+}
+
+// The gates of a token, for the kernel that follows and for the user: lane j's of slot j.
+__device__ __forceinline__ void write_gates(const LayerShape& S, const Rule& rule, int t, int chosen, int32_t* topk_idx,
+                                            float* topk_w)
+{
+    const int lane = lane_id(), E = S.E, k = S.k;
+    const float* const l = S.logit + (int64_t)t * E;
+    float most = -__builtin_inff(), all = 0;
+    if (!rule.sigmoid) {
+        for (int e = lane; e < E; e += kWave) most = fmaxf(most, l[e]);
+        most = wave_max(most);
+        if (!rule.normalize) {
+            for (int e = lane; e < E; e += kWave) all += expf(l[e] - most);
+            all = wave_total(all);
+        }
+    }
+    const float w = gate_of(rule, k, l[chosen], most, all);
+    if (lane < k) {
+        S.gate[t * k + lane] = w;
+        if (topk_idx) topk_idx[t * k + lane] = chosen;
+        if (topk_w) topk_w[t * k + lane] = w;
+    }
+}
+
+// Rows of an expert's tile p of `rows`: the first and how many.
+__device__ __forceinline__ int tile_rows(unsigned long long tokens, int rows, int p)
+{
+    return min(rows, (int)__popcll(tokens) - p * rows);
+}
+
+// Chooses the experts of all tokens and lists the tiles of up to `rows` rows.  What the kernel that follows needs of it is
+// written down once: by block t for token t, by the first block for all.  (A block more that does nothing else is a
+// round more where the others fill the card: 37.5 us against 31.8, one token, 256 4-bit experts of 7168 x 2048.)
 __device__ __forceinline__ void choose(const LayerShape& S, const Rule& rule, int rows, Choice& C, int32_t* topk_idx,
                                        float* topk_w)
 {
     const int lane = lane_id(), wave = wave_id(), E = S.E, k = S.k;
-    const bool write = blockIdx.x == 0;
     for (int e = threadIdx.x; e < E; e += kThreads) C.tokens[e] = 0;
     __syncthreads();
-    for (int t = wave; t < S.T; t += kWaves) {
-        const int chosen = E <= 64 ? choose_token<1>(S, t, C) : E <= 256 ? choose_token<4>(S, t, C) : choose_token<16>(S, t, C);
-        if (!write) continue;
-        const float* const l = S.logit + (int64_t)t * E;
-        float most = -__builtin_inff(), all = 0;
-        if (!rule.sigmoid) {
-            for (int e = lane; e < E; e += kWave) most = fmaxf(most, l[e]);
-            most = wave_max(most);
-            if (!rule.normalize) {
-                for (int e = lane; e < E; e += kWave) all += expf(l[e] - most);
-                all = wave_total(all);
+    const auto some = [&](auto each) {
+        constexpr int Each = decltype(each)::value, N = Each > 4 ? 1 : 2;
+#pragma unroll 1
+        for (int t0 = wave; t0 < S.T; t0 += N * kWaves) {
+            int chosen[N], t[N];
+            if (N == 1 || t0 + kWaves >= S.T) {
+                int one[1] = {t0}, its[1];
+                choose_tokens<Each, 1>(S, one, C, its);
+                t[0] = t0;
+                chosen[0] = its[0];
+                if (N > 1) t[N - 1] = -1;
+            } else {
+#pragma unroll
+                for (int n = 0; n < N; ++n) t[n] = t0 + n * kWaves;
+                choose_tokens<Each, N>(S, t, C, chosen);
+            }
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                if (t[n] < 0 || t[n] % (int)gridDim.x != (int)blockIdx.x) continue;
+                write_gates(S, rule, t[n], chosen[n], topk_idx, topk_w);
+                if (lane < k) S.row_of[t[n] * k + lane] = chosen[n];  // its row, once the first rows are known
             }
         }
-        const float w = gate_of(rule, k, l[chosen], most, all);
-        if (lane < k) {
-            S.gate[t * k + lane] = w;
-            if (topk_idx) topk_idx[t * k + lane] = chosen;
-            if (topk_w) topk_w[t * k + lane] = w;
-            S.row_of[t * k + lane] = chosen;  // its row, once the first rows are known
-        }
-    }
+    };
+    if (E <= 64) some(std::integral_constant<int, 1>());
+    else if (E <= 256) some(std::integral_constant<int, 4>());
+    else some(std::integral_constant<int, 16>());
     __syncthreads();
     // rows and tiles before each expert, two experts a thread, counted together: 512 at most of each
     int count[2], sum = 0;
@@ -213,29 +301,23 @@ __device__ __forceinline__ void choose(const LayerShape& S, const Rule& rule, in
     }
     if (threadIdx.x == 0) C.tiles = total >> 16;
     __syncthreads();
-    if (!write) return;
-    for (int e = threadIdx.x; e < E; e += kThreads) {
-        S.tokens[e] = C.tokens[e];
-        S.first[e] = C.first[e];
+    for (int t = blockIdx.x; t < S.T; t += gridDim.x)
+        for (int j = threadIdx.x; j < k; j += kThreads) {
+            const int e = S.row_of[t * k + j];
+            S.row_of[t * k + j] = C.first[e] + __popcll(C.tokens[e] & ((1ull << t) - 1));
+        }
+    if (blockIdx.x) return;
+    for (int i = threadIdx.x; i < C.tiles; i += kThreads) {
+        const int e = C.tile[i] & 0xffff, p = C.tile[i] >> 16;
+        S.tile[i] = make_int4(e, C.first[e] + p * rows, tile_rows(C.tokens[e], rows, p), 0);
     }
-    for (int i = threadIdx.x; i < C.tiles; i += kThreads) S.tile[i] = C.tile[i];
     if (threadIdx.x == 0) *S.tiles = C.tiles;
-    for (int p = threadIdx.x; p < S.P; p += kThreads) {
-        const int e = S.row_of[p], t = p / k;
-        S.row_of[p] = C.first[e] + __popcll(C.tokens[e] & ((1ull << t) - 1));
-    }
 }
 
 struct Weights {
     const char *w, *scale;
     int across;  // blocks over the features
 };
-
-// Rows of an expert's tile p of `rows`: the first and how many.
-__device__ __forceinline__ int tile_rows(unsigned long long tokens, int rows, int p)
-{
-    return min(rows, (int)__popcll(tokens) - p * rows);
-}
 
 template <int Group, int Rows, int Ways, bool Whole, bool Staged>
 __global__ __launch_bounds__(kThreads, Rows == 16 ? 4 : 2) void layer_up_kernel(LayerShape S, Rule rule, const char* x, Weights A,
@@ -315,18 +397,19 @@ __device__ __forceinline__ void combine(const LayerShape& S, const int* row_of, 
     const __amdgpu_buffer_rsrc_t rows = rows_of(S.y, (int64_t)S.P * S.H * 4);
     for (int i = threadIdx.x; i < S.T * quads; i += kThreads) {
         const int t = i / quads, n = n0 + 4 * (i - t * quads);
+        const int64_t at = (int64_t)t * S.H + n;
+        u32x2 r = {0, 0};
+        if (residual) r = *(const u32x2*)((const unsigned short*)residual + at);
         f32x4 sum = {0, 0, 0, 0};
 #pragma unroll 8
         for (int j = 0; j < S.k; ++j) {
             const float w = gate[t * S.k + j];
-            const unsigned at = ((unsigned)row_of[t * S.k + j] * S.H + n) * 4;
-            const f32x4 y = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rows, at, 0, kAgent));
+            const unsigned from = ((unsigned)row_of[t * S.k + j] * S.H + n) * 4;
+            const f32x4 y = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rows, from, 0, kAgent));
 #pragma unroll
             for (int c = 0; c < 4; ++c) sum[c] = fmaf(w, y[c], sum[c]);
         }
-        const int64_t at = (int64_t)t * S.H + n;
         if (residual) {
-            const u32x2 r = *(const u32x2*)((const unsigned short*)residual + at);
             sum[0] += bf16_lo(r[0]);
             sum[1] += bf16_hi(r[0]);
             sum[2] += bf16_lo(r[1]);
@@ -352,9 +435,9 @@ __global__ __launch_bounds__(kThreads, Rows == 16 ? 4 : 2) void layer_down_kerne
     const int tiles = *S.tiles, items = tiles * A.across;
     for (int item = blockIdx.x; item < items; item += gridDim.x) {
         const int tile = item / A.across, place = item - tile * A.across;
-        const int what = S.tile[tile], e = what & 0xffff, p = what >> 16;
-        const int nr = __builtin_amdgcn_readfirstlane(tile_rows(S.tokens[e], Rows, p));
-        const int64_t row0 = S.first[e] + p * Rows;
+        const int4 what = S.tile[tile];
+        const int e = __builtin_amdgcn_readfirstlane(what.x), nr = __builtin_amdgcn_readfirstlane(what.z);
+        const int64_t row0 = __builtin_amdgcn_readfirstlane(what.y);
         Source<Group> from;
         from.init(K);
         from.x.init(S.h + row0 * K * 2, (int64_t)nr * K * 2);
@@ -463,9 +546,7 @@ size_t layer_workspace(LayerShape* S, char* base)
     const size_t T = S->T, E = S->E, P = S->P;
     S->key = (unsigned long long*)take(T * E * 8);
     S->logit = (float*)take(T * E * 4);
-    S->tokens = (unsigned long long*)take(E * 8);
-    S->first = (int*)take(E * 4);
-    S->tile = (int*)take(P * 4);
+    S->tile = (int4*)take(P * 16);
     S->tiles = (int*)take(4);
     S->row_of = (int*)take(P * 4);
     S->gate = (float*)take(P * 4);

@@ -117,6 +117,19 @@ struct LayerSplit {
 
 constexpr int kMaxExperts = 1024;
 
+// Where there is a wave for each token and expert, and their sums are short, a block of the projections makes the scores
+// itself: one launch less.  Us a call in a graph, with and without: one token, 8 experts, H = 128 13.5 / 15.4, 1024 32.8
+// / 34.6, 4096 30.4 / 31.2; four tokens, 8 experts, H = 1024 36.7 / 36.1, 4096 41.4 / 33.1; one token, 64 experts, H = 512
+// 26.4 / 23.8.
+constexpr int kOwnPairs = kWaves;
+constexpr int64_t kOwnProducts = 1 << 15;
+
+bool own_scores(const LayerShape& S)
+{
+    const int64_t pairs = (int64_t)S.T * S.E;
+    return pairs <= kOwnPairs && pairs * S.H <= kOwnProducts;
+}
+
 // What every block of the projections finds out for itself.
 struct Choice {
     unsigned long long tokens[kMaxExperts];
@@ -124,7 +137,33 @@ struct Choice {
     int tile[kLayerPairs];
     int wave_sum[kWaves];
     int tiles;
+    unsigned long long key[kOwnPairs];  // of all tokens and experts, where there are few
+    float logit[kOwnPairs];
 };
+
+__device__ __forceinline__ void own_scores_of(const LayerShape& S, const Rule& rule, const u32x4* x, const u32x4* w,
+                                              Choice& C)
+{
+    const int V = S.H / 8;
+    for (int p = wave_id(); p < S.T * S.E; p += kWaves) {
+        const int t = p / S.E, e = p - t * S.E;
+        double sum = 0;
+        for (int v = lane_id(); v < V; v += kWave) {
+            const u32x4 a = w[(int64_t)e * V + v], b = x[(int64_t)t * V + v];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                sum = fma(as_double(a[c] << 16), as_double(b[c] << 16), sum);
+                sum = fma(as_double(a[c] & 0xffff0000u), as_double(b[c] & 0xffff0000u), sum);
+            }
+        }
+#pragma unroll
+        for (int d = 1; d < kWave; d <<= 1) sum += __shfl_xor(sum, d, kWave);
+        if (lane_id() == 0) {
+            C.logit[p] = (float)sum;
+            C.key[p] = ordered_key(rule.bias ? score64(sum) + (double)rule.bias[e] : sum);
+        }
+    }
+}
 
 // Sorts two keys with their experts, the larger first; of equal ones the one that comes first stays first.
 __device__ __forceinline__ void order(unsigned long long& a, unsigned long long& b, int& ea, int& eb)
@@ -141,7 +180,8 @@ __device__ __forceinline__ void order(unsigned long long& a, unsigned long long&
 // The k largest of the E keys of N tokens, by one wave with Each keys of a token a lane: the tokens' bits in the experts'
 // words, and lane j's expert of slot j.  A choice is a chain of some twenty dependent steps, so two tokens go side by side.
 template <int Each, int N>
-__device__ __forceinline__ void choose_tokens(const LayerShape& S, const int (&t)[N], Choice& C, int (&chosen)[N])
+__device__ __forceinline__ void choose_tokens(const LayerShape& S, bool own, const int (&t)[N], Choice& C,
+                                              int (&chosen)[N])
 {
     const int lane = lane_id();
     unsigned long long key[N][Each];
@@ -152,7 +192,8 @@ __device__ __forceinline__ void choose_tokens(const LayerShape& S, const int (&t
         for (int i = 0; i < Each; ++i) {
             const int e = lane + i * kWave;
             expert[n][i] = e;
-            key[n][i] = S.key[(int64_t)t[n] * S.E + min(e, S.E - 1)];
+            if (Each == 1 && own) key[n][i] = C.key[t[n] * S.E + min(e, S.E - 1)];
+            else key[n][i] = S.key[(int64_t)t[n] * S.E + min(e, S.E - 1)];
             if (e >= S.E) key[n][i] = 0;
         }
     if constexpr (Each == 4) {  // a lane's keys in order, so that only the first is looked at
@@ -210,11 +251,10 @@ __device__ __forceinline__ void choose_tokens(const LayerShape& S, const int (&t
 }
 
 // The gates of a token, for the kernel that follows and for the user: lane j's of slot j.
-__device__ __forceinline__ void write_gates(const LayerShape& S, const Rule& rule, int t, int chosen, int32_t* topk_idx,
-                                            float* topk_w)
+__device__ __forceinline__ void write_gates(const LayerShape& S, const Rule& rule, const float* l, int t, int chosen,
+                                            int32_t* topk_idx, float* topk_w)
 {
     const int lane = lane_id(), E = S.E, k = S.k;
-    const float* const l = S.logit + (int64_t)t * E;
     float most = -__builtin_inff(), all = 0;
     if (!rule.sigmoid) {
         for (int e = lane; e < E; e += kWave) most = fmaxf(most, l[e]);
@@ -241,11 +281,17 @@ __device__ __forceinline__ int tile_rows(unsigned long long tokens, int rows, in
 // Chooses the experts of all tokens and lists the tiles of up to `rows` rows.  What the kernel that follows needs of it is
 // written down once: by block t for token t, by the first block for all.  (A block more that does nothing else is a
 // round more where the others fill the card: 37.5 us against 31.8, one token, 256 4-bit experts of 7168 x 2048.)
-__device__ __forceinline__ void choose(const LayerShape& S, const Rule& rule, int rows, Choice& C, int32_t* topk_idx,
-                                       float* topk_w)
+__device__ __forceinline__ void choose(const LayerShape& S, const Rule& rule, int rows, const char* x, const char* w,
+                                       Choice& C, int32_t* topk_idx, float* topk_w)
 {
     const int lane = lane_id(), wave = wave_id(), E = S.E, k = S.k;
+    const bool own = w != nullptr;
     for (int e = threadIdx.x; e < E; e += kThreads) C.tokens[e] = 0;
+    if (own) {
+        own_scores_of(S, rule, (const u32x4*)x, (const u32x4*)w, C);
+        if (blockIdx.x == 0)
+            for (int i = threadIdx.x; i < (S.H + 63) / 64; i += kThreads) S.arrived[i] = 0;
+    }
     __syncthreads();
     const auto some = [&](auto each) {
         constexpr int Each = decltype(each)::value, N = Each > 4 ? 1 : 2;
@@ -254,19 +300,20 @@ __device__ __forceinline__ void choose(const LayerShape& S, const Rule& rule, in
             int chosen[N], t[N];
             if (N == 1 || t0 + kWaves >= S.T) {
                 int one[1] = {t0}, its[1];
-                choose_tokens<Each, 1>(S, one, C, its);
+                choose_tokens<Each, 1>(S, own, one, C, its);
                 t[0] = t0;
                 chosen[0] = its[0];
                 if (N > 1) t[N - 1] = -1;
             } else {
 #pragma unroll
                 for (int n = 0; n < N; ++n) t[n] = t0 + n * kWaves;
-                choose_tokens<Each, N>(S, t, C, chosen);
+                choose_tokens<Each, N>(S, own, t, C, chosen);
             }
 #pragma unroll
             for (int n = 0; n < N; ++n) {
                 if (t[n] < 0 || t[n] % (int)gridDim.x != (int)blockIdx.x) continue;
-                write_gates(S, rule, t[n], chosen[n], topk_idx, topk_w);
+                if (own) write_gates(S, rule, C.logit + t[n] * E, t[n], chosen[n], topk_idx, topk_w);
+                else write_gates(S, rule, S.logit + (int64_t)t[n] * E, t[n], chosen[n], topk_idx, topk_w);
                 if (lane < k) S.row_of[t[n] * k + lane] = chosen[n];  // its row, once the first rows are known
             }
         }
@@ -320,14 +367,14 @@ struct Weights {
 };
 
 template <int Group, int Rows, int Ways, bool Whole, bool Staged>
-__global__ __launch_bounds__(kThreads, Rows == 16 ? 4 : 2) void layer_up_kernel(LayerShape S, Rule rule, const char* x, Weights A,
-                                                            int32_t* topk_idx, float* topk_w)
+__global__ __launch_bounds__(kThreads, Rows == 16 ? 4 : 2) void layer_up_kernel(LayerShape S, Rule rule, const char* x, const char* w,
+                                                            Weights A, int32_t* topk_idx, float* topk_w)
 {
     typedef LayerSplit<Rows, Ways> P;
     constexpr int kOut = 32;  // output features of a wave
     __shared__ __align__(16) char lds[Staged ? P::kStage : P::kSums];
     __shared__ Choice C;
-    choose(S, rule, Rows, C, topk_idx, topk_w);
+    choose(S, rule, Rows, x, w, C, topk_idx, topk_w);
     const int ks = wave_id() % P::KS, fs = wave_id() / P::KS, K = S.H, N = S.I;
     const int items = C.tiles * A.across;
     for (int item = blockIdx.x; item < items; item += gridDim.x) {
@@ -480,7 +527,7 @@ hipError_t launch_up(const LayerShape& S, const Rule& rule, const LayerCall& C, 
     const int64_t items = (int64_t)((S.P < S.E ? S.P : S.E) + S.P / Rows) * A.across;
     const int grid = (int)(items < kResident ? items : kResident);
     layer_up_kernel<Group, Rows, Ways, Whole, Staged><<<grid, kThreads, 0, s>>>(
-        S, rule, (const char*)C.x, A, C.topk_idx, C.topk_w);
+        S, rule, (const char*)C.x, own_scores(S) ? (const char*)C.w_router : nullptr, A, C.topk_idx, C.topk_w);
     return hipGetLastError();
 }
 
@@ -495,7 +542,13 @@ hipError_t launch_down(const LayerShape& S, const Rule&, const LayerCall& C, hip
     return hipGetLastError();
 }
 
-// The rules of experts_few.hip: few ways over k where k is short, room for the scales permitting.
+// All eight waves share a sum of bf16 weights, whatever its length: us a call with eight ways and with two, one token,
+// 64 experts of 2048 x 1024 28.0 / 58.6, 16 tokens 161 / 177, 64 tokens 184 / 200; one token, 8 of 7168 x 2048 144.7 /
+// 143.7.  Of 4-bit weights, where k is short, two do, unless that leaves half of the card without work: groups of 128,
+// one token, 8 experts of 1024 x 512 13.3 / 18.7, 64 experts of 7168 x 2048 45.5 / 42.7, 16 tokens 316 / 304, 64 tokens,
+// 64 of 2048 x 1024 82.8 / 76.4.  The scales of the features have to fit LDS, or come from memory.
+constexpr int kFewItems = 128;
+
 template <int Group, int Rows, bool Up>
 hipError_t launch_one(const LayerShape& S, const Rule& rule, const LayerCall& C, hipStream_t s)
 {
@@ -503,11 +556,12 @@ hipError_t launch_one(const LayerShape& S, const Rule& rule, const LayerCall& C,
 #define MS_LAYER(WAYS, WHOLE, STAGED) \
     (Up ? launch_up<Group, Rows, WAYS, WHOLE, STAGED>(S, rule, C, s) : launch_down<Group, Rows, WAYS, WHOLE, STAGED>(S, rule, C, s))
     if constexpr (Group == 0) {
-        if (K % kChunk) return MS_LAYER(8, false, false);
-        return K >= kLongK ? MS_LAYER(8, true, false) : MS_LAYER(2, true, false);
+        return K % kChunk ? MS_LAYER(8, false, false) : MS_LAYER(8, true, false);
     } else {
+        const int N = Up ? S.I : S.H, wide = (Up ? 32 : 64) * LayerSplit<Rows, 2>::FS;
+        const bool few = K < kLongK && (int64_t)(S.P < S.E ? S.P : S.E) * ((N + wide - 1) / wide) >= kFewItems;
         const auto fits = [&](int ways) { return (int64_t)64 * (kWaves / ways) * (K / Group) * 2 <= 64 << 10; };
-        const bool two = fits(2) && K < kLongK;
+        const bool two = fits(2) && few;
         if (!two && !fits(8)) return MS_LAYER(8, false, false);
         if constexpr (Group % kChunk != 0)  // K is a multiple of the group
             if (K % kChunk) return two ? MS_LAYER(2, false, true) : MS_LAYER(8, false, true);
@@ -523,14 +577,17 @@ hipError_t launch_both(const LayerShape& S, const Rule& rule, const LayerCall& C
     return e != hipSuccess ? e : launch_one<Group, Rows, false>(S, rule, C, s);
 }
 
+// Rows an expert has on average, up to which tiles have 16 of them: two blocks fit a CU then, but an expert with more
+// has its weights read again.  Us a call with 16 and with 32, for 64 experts of 2048 x 1024, 8 of 4096 x 4096 and 16 of
+// 2048 x 2048: bf16, 4 rows 172 / 179, 184 / 175, 92 / 94; 10 rows -, 194 / 183, 103 / 105; 12 rows -, 218 / 187, 118 / 106;
+// groups of 128, 4 rows 62 / 73, 55 / 65, 44 / 45; 10 rows -, 65 / 76, 58 / 59; 12 rows -, 80 / 82, 72 / 65.
+constexpr int kRowsOf16 = 10;
+
 template <int Group>
 hipError_t launch_rows(const LayerShape& S, const Rule& rule, const LayerCall& C, hipStream_t s)
 {
-#ifndef MS_ROWS
-#define MS_ROWS 12
-#endif
-    return S.P <= (int64_t)MS_ROWS * (S.P < S.E ? S.P : S.E) ? launch_both<Group, 16>(S, rule, C, s)
-                                                             : launch_both<Group, 32>(S, rule, C, s);
+    return S.P <= (int64_t)kRowsOf16 * (S.P < S.E ? S.P : S.E) ? launch_both<Group, 16>(S, rule, C, s)
+                                                               : launch_both<Group, 32>(S, rule, C, s);
 }
 
 }  // namespace
@@ -558,7 +615,8 @@ size_t layer_workspace(LayerShape* S, char* base)
 
 hipError_t launch_layer(const LayerShape& S, const Rule& rule, const LayerCall& C, hipStream_t s)
 {
-    const hipError_t e = S.T == 1 ? launch_scores<1, 1, 1024>(S, rule, C, s)
+    const hipError_t e = own_scores(S) ? hipSuccess
+                         : S.T == 1 ? launch_scores<1, 1, 1024>(S, rule, C, s)
                          : S.T <= 4 ? launch_scores<4, 1, 512>(S, rule, C, s)
                                     : launch_scores<8, 4, 512>(S, rule, C, s);
     if (e != hipSuccess) return e;

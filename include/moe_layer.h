@@ -84,11 +84,11 @@ int moe_router_forward(const moe_shuffle_dims* dims, const moe_router_rule* rule
  *   dl_e = ds_e s_e (1 - s_e)                          SIGMOID, 0 elsewhere
  *   dl_e = s_e (ds_e - sum_i ds_i s_i)                 SOFTMAX, ds 0 elsewhere
  *   dl  += grad_logits, where given (of a loss on the logits themselves)
- *   grad_x        = bf16(grad_x_in + bf16(dl) w_router)          [T, H]
- *   grad_w_router = bf16(bf16(dl)^T x)                           [E, H]
+ *   grad_x        = bf16(grad_x_in + dl w_router)                [T, H]
+ *   grad_w_router = bf16(dl^T x)                                 [E, H]
  *
- * dl is rounded to bf16 because it is an operand of bf16 matrix products, as
- * the gradients inside moe_experts_ffn_backward are; sums are held in fp32.
+ * dl enters the matrix products, whose operands are bf16, as the sum of two
+ * bf16 numbers: 16 bits of it count.  Sums are held in fp32.
  *   logits, topk_idx  as the forward call wrote them (bad ids: no result is
  *                     promised, nothing out of bounds is touched)
  *   grad_logits, grad_x_in  may be NULL; grad_x_in may be grad_x

@@ -4,8 +4,7 @@
 //            blocks where there are few tiles (partial sums in fp32 in the workspace)
 //   choose   a wave a row: the partial sums' sum, the k largest keys, the gates
 //   dlogits  a wave a row: the gates' gradients to the logits', bf16
-//   grad_x   grad_x_in + dl W, added in fp32 before the one rounding: by tiles, or, where dl has k numbers a row, a sum
-//            of k rows of W a row
+//   grad_x   grad_x_in + dl W, added in fp32 before the one rounding: by tiles, or, with many rows, W in registers
 //   grad_w   dl^T x by tiles, T split over blocks, and the sum of their parts
 //
 // The choice has to be that of exact sums, and matrix instructions sum in fp32.  So `choose` knows how far a logit may
@@ -485,8 +484,7 @@ __global__ __launch_bounds__(kChooseWaves * kWave) void router_dlogits_kernel(Ro
                                                                               const float* grad_gate,
                                                                               const float* logits, const int32_t* idx,
                                                                               const float* grad_logits,
-                                                                              unsigned short* dl, int ld, float* few,
-                                                                              GridSpan span)
+                                                                              unsigned short* dl, int ld, GridSpan span)
 {
     __shared__ float ds[kChooseWaves][Each * kWave];
     const int lane = lane_id(), E = S.E, k = S.k;
@@ -521,8 +519,6 @@ __global__ __launch_bounds__(kChooseWaves * kWave) void router_dlogits_kernel(Ro
     }
     // normalized, the chosen scores' sum does not change: the mean is 0, and so is dl of the others
     const float mean = rule.sigmoid || rule.normalize ? 0.0f : wave_total(g * s);
-    if (few && lane < k) few[t * k + lane] = rule.sigmoid ? (in ? g * s * (1.0f - s) : 0.0f) : in ? s * g : 0.0f;
-    if (!dl) return;
     if (in) mine[e] = g;
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // this wave's own LDS
 #pragma unroll
@@ -575,11 +571,11 @@ struct Twice : Base {
 __device__ __forceinline__ int twice(int K) { return (K + kTileK - 1) / kTileK * kTileK * 2; }
 
 // grad_x = grad_x_in + dl W, a tile of rows and 256 columns a block.
-template <bool Small>
-__global__ __launch_bounds__(kGemmThreads, Small ? 4 : 2) void router_grad_x_kernel(RouterShape S, const char* dl, int ld,
+__global__ __launch_bounds__(kGemmThreads, 4) void router_grad_x_kernel(RouterShape S, const char* dl, int ld,
                                                                                     const char* w, const char* in,
                                                                                     char* out, int across, GridSpan span)
 {
+    constexpr bool Small = true;
     __shared__ __align__(1024) char lds[Lds<Small>::kBytes];
     const Place at = place_of(span, across);
     const int row0 = at.tile * Lds<Small>::kRows, nr = min(Lds<Small>::kRows, S.T - row0);
@@ -609,51 +605,143 @@ __global__ __launch_bounds__(kGemmThreads, Small ? 4 : 2) void router_grad_x_ker
     });
 }
 
-// grad_x = grad_x_in + sum over j of few[t][j] W[idx[t][j]]: a wave makes 512 columns of a row.  W is read k times a row,
-// from the L2s: all blocks work on one piece of 512 columns before the next, so that each L2 holds the few hundred
-// kilobytes of W that are needed.  A row's ids and factors are a lane's each, and come back as scalars.
-__global__ __launch_bounds__(256) void router_gather_kernel(RouterShape S, const float* few, const int32_t* idx,
-                                                            const u32x4* w, const u32x4* in, u32x4* out, GridSpan span)
+constexpr int kStripe = 512;  // columns of a block below, 64 a wave
+
+// The same for many rows and at most 256 experts: W stays in registers.  A wave has the fragments of 64 columns for all
+// k (32 KS experts), and its block walks down the rows, 16 at a time, with their dl (both parts) in LDS, the next ones'
+// on their way.  So W is read once a block, and what is left is to stream grad_x_in and grad_x: 8192 rows, H = 7168, 256
+// experts 66 us, 3.6 TB/s (113 by tiles; 83 as sums of the k rows of W that a sparse dl leaves, where unpacking them is the
+// cost).  Non-temporal stores of 64 bytes a row took 77.
+//   The features of a pair of fragments are dealt so that a lane ends with eight neighbouring ones of a row: matrix row m
+//   of fragment g is column 32 (g / 2) + 8 (m / 4) + 4 (g % 2) + m % 4.
+template <int KS>
+__global__ __launch_bounds__(kGemmThreads, 2) void router_grad_x_stripe_kernel(RouterShape S, const char* dl, int ld,
+                                                                               const char* w, const char* in, char* out,
+                                                                               int across, int each)
 {
-    const int t = span_block(span), lane = lane_id(), V = S.H / 8, k = S.k;
-    const unsigned v0 = (blockIdx.y * (256 / kWave) + wave_id()) * kWave, v = v0 + lane;
-    if (v0 >= (unsigned)V) return;
-    const unsigned at = min(v, (unsigned)V - 1);  // past the row's end its last vector
-    int id = 0;
-    float f = 0;
-    if (lane < k) {
-        const int e = idx[(int64_t)t * k + lane];
-        if ((unsigned)e < (unsigned)S.E) {  // a bad id counts as none
-            id = e;
-            f = few[(int64_t)t * k + lane];
-        }
-    }
-    u32x4 add = {0, 0, 0, 0};
-    if (in) add = load_row16<true>(in + (int64_t)t * V + at);
-    float sum[8] = {};
-    const auto some = [&](auto count, int j0) {
-        constexpr int N = decltype(count)::value;
-        u32x4 row[N];
+    constexpr int kRow = KS * 64 + 16;  // bytes of a row in LDS; the last 16 spread the rows over the banks
+    constexpr int kPieces = 16 * KS * 4;  // of 16 bytes, of each part of dl
+    // two tiles of dl; before that 32 rows of W at a time, which come out by columns
+    constexpr int kWide = kStripe * 2 + 32, kTiles = 4 * 16 * kRow, kLds = kTiles > 32 * kWide ? kTiles : 32 * kWide;
+    __shared__ __align__(16) char lds[kLds];
+    const int lane = lane_id(), r = lane & 15, q = lane >> 4, H = S.H, E = S.E;
+    const int n0 = (int)(blockIdx.x % across) * kStripe + wave_id() * 64;
+    const int64_t first = (int64_t)(blockIdx.x / across) * each, last = min(first + each, (int64_t)S.T);
+    // rows [t, t + 16) of dl, a piece of each part a thread; zeros past the last row and past ld
+    const int piece_row = threadIdx.x / (KS * 4), piece_k = threadIdx.x % (KS * 4);
+    const unsigned piece = (int)threadIdx.x < kPieces && piece_k * 8 < ld ? (unsigned)(piece_row * ld + piece_k * 8) * 2 : kOutside;
+    char* const home = lds + piece_row * kRow + piece_k * 16;
+    u32x4 held[2][2];
+    const auto fetch = [&](u32x4 (&held)[2], int64_t t) {
+        const int64_t bytes = max(min((int64_t)16, last - t), (int64_t)0) * ld * 2;
 #pragma unroll
-        for (int j = 0; j < N; ++j) row[j] = (w + (int64_t)__builtin_amdgcn_readlane(id, j0 + j) * V)[at];
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
-            const float d = __uint_as_float((unsigned)__builtin_amdgcn_readlane((int)__float_as_uint(f), j0 + j));
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                sum[2 * c] = fmaf(d, bf16_lo(row[j][c]), sum[2 * c]);
-                sum[2 * c + 1] = fmaf(d, bf16_hi(row[j][c]), sum[2 * c + 1]);
-            }
-        }
+        for (int plane = 0; plane < 2; ++plane)
+            held[plane] = __builtin_amdgcn_raw_buffer_load_b128(buffer(dl + (plane * (int64_t)S.T + t) * ld * 2, bytes), piece, 0, 0);
     };
-    int j = 0;
-    for (; j + 8 <= k; j += 8) some(std::integral_constant<int, 8>(), j);
-    for (; j + 2 <= k; j += 2) some(std::integral_constant<int, 2>(), j);
-    if (j < k) some(std::integral_constant<int, 1>(), j);
-    u32x4 r;
+    const auto put = [&](const u32x4 (&held)[2], int to) {
+        if ((int)threadIdx.x >= kPieces) return;
 #pragma unroll
-    for (int c = 0; c < 4; ++c) r[c] = bf16_pack2(sum[2 * c] + bf16_lo(add[c]), sum[2 * c + 1] + bf16_hi(add[c]));
-    if (v < (unsigned)V) store_row16<true>(r, out + (int64_t)t * V + v);
+        for (int plane = 0; plane < 2; ++plane) *(u32x4*)(home + (to * 2 + plane) * 16 * kRow) = held[plane];
+    };
+    if (first >= last) return;
+    fetch(held[0], first);
+    fetch(held[1], first + 16);
+    // experts past the last read as zero (dl is zero there too), and columns past H go nowhere
+    const int stripe = (int)(blockIdx.x % across) * kStripe;
+    const __amdgpu_buffer_rsrc_t weights = buffer(w, (int64_t)E * H * 2);
+    const int wide_row = threadIdx.x / 64, wide_c = threadIdx.x % 64 * 8;  // of 8 rows and 512 columns
+    const unsigned wide = stripe + wide_c < H ? (unsigned)(wide_row * H + stripe + wide_c) * 2 : kOutside;
+    u32x4 next[4];
+    const auto fetch_w = [&](int s) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) next[i] = __builtin_amdgcn_raw_buffer_load_b128(weights, wide, (32 * s + 8 * i) * H * 2, 0);
+    };
+    fetch_w(0);
+    bf16x8 f[4][KS];
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) *(u32x4*)(lds + (wide_row + 8 * i) * kWide + wide_c * 2) = next[i];
+        __syncthreads();
+        if (s + 1 < KS) fetch_w(s + 1);
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            // lanes 4 i .. 4 i + 3 of each sixteen name row i of four: four columns each, which come back by columns
+            const char* const from = lds + (8 * q + ((lane >> 2) & 3)) * kWide +
+                                     (wave_id() * 64 + 32 * (g >> 1) + 8 * (lane & 3) + 4 * (g & 1)) * 2;
+            union {
+                s16x4 h[2];
+                bf16x8 v;
+            } u;
+            u.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)from);
+            u.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(from + 4 * kWide));
+            f[g][s] = u.v;
+        }
+        __syncthreads();
+    }
+    unsigned place[2];  // of this lane's row and eight columns in 16 rows
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+        const int c = n0 + 32 * p + 8 * q;
+        place[p] = c < H ? (unsigned)(r * H + c) * 2 : kOutside;
+    }
+    // rows past the last lie past the descriptors' ends
+    const auto rows = [&](const char* p, int64_t t) {
+        return buffer(p ? p + t * H * 2 : nullptr, p ? max(min((int64_t)16, last - t), (int64_t)0) * H * 2 : 0);
+    };
+    u32x4 add[2][2];
+    const auto fetch_in = [&](u32x4 (&add)[2], int64_t t) {
+        const __amdgpu_buffer_rsrc_t from = rows(in, t);
+#pragma unroll
+        for (int p = 0; p < 2; ++p) add[p] = __builtin_amdgcn_raw_buffer_load_b128(from, place[p], 0, 0);
+    };
+    fetch_in(add[0], first);
+    fetch_in(add[1], first + 16);
+    put(held[0], 0);
+    __syncthreads();
+    // Rows [t, t + 16), in LDS at `at`.  What the tile after the next one needs is on its way meanwhile.
+    const auto tile = [&](int64_t t, auto parity) {
+        constexpr int at = decltype(parity)::value;
+        fetch(held[at], t + 32);
+        f32x4 acc[4];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) acc[g] = f32x4{0, 0, 0, 0};
+        const char* const from = lds + (at * 32 + r) * kRow + q * 16;
+        bf16x8 d[2][2];
+        const auto read = [&](int s) {
+#pragma unroll
+            for (int plane = 0; plane < 2; ++plane) d[s & 1][plane] = *(const bf16x8*)(from + plane * 16 * kRow + s * 64);
+        };
+        read(0);
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            if (s + 1 < KS) read(s + 1);
+#pragma unroll
+            for (int plane = 0; plane < 2; ++plane)
+#pragma unroll
+                for (int g = 0; g < 4; ++g) acc[g] = mfma_16x16x32(f[g][s], d[s & 1][plane], acc[g]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        const __amdgpu_buffer_rsrc_t outs = rows(out, t);
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            const f32x4 a = acc[2 * p], b = acc[2 * p + 1];
+            const u32x4 c = add[at][p];
+            const u32x4 v = {bf16_pack2(a[0] + bf16_lo(c[0]), a[1] + bf16_hi(c[0])),
+                             bf16_pack2(a[2] + bf16_lo(c[1]), a[3] + bf16_hi(c[1])),
+                             bf16_pack2(b[0] + bf16_lo(c[2]), b[1] + bf16_hi(c[2])),
+                             bf16_pack2(b[2] + bf16_lo(c[3]), b[3] + bf16_hi(c[3]))};
+            __builtin_amdgcn_raw_buffer_store_b128(v, outs, place[p], 0, 0);
+        }
+        fetch_in(add[at], t + 32);
+        put(held[at ^ 1], at ^ 1);  // read last before the barrier behind us
+        __syncthreads();
+    };
+#pragma unroll 1
+    for (int64_t t = first; t < last; t += 32) {
+        tile(t, std::integral_constant<int, 0>());
+        if (t + 16 < last) tile(t + 16, std::integral_constant<int, 1>());
+    }
 }
 
 // Part `blockIdx / tiles` of dl^T x: rows [part * each, ...) of both, 256 experts by 256 columns a block, fp32.
@@ -708,6 +796,15 @@ __global__ __launch_bounds__(256) void router_join_kernel(const f32x4* parts, in
 // ---- sizes ----
 
 constexpr int kMaxSplits = 16;
+
+// Whether grad_x is made in stripes.  dlogits and grad_x, us, in stripes and by tiles: H = 7168, 256 experts, 1024 rows 21 /
+// 23, 2048 31 / 36, 8192 81 / 108; H = 4096, 128 experts, 4096 rows 31 / 28, 8192 47 / 52; 8 experts, 4096 rows 25 / 24,
+// 8192 40 / 41; H = 2048, 64 experts, 8192 rows 29 / 25, 32768 84 / 91.
+bool in_stripes(const RouterShape& S)
+{
+    if (S.E > 256) return false;
+    return S.E > 128 ? S.T >= 1024 : (int64_t)S.T * S.H >= (int64_t)1 << 25;
+}
 
 int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -780,12 +877,11 @@ struct GoChoose {
 template <int Each>
 struct GoDlogits {
     static hipError_t go(const RouterShape& S, const Rule& rule, const float* grad_gate, const float* logits,
-                         const int32_t* idx, const float* grad_logits, unsigned short* dl, int ld, float* few,
-                         hipStream_t s)
+                         const int32_t* idx, const float* grad_logits, unsigned short* dl, int ld, hipStream_t s)
     {
         return launch_spans(up(S.T, kChooseWaves), kChooseWaves * kWave, [&](dim3 grid, GridSpan span) {
             router_dlogits_kernel<Each><<<grid, kChooseWaves * kWave, 0, s>>>(S, rule, grad_gate, logits, idx, grad_logits,
-                                                                              dl, ld, few, span);
+                                                                              dl, ld, span);
         });
     }
 };
@@ -802,8 +898,7 @@ size_t router_workspace(const RouterShape& S, bool backward)
     }
     if (backward && S.T > 0) {
         const GradCut g = grad_cut(S);
-        const size_t b = align256((size_t)S.T * g.ld * 4) + align256((size_t)g.splits * S.E * S.H * 4) +
-                         align256((size_t)S.T * S.k * 4);
+        const size_t b = align256((size_t)S.T * g.ld * 4) + align256((size_t)g.splits * S.E * S.H * 4);
         if (b > n) n = b;
     }
     return n;
@@ -839,20 +934,25 @@ hipError_t launch_router_backward(const RouterShape& S, const Rule& rule, const 
     float* const parts = (float*)(ws + align256((size_t)S.T * g.ld * 4));
     if (S.T == 0)  // no part: zeros
         return grad_w ? join(parts, 0, S, grad_w, s) : hipSuccess;
-    const bool sparse = (rule.sigmoid || rule.normalize) && !grad_logits;
-    float* const few = sparse && grad_x ? (float*)((char*)parts + align256((size_t)g.splits * S.E * S.H * 4)) : nullptr;
-    hipError_t e = by_experts<GoDlogits>(S.E, S, rule, grad_gate, logits, idx, grad_logits,
-                                         grad_w || !few ? dl : nullptr, g.ld, few, s);
-    if (e == hipSuccess && few) {
-        const unsigned pieces = (unsigned)up(S.H / 8, 256);
-        e = launch_spans(S.T, 256, [&](dim3 grid, GridSpan span) {
-            router_gather_kernel<<<dim3(grid.x, pieces), 256, 0, s>>>(S, few, idx, (const u32x4*)w, (const u32x4*)grad_x_in,
-                                                                      (u32x4*)grad_x, span);
-        });
+    hipError_t e = by_experts<GoDlogits>(S.E, S, rule, grad_gate, logits, idx, grad_logits, dl, g.ld, s);
+    if (e == hipSuccess && grad_x && in_stripes(S)) {
+        const int across = (int)up(S.H, kStripe);
+        int64_t groups = 256 / across;
+        if (groups < 1) groups = 1;
+        const int64_t each = up(up(S.T, groups), 16) * 16;
+        const unsigned grid = (unsigned)(up(S.T, each) * across);
+        const auto go = [&](auto ks) {
+            router_grad_x_stripe_kernel<decltype(ks)::value><<<grid, kGemmThreads, 0, s>>>(
+                S, (const char*)dl, g.ld, (const char*)w, (const char*)grad_x_in, (char*)grad_x, across, (int)each);
+        };
+        if (S.E <= 64) go(std::integral_constant<int, 2>());
+        else if (S.E <= 128) go(std::integral_constant<int, 4>());
+        else go(std::integral_constant<int, 8>());
+        e = hipGetLastError();
     } else if (e == hipSuccess && grad_x) {
         const int across = (int)up(S.H, kTileFeatures);
         e = launch_spans(places(up(S.T, Lds<true>::kRows), across), kGemmThreads, [&](dim3 grid, GridSpan span) {
-            router_grad_x_kernel<true><<<grid, kGemmThreads, 0, s>>>(S, (const char*)dl, g.ld, (const char*)w,
+            router_grad_x_kernel<<<grid, kGemmThreads, 0, s>>>(S, (const char*)dl, g.ld, (const char*)w,
                                                                      (const char*)grad_x_in, (char*)grad_x, across, span);
         });
     }

@@ -86,14 +86,15 @@ def score_gradient(l, idx, grad, sigmoid: bool, normalize: bool, scale: float):
 
 
 def router_backward(x, w, dl, e_dl, grad_x_in=None):
-    """grad_x and grad_w_router of a bf16-rounded dl, with element bounds."""
+    """grad_x and grad_w_router of a dl held as two bf16 numbers (U of what U leaves is lost), with element bounds; the
+    products are twice as many terms."""
     from experts_ref import GAMMA
     x, w = x.double(), w.double()
-    err = e_dl + U * (dl.abs() + e_dl) + TINY
+    err = e_dl + U * U * (dl.abs() + e_dl) + TINY
     size = dl.abs() + err
-    gx, ex = dl @ w, err @ w.abs() + GAMMA(w.shape[0]) * (size @ w.abs())
+    gx, ex = dl @ w, err @ w.abs() + GAMMA(2 * w.shape[0]) * (size @ w.abs())
     if grad_x_in is not None:
         gx = gx + grad_x_in.double()
         ex = ex + 2 * STEP * (gx.abs() + ex)
-    gw, ew = dl.T @ x, err.T @ x.abs() + GAMMA(x.shape[0] + 32) * (size.T @ x.abs())
+    gw, ew = dl.T @ x, err.T @ x.abs() + GAMMA(2 * x.shape[0] + 32) * (size.T @ x.abs())
     return gx, ex + U * (gx.abs() + ex) + TINY, gw, ew + U * (gw.abs() + ew) + TINY

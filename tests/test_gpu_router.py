@@ -143,6 +143,35 @@ def test_large_batch(rule):
         c.check(slice(lo, lo + 1024))
 
 
+@pytest.mark.parametrize("rule", RULES[1:3], ids=NAMES[1:3])
+@pytest.mark.parametrize("shape", [(1024, 520, 200, 8), (1041, 1544, 256, 4), (1055, 8, 129, 2), (8200, 4104, 40, 2),
+                                   (8207, 4104, 72, 3)], ids=lambda s: "-".join(map(str, s)))
+def test_many_rows_backward(shape, rule):
+    """grad_x in stripes of columns: rows and columns that end inside a tile, experts that end inside 32."""
+    c = Router(*shape, seed=sum(shape), **rule).forward()
+    add = bf16(c.gen, c.T, c.H, std=0.1)
+    gx, gw = c.backward(grad_x_in=add)
+    c.check_backward(gx, gw, add)
+    same = add.clone()
+    ms().moe_router_backward(c.dims, c.rule(), c.grad, c.logits, c.idx, c.x, c.w, same, None, c.ws, grad_x_in=same)
+    assert torch.equal(same, gx)
+    plain, _ = c.backward(want=("grad_x",))
+    c.check_backward(plain, gw)
+
+
+def test_values_that_are_not_finite_stay_in_their_rows():
+    """In stripes, an infinite element of W reaches its column alone, a NaN gradient its row alone."""
+    c = Router(1100, 512, 160, 4, norm=False, seed=15).forward()
+    gx, _ = c.backward()
+    c.w[3, 100] = float("inf")
+    c.grad[50, 1] = float("nan")
+    bad, _ = c.backward()
+    rows = torch.arange(1100, device="cuda") != 50
+    columns = torch.arange(512, device="cuda") != 100
+    assert torch.equal(bad[rows][:, columns], gx[rows][:, columns])
+    assert not bool(torch.isfinite(bad[rows, 100]).any()) and bool(torch.isnan(bad[50]).all())
+
+
 def near_ties(c, size):
     """Rows whose keys differ by little: all experts share a row but for one element, where x is small."""
     c.w[:] = c.w[:1].clone()

@@ -1,11 +1,13 @@
-"""MoE token shuffle for AMD MI355X (gfx950): plan, dispatch, combine, and the
-experts' gated feed-forward block in between.
+"""MoE token shuffle for AMD MI355X (gfx950): plan, dispatch, combine, the
+experts' gated feed-forward block in between, the router before it, a whole
+layer for few tokens, and the optimizer's step.
 
-A thin Python face of the C ABI in include/moe_shuffle.h and
-include/moe_experts.h; every step runs in
+A thin Python face of the C ABI in include/moe_shuffle.h, include/moe_experts.h,
+include/moe_layer.h and include/moe_optim.h; every step runs in
 the HIP kernels of libmoe_shuffle.so.  Tensors are torch tensors on the GPU;
 bf16 activations may be torch.bfloat16 or any 16-bit view of the same bits.
-The experts' calls compute with the values and refuse other floating types.
+The experts', router's and layer's calls compute with the values and refuse
+other floating types.
 """
 
 from ._lib import (  # noqa: F401

@@ -1,10 +1,10 @@
 // layer.hip -- a whole mixture-of-experts layer for a few tokens in three kernels: the router's scores, the two
-// projections, the down projection with the weighted sum.
+// projections, the down projection with the weighted sum.  Very few scores are made in the projections: two kernels.
 //
 // The weights of the chosen experts are the cost (experts_stream.h has how a wave streams them); all else is latency.
 // So nothing goes through memory that a block can find out by itself: every block of the projections chooses the
-// experts of all tokens anew from the scores (2 us, beside weights of 25 to 600) and makes its own list of row tiles,
-// where a plan, a dispatch and a copy of the rows would be three launches.
+// experts of all tokens anew from the scores and makes its own list of row tiles, where a plan, a dispatch and a copy of
+// the rows would be three launches.
 //
 //   scores   l = x w^T, one expert a block: products of bf16 numbers are exact in fp32, and are summed in 64 bits, so
 //            that the choice does not depend on the sum's order

@@ -5,8 +5,9 @@
 // parameters, their bf16 copy and bf16 gradients, 16.1 with 8-bit states.  What reaches the memory's rate is small
 // blocks in the order of memory: with four neighbouring elements a lane (16 contiguous bytes of fp32) and 1024 a block,
 // 197 M parameters with fp32 states take 910 us (6.1 TB/s, a large copy 6.5); 1028 with 8192 a block, 1128 with 8192 in
-// lanes of eight.  8-bit states, 1.4 G parameters: 3.81 ms (6.0 TB/s) with 1024 a block of two waves, 4.07 of four, 4.27
-// with 8192.  Unpacking moves fewer bytes an element and likes lanes of eight: 1.37 ms against 1.57 (6.2 TB/s).
+// lanes of eight.  8-bit states, 1.4 G parameters: 3.81 to 3.98 ms (6.0 to 5.8 TB/s) with 1024 a block of two waves, 4.07
+// of four, 4.27 with 8192.  Unpacking moves fewer bytes an element and likes lanes of eight: 1.37 to 1.42 ms (6.2 to 6.0
+// TB/s) against 1.57.
 //
 // A group of 128 is 32 or 16 neighbouring lanes, which find its largest magnitudes by five or four exchanges.  The
 // tensors' addresses come with the kernel's arguments, 40 a launch, so that nothing has to be copied to the device first.

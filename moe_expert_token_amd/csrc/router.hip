@@ -1,9 +1,9 @@
 // router.hip -- the router of many rows and its backward pass.
 //
-//   logits   x W^T by the tile product of experts_gemm.h, a tile of 64 rows and 256 experts a block, H split over
+//   logits   x W^T by the tile product of experts_gemm.h, a tile of 64 or 128 rows and 256 experts a block, H split over
 //            blocks where there are few tiles (partial sums in fp32 in the workspace)
 //   choose   a wave a row: the partial sums' sum, the k largest keys, the gates
-//   dlogits  a wave a row: the gates' gradients to the logits', bf16
+//   dlogits  a wave a row: the gates' gradients to the logits', in two bf16 parts
 //   grad_x   grad_x_in + dl W, added in fp32 before the one rounding: by tiles, or, with many rows, W in registers
 //   grad_w   dl^T x by tiles, T split over blocks, and the sum of their parts
 //
@@ -11,7 +11,7 @@
 // be off: a sum of products computed in `steps` roundings one after another is off by at most steps 2^-23 sum |x w|, and
 // sum |x w| <= ||x|| ||w||.  The norms come out of the same product for nothing (the fragments are in registers: one of
 // four waves squares a tile of k).  Two neighbours among the k + 1 largest keys that are nearer than twice that bound
-// are summed again, in 64 bits, by the wave that found them.
+// are summed again, in 64 bits, by the whole block.
 #include <math.h>
 
 #include "experts_tiles.h"

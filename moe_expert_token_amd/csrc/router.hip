@@ -650,11 +650,14 @@ __global__ __launch_bounds__(kGemmThreads, 2) void router_grad_x_stripe_kernel(R
     const int stripe = (int)(blockIdx.x % across) * kStripe;
     const __amdgpu_buffer_rsrc_t weights = buffer(w, (int64_t)E * H * 2);
     const int wide_row = threadIdx.x / 64, wide_c = threadIdx.x % 64 * 8;  // of 8 rows and 512 columns
-    const unsigned wide = stripe + wide_c < H ? (unsigned)(wide_row * H + stripe + wide_c) * 2 : kOutside;
     u32x4 next[4];
     const auto fetch_w = [&](int s) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) next[i] = __builtin_amdgcn_raw_buffer_load_b128(weights, wide, (32 * s + 8 * i) * H * 2, 0);
+        for (int i = 0; i < 4; ++i) {  // all of the offset in a vector register: a scalar one is not held to the range
+            const int e = wide_row + 32 * s + 8 * i;
+            const unsigned from = e < E && stripe + wide_c < H ? (unsigned)(e * H + stripe + wide_c) * 2 : kOutside;
+            next[i] = __builtin_amdgcn_raw_buffer_load_b128(weights, from, 0, 0);
+        }
     };
     fetch_w(0);
     bf16x8 f[4][KS];

@@ -118,6 +118,28 @@ def test_bf16(shape, rule):
     c.check(c.run())
 
 
+@pytest.mark.parametrize("shape", [(3, 136, 5, 5, 72, 0), (1, 128, 8, 2, 256, 0), (17, 1544, 40, 6, 712, 0), (64, 64, 3, 1, 128, 0),
+                                   (5, 128, 65, 3, 4224, 0), (4, 160, 6, 2, 96, 32), (2, 384, 9, 2, 640, 128),
+                                   (40, 1088, 20, 4, 320, 64), (1, 4096, 8, 2, 512, 128)], ids=lambda s: "-".join(map(str, s)))
+def test_what_lies_around_the_inputs(shape):
+    """NaN before and after every input reach nothing."""
+    *sizes, group = shape
+    c = Layer(*sizes, group=group, seed=sum(shape))
+    want = [c.run(), c.idx, c.gates]
+
+    def inside(t):
+        value = float("nan") if t.is_floating_point() else 0xff
+        n, pad = t.numel(), 1 << 16
+        whole = torch.full((n + 2 * pad,), value, dtype=t.dtype, device="cuda")
+        whole[pad:pad + n] = t.flatten()
+        return whole[pad:pad + n].view(t.shape)
+
+    c.x, c.w_router, c.residual = inside(c.x), inside(c.w_router), inside(c.residual)
+    c.weights = [inside(t) for t in c.weights]
+    for g, w in zip([c.run(), c.idx, c.gates], want):
+        assert torch.equal(g, w)
+
+
 @pytest.mark.parametrize("group", [32, 64, 128])
 @pytest.mark.parametrize("shape", [(1, 128, 8, 2, 256), (1, 7168, 16, 8, 2048), (7, 256, 5, 5, 384), (16, 640, 40, 6, 896),
                                    (17, 640, 40, 6, 896), (48, 1024, 64, 8, 512), (64, 4224, 3, 2, 4096),

@@ -172,6 +172,27 @@ def test_values_that_are_not_finite_stay_in_their_rows():
     assert not bool(torch.isfinite(bad[rows, 100]).any()) and bool(torch.isnan(bad[50]).all())
 
 
+@pytest.mark.parametrize("shape", [(1041, 1544, 200, 4), (1055, 72, 129, 2), (8207, 4104, 72, 3), (8200, 4104, 5, 2),
+                                   (77, 136, 37, 3), (2050, 72, 30, 2)], ids=lambda s: "-".join(map(str, s)))
+def test_what_lies_around_the_inputs(shape):
+    """NaN before and after every input reach nothing: experts, rows and columns past the last are not looked at."""
+    c = Router(*shape, seed=sum(shape)).forward()
+    add = bf16(c.gen, c.T, c.H, std=0.1)
+    want = [c.idx, c.gates, c.logits] + list(c.backward(grad_x_in=add))
+
+    def inside(t, rows):
+        whole = torch.full((t.shape[0] + 2 * rows, t.shape[1]), float("nan"), dtype=t.dtype, device="cuda")
+        whole[rows:rows + t.shape[0]] = t
+        return whole[rows:rows + t.shape[0]]
+
+    c.x, c.w, add, c.grad = inside(c.x, 256), inside(c.w, 256), inside(add, 256), inside(c.grad, 256)
+    c.forward()
+    c.logits = inside(c.logits, 256)
+    got = [c.idx, c.gates, c.logits] + list(c.backward(grad_x_in=add))
+    for g, w in zip(got, want):
+        assert torch.equal(g, w)
+
+
 def near_ties(c, size):
     """Rows whose keys differ by little: all experts share a row but for one element, where x is small."""
     c.w[:] = c.w[:1].clone()

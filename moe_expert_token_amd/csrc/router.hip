@@ -8,10 +8,18 @@
 //   grad_w   dl^T x by tiles, T split over blocks, and the sum of their parts
 //
 // The choice has to be that of exact sums, and matrix instructions sum in fp32.  So `choose` knows how far a logit may
-// be off: a sum of products computed in `steps` roundings one after another is off by at most steps 2^-23 sum |x w|, and
-// sum |x w| <= ||x|| ||w||.  The norms come out of the same product for nothing (the fragments are in registers: one of
-// four waves squares a tile of k).  Two neighbours among the k + 1 largest keys that are nearer than twice that bound
-// are summed again, in 64 bits, by the whole block.
+// be off.  An instruction of 32 k adds four sums of eight products to its accumulator, each rounded to nearest: half of
+// 2^-23 of what is there by then, which is at most the sum of |x w| up to that k, and that at most |x| |w| up to that k
+// (Cauchy-Schwarz).  A sum of eight is off by up to 4 2^-23 of its own (products are cut half a step under the largest
+// one's last bit).  So a tile of 64 k brings 4 2^-23 |x| |w| up to its end, the sums of eight all together 8 2^-23 of
+// the whole, and the parts' sum splits 2^-23; once more by Cauchy-Schwarz, over the tiles, all of it is at most
+//
+//   4 2^-23 sqrt(sum_i c_i x_i^2) sqrt(sum_i c_i w_i^2),    c_i = the tiles from k = i on + (8 + splits) / 4
+//
+// The weighted squares come out of the same product for nothing (the fragments are in registers: one of four waves
+// squares a tile of k).  One large product before thousands of 2^-27 of it reaches nine tenths of it.  Two
+// neighbours among the k + 1 largest keys that are nearer than twice that bound are summed again, in 64 bits, by the
+// whole block.
 #include <math.h>
 
 #include "experts_tiles.h"
@@ -24,12 +32,12 @@ namespace {
 struct Cut {
     int tokens;            // rows of a tile
     int splits, each, ld;  // ld: a row of partial sums, E rounded up to 4
-    float gamma;           // a logit is off by at most gamma ||x|| ||w||
+    float more;            // (8 + splits) / 4, of the weights below
 };
 
 struct Partial {
-    float *sum, *x2, *w2;  // [splits][T][ld], [splits][T]: parts of logits and of squared norms; [splits][expert tiles]:
-                           // the largest of a tile's experts' squared norms
+    float *sum, *x2, *w2;  // [splits][T][ld], [splits][T]: parts of logits and of rows' weighted squares;
+                           // [splits][expert tiles]: the largest of a tile's experts' weighted squares
 };
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
@@ -47,6 +55,7 @@ __device__ __forceinline__ float squares(bf16x8 v, float sum)
 // Adds up the squares of rows and features; of the waves that share rows or features one does it for a tile of k.
 template <int MF>
 struct Squares {
+    float weight;  // of tile 0; the next ones' is one less each
     float row[MF], feature[4];
 
     template <int N>
@@ -54,15 +63,16 @@ struct Squares {
     {
         if ((kt & 3) != (wave_id() & 3)) return;
 #pragma unroll
-        for (int i = 0; i < N; ++i) row[first + i] = squares(r[i][1], squares(r[i][0], row[first + i]));
+        for (int i = 0; i < N; ++i)
+            row[first + i] = fmaf(weight - (float)kt, squares(r[i][1], squares(r[i][0], 0.0f)), row[first + i]);
     }
     __device__ __forceinline__ void features(int kt, const bf16x8 (&f0)[2][2], const bf16x8 (&f1)[2][2])
     {
         if ((kt & 1) != (wave_id() >> 2)) return;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            feature[i] = squares(f0[i][1], squares(f0[i][0], feature[i]));
-            feature[2 + i] = squares(f1[i][1], squares(f1[i][0], feature[2 + i]));
+            feature[i] = fmaf(weight - (float)kt, squares(f0[i][1], squares(f0[i][0], 0.0f)), feature[i]);
+            feature[2 + i] = fmaf(weight - (float)kt, squares(f1[i][1], squares(f1[i][0], 0.0f)), feature[2 + i]);
         }
     }
 };
@@ -95,6 +105,7 @@ __global__ __launch_bounds__(kGemmThreads, MF <= 2 ? 4 : 2) void router_logits_k
         f.slot(i, w + ((int64_t)e * S.H + k0) * 2, S.E - e);
     }
     Squares<MF> see = {};
+    see.weight = (float)((K + kTileK - 1) / kTileK) + cut.more;
     Acc<MF> acc;
     tile_product<kSmall, MF>(r, f, K, lds, acc, see);
     float* const to = P.sum + ((int64_t)part * S.T + t0) * cut.ld + e0;
@@ -128,10 +139,18 @@ __global__ __launch_bounds__(kGemmThreads, MF <= 2 ? 4 : 2) void router_logits_k
         if (lane == 0) rows[4 * kTokens + 2 * kTileFeatures + wave] = top;
     }
     __syncthreads();
-    if (i == 0) {
-        const float* const t = rows + 4 * kTokens + 2 * kTileFeatures;
-        P.w2[part * across + e0 / kTileFeatures] = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+    const float* const t = rows + 4 * kTokens + 2 * kTileFeatures;
+    float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+    if (top == 0.0f) {  // no squares, or their underflow: then as little as makes `choose` trust no sum
+        const int V = K / 8, vectors = min(kTileFeatures, S.E - e0) * V;
+        unsigned any = 0;
+        for (int v = i; v < vectors; v += kGemmThreads) {
+            const u32x4 a = *(const u32x4*)(w + ((int64_t)(e0 + v / V) * S.H + k0 + v % V * 8) * 2);
+            any |= (a[0] | a[1] | a[2] | a[3]) & 0x7fff7fffu;
+        }
+        if (__syncthreads_or(any != 0)) top = 1e-30f;
     }
+    if (i == 0) P.w2[part * across + e0 / kTileFeatures] = top;
 }
 
 // ---- the choice ----
@@ -314,7 +333,7 @@ __global__ __launch_bounds__(kChooseWaves * kWave, Each <= 4 ? 8 : 1) void route
             zero = __ballot(any != 0) == 0;
             exact = !zero;
         }
-        off = zero ? 0.0f : cut.gamma * sqrtf(x2) * sqrtf(w2) * 1.01f;
+        off = zero ? 0.0f : 4.76837158e-7f * sqrtf(x2) * sqrtf(w2) * 1.01f;
     }
     if (row && !exact) {
         unsigned key[Each];
@@ -825,8 +844,7 @@ Cut cut_of(const RouterShape& S)
     c.each = (int)up(up(S.H, splits), kTileK) * kTileK;
     c.splits = (int)up(S.H, c.each);
     c.ld = (int)up(S.E, 4) * 4;
-    // roundings one after another: a matrix instruction for 32 k, the 32 products inside one, the sum of the parts
-    c.gamma = (float)(c.each / 32 + 32 + c.splits + 8) * 1.1920929e-7f;
+    c.more = (float)(8 + c.splits) / 4;
     return c;
 }
 

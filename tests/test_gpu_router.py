@@ -214,6 +214,42 @@ def test_keys_that_nearly_tie(size, E, rule):
     c.forward().check()
 
 
+@pytest.mark.parametrize("at", [0, 9, 31])
+@pytest.mark.parametrize("T,H", [(64, 256), (300, 7168), (2500, 4096), (8192, 7168)])
+def test_ids_where_sums_round_one_way(T, H, at):
+    """One large element and products of half a step for every eight of them: fp32 sums lose all of these, in one expert
+    above the other, and the choice is still that of exact sums, whatever the large one's lead."""
+    c = Router(T, H, 3, 1)
+    c.x[:] = 2.0 ** -13
+    c.w.zero_()
+    c.w[0, :1792] = 2.0 ** -14  # true sums are up to 224 steps of 2^-23 apart, and leads up to 255
+    c.w[1, :1792] = -2.0 ** -14
+    c.x[:, at] = 1
+    c.w[:2, at] = 1
+    lead = (at + 1) % H
+    c.x[:, lead] = (torch.arange(T, device="cuda") % 256).float() * 2.0 ** -16
+    c.w[:, lead] = 0
+    c.w[1, lead] = 2.0 ** -7
+    c.forward()
+    l = c.x.double() @ c.w.double().T
+    want = ref.choose(l, 1, False)
+    assert bool((want == 0).any()) and bool((want == 1).any())
+    assert torch.equal(c.idx.long(), want)
+
+
+@pytest.mark.parametrize("down", [2.0 ** -70, 2.0 ** -100])
+def test_weights_whose_squares_underflow(down):
+    """Ids as those of the same weights, larger by a power of two; and of zeros, by index."""
+    c = Router(200, 1024, 40, 4, seed=17)
+    near_ties(c, 2.0 ** -10)
+    ids = c.forward().idx.clone()
+    c.check()
+    c.w *= down
+    assert torch.equal(c.forward().idx, ids)
+    c.w[:, :] = 0
+    assert c.forward().idx[5].tolist() == [0, 1, 2, 3]
+
+
 def test_ids_do_not_depend_on_the_batch():
     c = Router(2000, 1024, 96, 6, sigmoid=True, bias=True, seed=3)
     near_ties(c, 2.0 ** -10)

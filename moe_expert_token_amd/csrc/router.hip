@@ -495,6 +495,14 @@ __global__ __launch_bounds__(kChooseWaves * kWave, Each <= 4 ? 8 : 1) void route
 
 // ---- the backward pass ----
 
+// s (1 - s) of a logit's sigmoid, to a few steps of fp32 however large the logit: 1 - s of a rounded s loses 17 % of it
+// at 15, and is 0 from 17 on.
+__device__ __forceinline__ float sigmoid_slope(float l)
+{
+    const float e = expf(-fabsf(l)), d = 1.0f + e;
+    return e / (d * d);
+}
+
 // dl of a row as two bf16 numbers, the second what the first leaves: [2][T][ld], zeros from E to ld (a multiple of 8).
 // The products below take both, so that 16 bits of dl reach the gradients; with the first alone their error against 64
 // bits is 1.4 to 1.5 times that of rounding them to bf16.
@@ -549,10 +557,7 @@ __global__ __launch_bounds__(kChooseWaves * kWave) void router_dlogits_kernel(Ro
             const float g = mine[e];
             if (rule.sigmoid) {
                 // 0 where nothing was chosen, also beside a logit that is not finite
-                if (g != 0.0f) {
-                    const float s = score(l[i]);
-                    d = g * s * (1.0f - s);
-                }
+                if (g != 0.0f) d = g * sigmoid_slope(l[i]);
             } else if (g != mean) {
                 d = score(l[i]) * (g - mean);
             }

@@ -329,6 +329,42 @@ def test_bad_ids_touch_nothing_else():
     assert bool((gx[7] == 0).all())  # nothing was chosen
 
 
+def unit_weights(c):
+    """Weights under which grad_x of columns 0 .. E - 1 is dl, rounded to bf16."""
+    c.w.zero_()
+    at = torch.arange(c.E)
+    c.w[at, at] = 1
+
+
+@pytest.mark.parametrize("T,E", [(31, 8), (1100, 160)])
+@pytest.mark.parametrize("norm", [False, True])
+def test_gradient_of_saturated_sigmoids(norm, T, E):
+    """Chosen logits from -30 to 30: dl keeps its relative accuracy where 1 - s has few bits or none in fp32.  In dl are the
+    roundings of the exponential (4 STEP), of three operations on it and of two on the gradient's side (normalized: two
+    divisions more), in grad_x those to two parts (U^2) and of the output (U)."""
+    c = Router(T, 256, E, 2, sigmoid=True, norm=norm, seed=16).forward()
+    unit_weights(c)
+    at = torch.linspace(-30, 30, T, device="cuda")
+    c.idx[:, 0], c.idx[:, 1] = 3, E - 2
+    c.logits[:, 3], c.logits[:, E - 2] = at, at.flip(0)
+    c.grad[:, 0], c.grad[:, 1] = 1.25, -0.75
+    gx, _ = c.backward(want=("grad_x",))
+    s = 1 / (1 + torch.exp(-c.logits.double().gather(1, c.idx.long())))
+    slope = s * (1 / (1 + torch.exp(c.logits.double().gather(1, c.idx.long()))))
+    g = c.grad.double()
+    if norm:
+        total = s.sum(1, keepdim=True) + 1e-20
+        g = ((g - g.flip(1)) * s.flip(1) + 1e-20 * g) / total / total  # g_j - sum_i g_i s_i / total, the s_j g_j taken out
+    want = torch.zeros(T, 256, dtype=torch.float64, device="cuda").scatter_(1, c.idx.long(), g * slope)
+    far = (gx.double() - want).abs()
+    # normalized, the mean of g is off by the scores' 6 STEP, 7 of their sum, and three of product, sum and division, and
+    # the difference rounds once
+    err = (2.0 ** -8 * (1 + 2.0 ** -6) + 32 * ref.STEP) * want.abs()
+    if norm:
+        err += torch.zeros_like(err).scatter_(1, c.idx.long(), 20 * ref.STEP * 1.25 / total * slope)
+    assert bool((far <= err).all()), f"{float((far / err.clamp(min=1e-300)).max()):.3g} of the bound"
+
+
 def test_no_rows():
     m = ms()
     c = Router(4, 64, 8, 2, seed=10)

@@ -503,6 +503,11 @@ __device__ __forceinline__ float sigmoid_slope(float l)
     return e / (d * d);
 }
 
+__device__ __forceinline__ float lane_value(float v, int lane)
+{
+    return __uint_as_float((unsigned)__builtin_amdgcn_readlane((int)__float_as_uint(v), lane));
+}
+
 // dl of a row as two bf16 numbers, the second what the first leaves: [2][T][ld], zeros from E to ld (a multiple of 8).
 // The products below take both, so that 16 bits of dl reach the gradients; with the first alone their error against 64
 // bits is 1.4 to 1.5 times that of rounding them to bf16.
@@ -513,13 +518,11 @@ __global__ __launch_bounds__(kChooseWaves * kWave) void router_dlogits_kernel(Ro
                                                                               const float* grad_logits,
                                                                               unsigned short* dl, int ld, GridSpan span)
 {
-    __shared__ float ds[kChooseWaves][Each * kWave];
+    __shared__ float slopes[kChooseWaves][Each * kWave];
     const int lane = lane_id(), E = S.E, k = S.k;
     const int64_t t = (int64_t)span_block(span) * kChooseWaves + wave_id();
     if (t >= S.T) return;
-    float* const mine = ds[wave_id()];
-#pragma unroll
-    for (int i = 0; i < Each; ++i) mine[lane + i * kWave] = 0;
+    float* const mine = slopes[wave_id()];
     float l[Each], most = -__builtin_inff(), all = 0;
 #pragma unroll
     for (int i = 0; i < Each; ++i) {
@@ -538,16 +541,38 @@ __global__ __launch_bounds__(kChooseWaves * kWave) void router_dlogits_kernel(Ro
     const int e = lane < k ? idx[t * k + lane] : 0;
     const bool in = lane < k && e >= 0 && e < E;
     const float s = in ? score(logits[t * E + e]) : 0.0f;
-    float g = in ? rule.scale * grad_gate[t * k + lane] : 0.0f;
-    if (rule.normalize) {
-        const float total = wave_total(s) + 1e-20f;
-        g = (g - wave_total(g * s) / total) / total;
-        if (!in) g = 0.0f;
+    const float g = in ? rule.scale * grad_gate[t * k + lane] : 0.0f;
+    // ds of the lane's slot, less `mean`, which is that of the experts not chosen.  With sum s_i = 1, g_j - sum_i g_i s_i is
+    // sum_i s_i (g_j - g_i), which loses nothing where one score is nearly all of the sum: there the plain difference is
+    // rounding errors of g_j.
+    float ds = g, mean = 0;
+    unsigned chosen = 0;  // bit i: expert lane + i * kWave is
+    if (rule.normalize || !rule.sigmoid) {
+        float apart = 0;
+#pragma unroll 1
+        for (int i = 0; i < k; ++i) {
+            const int its = __builtin_amdgcn_readlane(in ? e : -1, i);
+            apart += lane_value(s, i) * (g - lane_value(g, i));
+            if (its >= 0 && (its & (kWave - 1)) == lane) chosen |= 1u << (its / kWave);
+        }
+        if (rule.normalize) {
+            // the chosen scores' sum does not change: the mean is 0, and so is dl of the others
+            const float total = wave_total(s) + 1e-20f;
+            ds = (apart + 1e-20f * g) / total / total;
+        } else {
+            float rest = 0;
+#pragma unroll
+            for (int i = 0; i < Each; ++i)
+                if (lane + i * kWave < E && !(chosen >> i & 1)) rest += expf(l[i] - most);
+            ds = apart + wave_total(rest) / all * g;
+            mean = wave_total(g * s);
+        }
     }
-    // normalized, the chosen scores' sum does not change: the mean is 0, and so is dl of the others
-    const float mean = rule.sigmoid || rule.normalize ? 0.0f : wave_total(g * s);
-    if (in) mine[e] = g;
+#pragma unroll
+    for (int i = 0; i < Each; ++i) mine[lane + i * kWave] = 0.0f - mean;
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // this wave's own LDS
+    if (in) mine[e] = ds;
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 #pragma unroll
     for (int i = 0; i < Each; ++i) {
         const int e = lane + i * kWave;
@@ -555,12 +580,8 @@ __global__ __launch_bounds__(kChooseWaves * kWave) void router_dlogits_kernel(Ro
         float d = 0;
         if (e < E) {
             const float g = mine[e];
-            if (rule.sigmoid) {
-                // 0 where nothing was chosen, also beside a logit that is not finite
-                if (g != 0.0f) d = g * sigmoid_slope(l[i]);
-            } else if (g != mean) {
-                d = score(l[i]) * (g - mean);
-            }
+            // 0 where nothing was chosen, also beside a logit that is not finite
+            if (g != 0.0f) d = g * (rule.sigmoid ? sigmoid_slope(l[i]) : score(l[i]));
             if (grad_logits) d += grad_logits[t * E + e];
         }
         const unsigned first = bf16_pack2(d, d) & 0xffffu;

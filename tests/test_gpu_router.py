@@ -365,6 +365,43 @@ def test_gradient_of_saturated_sigmoids(norm, T, E):
     assert bool((far <= err).all()), f"{float((far / err.clamp(min=1e-300)).max()):.3g} of the bound"
 
 
+@pytest.mark.parametrize("T,E", [(34, 8), (1105, 160), (17, 600)])
+@pytest.mark.parametrize("rule", [dict(norm=False), dict(), dict(sigmoid=True)], ids=["plain", "softmax", "sigmoid"])
+def test_gradient_where_one_score_is_nearly_all(rule, T, E):
+    """The first of three chosen leads by up to 16 in the logits, so that the others' scores are 2^-23 of the sum: dl keeps its
+    relative accuracy.  The gradients are such that no term of sum_i s_i (g_j - g_i) is against another.  A score is off by
+    20 + E / 64 STEP at most (exponential 4, whole numbers' differences none, the sum's terms and additions, division), the
+    sum of the chosen by as much and three, products and sums over the chosen by five: under 100 STEP together."""
+    c = Router(T, 640, E, 3, seed=17, **rule).forward()
+    unit_weights(c)
+    lead = (torch.arange(T, device="cuda") % 17).float()
+    top = 4.0 if c.sigmoid else 20.0
+    c.logits[:] = (top - lead - 6)[:, None]
+    for j, (e, down) in enumerate(((5, 0), (E - 1, lead), (0, lead + 1))):
+        c.idx[:, j] = e
+        c.logits[:, e] = top - down
+    c.grad[:] = torch.tensor([1.25, -0.75, -0.75], device="cuda")
+    gx, _ = c.backward(want=("grad_x",))
+    l, at = c.logits.double(), c.idx.long()
+    want, _ = ref.score_gradient(l, at, c.grad, c.sigmoid, c.norm, 1.0)
+    s = ref.scores(l, c.sigmoid)
+    mine, g = s.gather(1, at), c.grad.double()
+    apart = (mine[:, None, :] * (g[:, :, None] - g[:, None, :]).abs()).sum(2)
+    if c.norm:
+        total = mine.sum(1, keepdim=True)
+        size = torch.zeros_like(s).scatter_(1, at, apart / total ** 2)
+    else:
+        size = (mine * g.abs()).sum(1, keepdim=True).expand_as(s).scatter(1, at, apart + (1 - mine.sum(1, keepdim=True)) * g.abs())
+    size = size * (s * (1 - s) if c.sigmoid else s)
+    err = 2.0 ** -8 * (1 + 2.0 ** -6) * want.abs() + 100 * ref.STEP * size + ref.TINY
+    if c.norm and not c.sigmoid:
+        # of the experts not chosen it is -s_e sum_i ds_i s_i, 0 but for 1e-20 of the gradients; `want` has it as a sum in 64
+        # bits of three terms of |g_i| s_i / D and less, in which 16 roundings of 2^-53 leave up to 2^-49 of those
+        err += 2.0 ** -49 * s * (g.abs() * mine / total).sum(1, keepdim=True) / total
+    far = (gx[:, :E].double() - want).abs()
+    assert bool((far <= err).all()), f"{float((far / err).max()):.3g} of the bound"
+
+
 def test_no_rows():
     m = ms()
     c = Router(4, 64, 8, 2, seed=10)

@@ -323,7 +323,7 @@ __global__ __launch_bounds__(kChooseWaves * kWave, Each <= 4 ? 8 : 1) void route
         // how far a key may be off.  Squares that underflow say nothing, unless all is zero
         const bool tiny = x2 < 8e-25f || w2 < 8e-25f;
         exact = !(x2 <= 1e38f && w2 <= 1e38f);
-        zero = w2 == 0.0f;
+        zero = !exact && w2 == 0.0f;  // weights of 0 make NaN of infinities
         if (!exact && tiny && !zero) {
             unsigned any = 0;
             for (int v = lane; v < V; v += kWave) {

@@ -319,6 +319,27 @@ def test_rows_that_are_not_finite():
     assert torch.equal(s.idx.long(), ref.choose(s.x.double() @ s.w.double().T, 5, True, s.bias))
 
 
+@pytest.mark.parametrize("T", [3, 2100])
+def test_rows_that_are_not_finite_under_zero_weights(T):
+    """0 times infinity or NaN is NaN, of every expert: whatever the bias, the ids are 0 .. k - 1, as the layer's are."""
+    m = ms()
+    c = Router(T, 256, 20, 4, sigmoid=True, bias=True, seed=18)
+    c.w.zero_()
+    c.x[0, 3], c.x[1, 200] = float("nan"), float("inf")
+    c.forward()
+    assert c.idx[:2].tolist() == [[0, 1, 2, 3]] * 2
+    assert bool(c.logits[:2].isnan().all()) and bool((c.logits[2:] == 0).all())
+    first = torch.sort(c.bias.double() + 0.5, descending=True, stable=True).indices[:4]
+    assert bool((c.idx[2:].long() == first).all())
+    for n in (1, 3):
+        dims = m.dims_of(n, 256, 20, 4, 1)
+        ws = torch.empty(m.moe_layer_workspace_size(dims, 8), dtype=torch.uint8, device="cuda")
+        w1, w2 = bf16(c.gen, 20, 16, 256), bf16(c.gen, 20, 256, 8)
+        out, idx = torch.empty(n, 256, dtype=torch.bfloat16, device="cuda"), torch.empty(n, 4, dtype=torch.int32, device="cuda")
+        m.moe_layer_forward(dims, c.rule(), c.x[:n], c.w, w1, w2, out, ws, topk_idx=idx)
+        assert torch.equal(idx, c.idx[:n])
+
+
 def test_bad_ids_touch_nothing_else():
     c = Router(40, 128, 12, 3, seed=9).forward()
     good = c.backward()[0].clone()

@@ -17,9 +17,8 @@
 //   4 2^-23 sqrt(sum_i c_i x_i^2) sqrt(sum_i c_i w_i^2),    c_i = the tiles from k = i on + (8 + splits) / 4
 //
 // The weighted squares come out of the same product for nothing (the fragments are in registers: one of four waves
-// squares a tile of k).  One large product before thousands of 2^-27 of it reaches nine tenths of it.  Two
-// neighbours among the k + 1 largest keys that are nearer than twice that bound are summed again, in 64 bits, by the
-// whole block.
+// squares a tile of k).  One large product before thousands of 2^-27 of it reaches nine tenths of it.  Of
+// the k + 1 largest keys those whose order that bound leaves open are summed again, in 64 bits, by the whole block.
 #include <math.h>
 
 #include "experts_tiles.h"
@@ -412,9 +411,22 @@ __global__ __launch_bounds__(kChooseWaves * kWave, Each <= 4 ? 8 : 1) void route
                 slack = off * fminf(fabsf(s * (1.0f - s)) + 0.1f * off + 1e-6f, 0.25f) + rounds;
                 if (!(slack >= 0.0f)) slack = widest;  // beside an infinite bias
             }
-            const float after = __shfl_down(v, 1, kWave), both = slack + __shfl_down(slack, 1, kWave);
-            // nothing is off where all keys are exact: equal ones are listed in the order of their indexes
-            again = __ballot(widest > 0 && lane + 1 < m && v - after <= both);
+            // Listed neighbours are told apart where no key up to the one can be as small as one from the other on.  Without a
+            // bias all may be off by as much, and the two themselves say it; with one, a key that may be far off can reach
+            // past neighbours that are not.  Infinite keys, those beside an infinite bias, are exact, and in order.
+            const float after = __shfl_down(v, 1, kWave);
+            bool near = widest > 0 && v - after <= 2 * off;
+            if (rule.bias) {
+                float lowest = lane < m ? v - slack : __builtin_inff(), highest = lane < m ? v + slack : -__builtin_inff();
+#pragma unroll
+                for (int d = 1; d < kWave; d <<= 1) {
+                    lowest = fminf(lowest, __shfl_up(lowest, d, kWave));
+                    highest = fmaxf(highest, __shfl_down(highest, d, kWave));
+                }
+                highest = __shfl_down(highest, 1, kWave);  // of all lanes: a shuffle reads none that are left out
+                near = fabsf(after) <= 3.40282347e38f && !(lowest > highest);
+            }
+            again = __ballot(lane + 1 < m && near);  // equal keys that are exact are listed in the order of their indexes
             again |= again << 1;
             if (__popcll(again) > kAgain) exact = true;
         }

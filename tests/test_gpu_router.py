@@ -237,6 +237,35 @@ def test_ids_where_sums_round_one_way(T, H, at):
     assert torch.equal(c.idx.long(), want)
 
 
+@pytest.mark.parametrize("above", [True, False])
+@pytest.mark.parametrize("below", [True, False])
+@pytest.mark.parametrize("T", [70, 2100])
+def test_ids_where_one_key_is_less_sure_than_its_neighbours(T, below, above):
+    """Expert 0's logit is near 1 and its fp32 sum off by 55 2^-20, 1e-5 of the key; those of 1 and 2 are 42.5 and their keys off
+    by a step at most, which the biases set: 1 is clear of 2 by 5e-6, and 0 comes out of fp32 beyond 1 (`above`: above both,
+    else below) but is exactly within a step of 2, on the side where 2's fp32 key has it wrong."""
+    c = Router(T, 448, 3, 2 if above else 1, sigmoid=True, bias=True)
+    c.x[:] = 2.0 ** -13
+    c.x[:, 9], c.x[:, 447] = 17, -16
+    c.w.zero_()
+    c.w[0] = -2.0 ** -10 if above else 2.0 ** -10  # sums of eight are half a step of 17, and lost
+    c.w[0, 9] = c.w[0, 447] = 1
+    c.w[1:, 9] = 2.5
+    step = 2.0 ** -23  # of keys from 1 to 2
+    # the key 1 + bias of expert 2 is rounded down by 3/8 of a step, or up; and 0's is an eighth to 3/8 from its exact one
+    c.bias[2] = 2.0 ** -10 + (0.375 if below else 0.625) * step
+    exact = 1 + c.bias[2].double()
+    c.bias[1] = c.bias[2] + (5e-6 if above else -5e-6)
+    s = ref.scores(c.x[:1].double() @ c.w.double().T, True)[0, 0]
+    c.bias[0] = (exact + (-0.25 if below else 0.25) * step - s).float()
+    off = float(s + c.bias[0].double() - exact) / step
+    assert 0.1 < (-off if below else off) < 0.37
+    c.forward()
+    want = ref.choose(c.x.double() @ c.w.double().T, c.k, True, c.bias)
+    assert want[0].tolist() == ([1] if above else []) + [2 if below else 0]
+    assert torch.equal(c.idx.long(), want)
+
+
 @pytest.mark.parametrize("down", [2.0 ** -70, 2.0 ** -100])
 def test_weights_whose_squares_underflow(down):
     """Ids as those of the same weights, larger by a power of two; and of zeros, by index."""

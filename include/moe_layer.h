@@ -21,10 +21,10 @@
  *               the rule normalizes                    the gates, fp32
  *
  * The choice of experts and their order are those of logits summed in 64 bits
- * (of exact products), whatever the number of rows and whichever call routes
- * them: a token is routed alike in a long prompt, alone, and by
- * moe_layer_forward.  Sums in 32 bits would swap experts whose keys nearly
- * tie, and another sum order would swap others.
+ * (of exact products, in one order of additions that goes by H alone), whatever
+ * the number of rows and whichever call routes them: a token is routed alike in
+ * a long prompt, alone, and by moe_layer_forward.  Sums in 32 bits would swap
+ * experts whose keys nearly tie, and another sum order would swap others.
  *
  * No output may overlap an input, another output or the workspace
  * (MOE_SHUFFLE_E_INVALID_ARG), but for `residual` and `grad_x_in`, which may be

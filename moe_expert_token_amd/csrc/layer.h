@@ -70,6 +70,117 @@ __device__ __forceinline__ unsigned long long ordered_key(double v)
 
 __device__ __forceinline__ double score64(double l) { return 1.0 / (1.0 + exp(-l)); }
 
+// The sums in 64 bits that the choice of experts goes by have one order, whichever kernel makes them, so that a token is
+// routed alike by all calls also where products span more than 53 bits and the sum depends on their order: vectors of
+// eight k are dealt to kSumParts parts of a wave each (vector v: lane v % 64 of part v / 64 % 8), a lane adds its products
+// in the order of k, the lanes of a part are added those 32 apart first, then 16, 8, 4, 2, 1, and the parts in turn.
+constexpr int kSumParts = 8;
+
+// A double by its two registers.
+union Halves {
+    double d;
+    unsigned u[2];
+};
+
+// a and b so that their sum is, in the lower of each two groups of D lanes, a's of both groups, in the upper b's.
+template <int D>
+__device__ __forceinline__ void exchange(double& a, double& b)
+{
+    Halves x, y;
+    x.d = a;
+    y.d = b;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        if constexpr (D == 32) {
+            const auto r = __builtin_amdgcn_permlane32_swap(x.u[i], y.u[i], false, false);
+            x.u[i] = r[0];
+            y.u[i] = r[1];
+        } else if constexpr (D == 16) {
+            const auto r = __builtin_amdgcn_permlane16_swap(x.u[i], y.u[i], false, false);
+            x.u[i] = r[0];
+            y.u[i] = r[1];
+        } else {
+            const bool upper = lane_id() & D;
+            const unsigned keep = upper ? y.u[i] : x.u[i], give = upper ? x.u[i] : y.u[i];
+            x.u[i] = keep;
+            y.u[i] = __shfl_xor(give, D, kWave);
+        }
+    }
+    a = x.d;
+    b = y.d;
+}
+
+// The value of the lane D further on in a row of sixteen, around its end.
+template <int D>
+__device__ __forceinline__ double turned(double v)
+{
+    Halves x;
+    x.d = v;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) x.u[i] = (unsigned)__builtin_amdgcn_update_dpp(0, (int)x.u[i], 0x120 + D, 0xf, 0xf, false);
+    return x.d;
+}
+
+// The wave's sums of N values a lane (a power of two, up to 32): each exchange halves the values that a lane is left
+// with, so that N + 5 or so of them do it and not 6 N.  Leaves one sum; returns which: the upper bits of the lane, so
+// the first of 64 / N lanes each.
+template <int N, int D = kWave / 2>
+__device__ __forceinline__ int wave_sums(double (&v)[N], double* sum)
+{
+    if constexpr (N == 1) {
+        double a = v[0];
+        if constexpr (D >= 16) {  // both are `a`: the sum is the same in both groups
+            double b = a;
+            exchange<D>(a, b);
+            double more[1] = {a + b};
+            return wave_sums<1, D / 2>(more, sum);
+        } else if constexpr (D == 8) {
+            // the partner is that many lanes on: what comes out repeats itself as often in the row
+            a += turned<8>(a);
+            a += turned<4>(a);
+            a += turned<2>(a);
+            a += turned<1>(a);
+        } else {
+#pragma unroll
+            for (int d = D; d > 0; d >>= 1) a += __shfl_xor(a, d, kWave);
+        }
+        *sum = a;
+        return 0;
+    } else {
+        double half[N / 2];
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+            double a = v[i], b = v[i + N / 2];
+            exchange<D>(a, b);
+            half[i] = a + b;
+        }
+        return (lane_id() & D ? N / 2 : 0) + wave_sums<N / 2, D / 2>(half, sum);
+    }
+}
+
+__device__ __forceinline__ float lane_value(float v, int lane)
+{
+    return __uint_as_float((unsigned)__builtin_amdgcn_readlane((int)__float_as_uint(v), lane));
+}
+
+__device__ __forceinline__ double lane_value(double v, int lane)
+{
+    Halves x;
+    x.d = v;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) x.u[i] = (unsigned)__builtin_amdgcn_readlane((int)x.u[i], lane);
+    return x.d;
+}
+
+template <class Part>
+__device__ __forceinline__ double parts_total(Part&& part)
+{
+    double l = 0;
+#pragma unroll
+    for (int i = 0; i < kSumParts; ++i) l += part(i);
+    return l;
+}
+
 template <int Ctrl, int Rows>
 __device__ __forceinline__ unsigned dpp_max(unsigned v)
 {

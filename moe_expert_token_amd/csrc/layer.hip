@@ -6,8 +6,8 @@
 // experts of all tokens anew from the scores and makes its own list of row tiles, where a plan, a dispatch and a copy of
 // the rows would be three launches.
 //
-//   scores   l = x w^T, one expert a block: products of bf16 numbers are exact in fp32, and are summed in 64 bits, so
-//            that the choice does not depend on the sum's order
+//   scores   l = x w^T, one expert a block: products of bf16 numbers are exact in fp32, and are summed in 64 bits, in
+//            the order that layer.h sets for all calls
 //   up       the choice, the list of tiles (an expert and up to 16 or 32 of its tokens), act(g) u for each, fp32
 //            rounded once to bf16.  The tokens of an expert are the bits of one 64-bit word.
 //   down     y = h Wd^T in fp32 for each tile; the block that finishes a column last (a counter a column, cleared by
@@ -25,36 +25,15 @@ using namespace stream;
 
 __device__ __forceinline__ double as_double(unsigned bits) { return (double)__uint_as_float(bits); }
 
-// The wave's sums of N values a lane (a power of two, up to 32): each exchange halves the values that a lane is left
-// with, so that N + 5 or so of them do it and not 6 N.  Leaves one sum; returns which.
-template <int N, int D = kWave / 2>
-__device__ __forceinline__ int wave_sums(double (&v)[N], double* sum)
-{
-    if constexpr (N == 1) {
-        *sum = v[0];
-#pragma unroll
-        for (int d = D; d > 0; d >>= 1) *sum += __shfl_xor(*sum, d, kWave);
-        return 0;
-    } else {
-        const bool upper = lane_id() & D;
-        double half[N / 2];
-#pragma unroll
-        for (int i = 0; i < N / 2; ++i) {
-            const double keep = upper ? v[i + N / 2] : v[i], give = upper ? v[i] : v[i + N / 2];
-            half[i] = keep + __shfl_xor(give, D, kWave);
-        }
-        return (upper ? N / 2 : 0) + wave_sums<N / 2, D / 2>(half, sum);
-    }
-}
-
 // Experts [Experts blockIdx.x, ...) and Tokens tokens a block; its waves share H.  What a number costs is its way
 // to 64 bits, so with many tokens four experts share it (48 tokens, 256 experts, H = 7168: 18 us).
 template <int Tokens, int Experts, int Threads>
 __global__ __launch_bounds__(Threads) void layer_scores_kernel(LayerShape S, Rule rule, const u32x4* x,
                                                                      const u32x4* w, int columns)
 {
-    constexpr int kParts = Threads / kWave, kSums = Tokens * Experts;
-    __shared__ double part[kParts][kSums];
+    constexpr int kSums = Tokens * Experts;
+    static_assert(Threads == kSumParts * kWave, "a wave is a part of the sums");
+    __shared__ double part[kSumParts][kSums];
     const int e0 = blockIdx.x * Experts, t0 = blockIdx.y * Tokens, V = S.H / 8;
     if (e0 == 0 && t0 == 0)
         for (int i = threadIdx.x; i < columns; i += Threads) S.arrived[i] = 0;
@@ -87,9 +66,7 @@ __global__ __launch_bounds__(Threads) void layer_scores_kernel(LayerShape S, Rul
     __syncthreads();
     const int t = t0 + (int)threadIdx.x % Tokens, e = e0 + (int)threadIdx.x / Tokens;
     if ((int)threadIdx.x >= kSums || t >= S.T || e >= S.E) return;
-    double l = 0;
-#pragma unroll
-    for (int i = 0; i < kParts; ++i) l += part[i][threadIdx.x];
+    const double l = parts_total([&](int i) { return part[i][threadIdx.x]; });
     const int64_t at = (int64_t)t * S.E + e;
     S.logit[at] = (float)l;
     S.key[at] = ordered_key(rule.bias ? score64(l) + (double)rule.bias[e] : l);
@@ -147,20 +124,32 @@ __device__ __forceinline__ void own_scores_of(const LayerShape& S, const Rule& r
     const int V = S.H / 8;
     for (int p = wave_id(); p < S.T * S.E; p += kWaves) {
         const int t = p / S.E, e = p - t * S.E;
-        double sum = 0;
-        for (int v = lane_id(); v < V; v += kWave) {
-            const u32x4 a = w[(int64_t)e * V + v], b = x[(int64_t)t * V + v];
+        double sum[kSumParts] = {};
+        for (int v0 = lane_id(); v0 < V; v0 += kSumParts * kWave) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                sum = fma(as_double(a[c] << 16), as_double(b[c] << 16), sum);
-                sum = fma(as_double(a[c] & 0xffff0000u), as_double(b[c] & 0xffff0000u), sum);
+            for (int i = 0; i < kSumParts; ++i) {
+                const int v = v0 + i * kWave;
+                if (v >= V) break;
+                const u32x4 a = w[(int64_t)e * V + v], b = x[(int64_t)t * V + v];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    sum[i] = fma(as_double(a[c] << 16), as_double(b[c] << 16), sum[i]);
+                    sum[i] = fma(as_double(a[c] & 0xffff0000u), as_double(b[c] & 0xffff0000u), sum[i]);
+                }
             }
         }
-#pragma unroll
-        for (int d = 1; d < kWave; d <<= 1) sum += __shfl_xor(sum, d, kWave);
+        double l;
+        if (V <= kWave) {  // the other parts are 0
+            double first[1] = {sum[0]};
+            wave_sums(first, &l);
+        } else {
+            double mine;
+            wave_sums(sum, &mine);  // part i in lanes 8 i on
+            l = parts_total([&](int i) { return lane_value(mine, i * (kWave / kSumParts)); });
+        }
         if (lane_id() == 0) {
-            C.logit[p] = (float)sum;
-            C.key[p] = ordered_key(rule.bias ? score64(sum) + (double)rule.bias[e] : sum);
+            C.logit[p] = (float)l;
+            C.key[p] = ordered_key(rule.bias ? score64(l) + (double)rule.bias[e] : l);
         }
     }
 }
@@ -616,7 +605,7 @@ size_t layer_workspace(LayerShape* S, char* base)
 hipError_t launch_layer(const LayerShape& S, const Rule& rule, const LayerCall& C, hipStream_t s)
 {
     const hipError_t e = own_scores(S) ? hipSuccess
-                         : S.T == 1 ? launch_scores<1, 1, 1024>(S, rule, C, s)
+                         : S.T == 1 ? launch_scores<1, 1, 512>(S, rule, C, s)
                          : S.T <= 4 ? launch_scores<4, 1, 512>(S, rule, C, s)
                                     : launch_scores<8, 4, 512>(S, rule, C, s);
     if (e != hipSuccess) return e;

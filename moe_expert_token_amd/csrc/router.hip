@@ -157,40 +157,55 @@ __global__ __launch_bounds__(kGemmThreads, MF <= 2 ? 4 : 2) void router_logits_k
 constexpr int kChooseWaves = 4;
 constexpr int kAtOnce = 8;  // partial sums on their way
 
-// Vectors [from, to) of x . w[e] in 64 bits for two experts, the same in every lane.
-__device__ __forceinline__ void exact_logits(const u32x4* x, const u32x4* w, int e0, int e1, int V, int from, int to,
-                                             double (&out)[2])
+// Parts 2 share and 2 share + 1 of x . w[e] in 64 bits for two experts: part 2 share + h of expert n in the lanes from
+// 16 (2 n + h) on.
+__device__ __forceinline__ double exact_parts(const u32x4* x, const u32x4* w, int e0, int e1, int V, int share)
 {
-    constexpr int kAhead = 4;
+    constexpr int kAhead = 4;  // vectors on their way: two of each part
     const u32x4 *const w0 = w + (int64_t)e0 * V, *const w1 = w + (int64_t)e1 * V;
-    double sum[2] = {};
+    double sum[4] = {};
 #pragma unroll 1
-    for (int v0 = from + lane_id(); v0 < to; v0 += kAhead * kWave) {
+    for (int v0 = 2 * share * kWave + lane_id(); v0 < V; v0 += kAhead / 2 * kSumParts * kWave) {
         u32x4 a[kAhead], b[2][kAhead];
+        const auto at = [&](int i) { return v0 + (i / 2 * kSumParts + i % 2) * kWave; };
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {  // past the end the last vector, which is left out below
-            const unsigned v = min(v0 + i * kWave, to - 1);
+            const unsigned v = min(at(i), V - 1);
             a[i] = x[v];
             b[0][i] = w0[v];
             b[1][i] = w1[v];
         }
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
-            if (v0 + i * kWave >= to) break;
+            if (at(i) >= V) break;
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 const double lo = (double)bf16_lo(a[i][c]), hi = (double)bf16_hi(a[i][c]);
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
-                    sum[n] = fma(hi, (double)bf16_hi(b[n][i][c]), fma(lo, (double)bf16_lo(b[n][i][c]), sum[n]));
+                for (int n = 0; n < 2; ++n) {
+                    double& to = sum[2 * n + i % 2];
+                    to = fma(hi, (double)bf16_hi(b[n][i][c]), fma(lo, (double)bf16_lo(b[n][i][c]), to));
+                }
             }
         }
     }
+    double mine;
+    wave_sums(sum, &mine);
+    return mine;
+}
+
+// x . w[e] in 64 bits for two experts, the same in every lane.
+__device__ __forceinline__ void exact_logits(const u32x4* x, const u32x4* w, int e0, int e1, int V, double (&out)[2])
+{
+    out[0] = out[1] = 0;
+#pragma unroll 1
+    for (int share = 0; share < kSumParts / 2; ++share) {
+        const double mine = exact_parts(x, w, e0, e1, V, share);
 #pragma unroll
-    for (int n = 0; n < 2; ++n) {
-#pragma unroll
-        for (int d = 1; d < kWave; d <<= 1) sum[n] += __shfl_xor(sum[n], d, kWave);
-        out[n] = sum[n];
+        for (int n = 0; n < 2; ++n) {
+            out[n] += lane_value(mine, 32 * n);
+            out[n] += lane_value(mine, 32 * n + 16);
+        }
     }
 }
 
@@ -222,7 +237,7 @@ __device__ __forceinline__ int choose_exact(const RouterShape& S, const Rule& ru
 #pragma unroll 1
             for (int i = 0; i < kWave && e0 + i < S.E; i += 2) {
                 double d[2];
-                exact_logits(x, w, e0 + i, min(e0 + i + 1, S.E - 1), V, 0, V, d);
+                exact_logits(x, w, e0 + i, min(e0 + i + 1, S.E - 1), V, d);
                 if (lane == i) l = d[0];
                 if (lane == i + 1) l = d[1];
             }
@@ -272,7 +287,7 @@ __global__ __launch_bounds__(kChooseWaves * kWave, Each <= 4 ? 8 : 1) void route
                                                                              ChooseArgs A, GridSpan span)
 {
     __shared__ unsigned long long keys[kChooseWaves][Each * kWave];
-    __shared__ double part[kChooseWaves][kAgain][kChooseWaves];  // of a row's candidates, by the wave that summed it
+    __shared__ double part[kChooseWaves][kAgain][kSumParts];  // of a row's candidates
     __shared__ int again_of[kChooseWaves][kAgain], agains[kChooseWaves];
     const int lane = lane_id(), wave = wave_id(), E = S.E, k = S.k, V = S.H / 8;
     const int64_t t = (int64_t)span_block(span) * kChooseWaves + wave;
@@ -437,21 +452,17 @@ __global__ __launch_bounds__(kChooseWaves * kWave, Each <= 4 ? 8 : 1) void route
     if (sum_again && (again >> lane & 1)) again_of[wave][place] = mine;
     if (lane == 0) agains[wave] = sum_again ? __popcll(again) : 0;
     __syncthreads();
-    // the block's waves share such a row: a quarter of H each, two experts at a time (they come in pairs)
-    const int quarter = (V + kChooseWaves - 1) / kChooseWaves, from = min(wave * quarter, V), to = min(from + quarter, V);
+    // the block's waves share such a row: two parts of the sums each, two experts at a time
+    static_assert(kSumParts == 2 * kChooseWaves, "two parts a wave");
 #pragma unroll 1
     for (int r = 0; r < kChooseWaves; ++r) {
         const int n = __builtin_amdgcn_readfirstlane(agains[r]);
 #pragma unroll 1
         for (int i = 0; i < n; i += 2) {
             const int j = min(i + 1, n - 1);
-            double d[2];
-            exact_logits(A.x + (t - wave + r) * V, A.w, __builtin_amdgcn_readfirstlane(again_of[r][i]),
-                         __builtin_amdgcn_readfirstlane(again_of[r][j]), V, from, to, d);
-            if (lane == 0) {
-                part[r][i][wave] = d[0];
-                part[r][j][wave] = d[j - i];
-            }
+            const double d = exact_parts(A.x + (t - wave + r) * V, A.w, __builtin_amdgcn_readfirstlane(again_of[r][i]),
+                                         __builtin_amdgcn_readfirstlane(again_of[r][j]), V, wave);
+            if (lane % 16 == 0) part[r][lane < 32 ? i : j][2 * wave + lane / 16 % 2] = d;
         }
     }
     __syncthreads();
@@ -463,7 +474,7 @@ __global__ __launch_bounds__(kChooseWaves * kWave, Each <= 4 ? 8 : 1) void route
         double key64 = (double)key_value(my_key);
         if (again >> lane & 1) {
             const double* const d = part[wave][place];
-            const double l64 = zero ? 0.0 : (d[0] + d[1]) + (d[2] + d[3]);
+            const double l64 = zero ? 0.0 : parts_total([&](int i) { return d[i]; });
             key64 = rule.bias ? score64(l64) + (double)rule.bias[mine] : l64;
         }
         const unsigned long long u = lane < m ? ordered_key(key64) : 0;
@@ -513,11 +524,6 @@ __device__ __forceinline__ float sigmoid_slope(float l)
 {
     const float e = expf(-fabsf(l)), d = 1.0f + e;
     return e / (d * d);
-}
-
-__device__ __forceinline__ float lane_value(float v, int lane)
-{
-    return __uint_as_float((unsigned)__builtin_amdgcn_readlane((int)__float_as_uint(v), lane));
 }
 
 // dl of a row as two bf16 numbers, the second what the first leaves: [2][T][ld], zeros from E to ld (a multiple of 8).

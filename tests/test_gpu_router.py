@@ -298,6 +298,39 @@ def test_ids_do_not_depend_on_the_batch():
             assert torch.equal(idx, ids[lo:lo + n])
 
 
+@pytest.mark.parametrize("rule", RULES[:2], ids=NAMES[:2])
+@pytest.mark.parametrize("E", [4, 8, 40])
+@pytest.mark.parametrize("H", [64, 1000, 4096, 7168])
+def test_sums_that_depend_on_their_order(H, E, rule):
+    """Logits of 0, of products of 2^-40 to 2^40 each of which some other one cancels: what 64 bits leave of them goes by the
+    order of the additions, and so do the ids.  They are the same of many rows, few and one, and by every form of the
+    layer's scores."""
+    m = ms()
+    c = Router(2100, H, E, 3, seed=H + E, **rule)
+    order = torch.randperm(H, device="cuda", generator=c.gen)
+    one, other = order[:H // 2], order[H // 2:]
+    for t in (c.x, c.w):
+        t.mul_(torch.exp2(40 * torch.rand(t.shape, device="cuda", generator=c.gen) - 20).to(torch.bfloat16))
+    c.x[:, other] = -c.x[:, one]
+    c.w[:, other] = c.w[:, one]
+    if c.bias is not None:
+        c.bias.zero_()
+    ids = c.forward().idx.clone()
+    assert len(set(map(tuple, ids.tolist()))) > 3  # as the sums' ends fall
+    for n in (1, 2, 3, 8, 40, 300):
+        d = Router(n, H, E, 3, sigmoid=c.sigmoid, seed=4)
+        d.x, d.w, d.bias = c.x[:n].contiguous(), c.w, c.bias
+        assert torch.equal(d.forward().idx, ids[:n]), f"{n} rows"
+        if n > 64:
+            continue
+        dims = m.dims_of(n, H, E, 3, 1)
+        ws = torch.empty(m.moe_layer_workspace_size(dims, 8), dtype=torch.uint8, device="cuda")
+        w1, w2 = torch.zeros(E, 16, H, dtype=torch.bfloat16, device="cuda"), torch.zeros(E, H, 8, dtype=torch.bfloat16, device="cuda")
+        out, idx = torch.empty_like(d.x), torch.empty(n, 3, dtype=torch.int32, device="cuda")
+        m.moe_layer_forward(dims, d.rule(), d.x, d.w, w1, w2, out, ws, topk_idx=idx)
+        assert torch.equal(idx, ids[:n]), f"layer of {n} rows"
+
+
 @pytest.mark.parametrize("rule", RULES, ids=NAMES)
 def test_ties_and_zero_rows(rule):
     c = Router(130, 256, 100, 5, seed=5, **rule)

@@ -541,6 +541,8 @@ __global__ __launch_bounds__(kChooseWaves * kWave) void router_dlogits_kernel(Ro
     const int64_t t = (int64_t)span_block(span) * kChooseWaves + wave_id();
     if (t >= S.T) return;
     float* const mine = slopes[wave_id()];
+#pragma unroll
+    for (int i = 0; i < Each; ++i) mine[lane + i * kWave] = 0;
     float l[Each], most = -__builtin_inff(), all = 0;
 #pragma unroll
     for (int i = 0; i < Each; ++i) {
@@ -558,48 +560,45 @@ __global__ __launch_bounds__(kChooseWaves * kWave) void router_dlogits_kernel(Ro
     const auto score = [&](float v) { return rule.sigmoid ? 1.0f / (1.0f + expf(-v)) : expf(v - most) / all; };
     const int e = lane < k ? idx[t * k + lane] : 0;
     const bool in = lane < k && e >= 0 && e < E;
-    const float s = in ? score(logits[t * E + e]) : 0.0f;
+    const float its = in ? logits[t * E + e] : 0.0f, s = in ? score(its) : 0.0f;
     const float g = in ? rule.scale * grad_gate[t * k + lane] : 0.0f;
     // ds of the lane's slot, less `mean`, which is that of the experts not chosen.  With sum s_i = 1, g_j - sum_i g_i s_i is
     // sum_i s_i (g_j - g_i), which loses nothing where one score is nearly all of the sum: there the plain difference is
     // rounding errors of g_j.
     float ds = g, mean = 0;
-    unsigned chosen = 0;  // bit i: expert lane + i * kWave is
+    unsigned others = 0;  // bit i: expert lane + i * kWave is not chosen, and its dl not 0
     if (rule.normalize || !rule.sigmoid) {
         float apart = 0;
-#pragma unroll 1
-        for (int i = 0; i < k; ++i) {
-            const int its = __builtin_amdgcn_readlane(in ? e : -1, i);
-            apart += lane_value(s, i) * (g - lane_value(g, i));
-            if (its >= 0 && (its & (kWave - 1)) == lane) chosen |= 1u << (its / kWave);
-        }
+        for (int i = 0; i < k; ++i) apart += lane_value(s, i) * (g - lane_value(g, i));
         if (rule.normalize) {
             // the chosen scores' sum does not change: the mean is 0, and so is dl of the others
             const float total = wave_total(s) + 1e-20f;
             ds = (apart + 1e-20f * g) / total / total;
         } else {
+            others = ~0u;
+            for (int i = 0; i < k; ++i) {
+                const int its = __builtin_amdgcn_readlane(in ? e : -1, i);
+                if (its >= 0 && (its & (kWave - 1)) == lane) others &= ~(1u << (its / kWave));
+            }
             float rest = 0;
 #pragma unroll
             for (int i = 0; i < Each; ++i)
-                if (lane + i * kWave < E && !(chosen >> i & 1)) rest += expf(l[i] - most);
+                if (lane + i * kWave < E && (others >> i & 1)) rest += expf(l[i] - most);
             ds = apart + wave_total(rest) / all * g;
             mean = wave_total(g * s);
         }
     }
-#pragma unroll
-    for (int i = 0; i < Each; ++i) mine[lane + i * kWave] = 0.0f - mean;
+    // 0 also beside a logit that is not finite
+    if (in) mine[e] = ds != 0.0f ? ds * (rule.sigmoid ? sigmoid_slope(its) : s) : 0.0f;
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // this wave's own LDS
-    if (in) mine[e] = ds;
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 #pragma unroll
     for (int i = 0; i < Each; ++i) {
         const int e = lane + i * kWave;
         if (e >= ld) continue;
         float d = 0;
         if (e < E) {
-            const float g = mine[e];
-            // 0 where nothing was chosen, also beside a logit that is not finite
-            if (g != 0.0f) d = g * (rule.sigmoid ? sigmoid_slope(l[i]) : score(l[i]));
+            d = mine[e];
+            if ((others >> i & 1) && mean != 0.0f) d = -mean * score(l[i]);
             if (grad_logits) d += grad_logits[t * E + e];
         }
         const unsigned first = bf16_pack2(d, d) & 0xffffu;

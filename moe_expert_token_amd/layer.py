@@ -54,14 +54,18 @@ def _load():
 
 class RouterRule:
     """How logits become gates: the scores, whether the chosen ones are normalized, their scale, and (sigmoid scores
-    only) a bias fp32 [E] that the choice goes by and the gates do not.  Holds the bias."""
+    only) a bias fp32 [E] that the choice goes by and the gates do not.  `bias` may be written to or set to another
+    tensor between calls: each call takes the one that is there."""
 
     def __init__(self, scoring: int = SCORE_SOFTMAX, normalize: bool = True, scale: float = 1.0, bias=None):
         if bias is not None and (bias.dtype != torch.float32 or bias.dim() != 1):
             _refuse("RouterRule", "bias must be float32 [E]")
         self.bias = bias
-        self.struct = _Rule(int(scoring), int(bool(normalize)), float(scale), 0,
-                            None if bias is None else bias.data_ptr())
+        self._fixed = int(scoring), int(bool(normalize)), float(scale), 0
+
+    @property
+    def struct(self):
+        return _Rule(*self._fixed, None if self.bias is None else self.bias.data_ptr())
 
 
 def _f32(func: str, name: str, t, shape):
@@ -81,8 +85,9 @@ def _ids(func: str, t, shape):
 
 
 def _bias(func: str, rule: RouterRule, E: int):
-    if rule.bias is not None and (rule.bias.numel() != E or not rule.bias.is_contiguous()):
-        _refuse(func, f"the rule's bias must be contiguous [{E}], not {list(rule.bias.shape)}")
+    b = rule.bias
+    if b is not None and (b.dtype != torch.float32 or tuple(b.shape) != (E,) or not b.is_contiguous()):
+        _refuse(func, f"the rule's bias must be contiguous float32 [{E}], not {list(b.shape)} of {b.dtype}")
 
 
 def moe_router_workspace_size(dims: Dims, backward: bool = False) -> int:

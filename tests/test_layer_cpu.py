@@ -220,6 +220,37 @@ def test_rules_that_are_refused():
             ms.RouterRule(ms.SCORE_SIGMOID, bias=bias)
 
 
+@pytest.mark.parametrize("which", CALLS)
+def test_the_rules_bias_is_that_of_the_call(which, monkeypatch):
+    """A bias set anew, or one whose memory moved, after the rule was made: the library is given the new address."""
+    ms, layer, _ = _ms()
+    call, args = binding_calls(ms)[which]
+    seen = []
+
+    class Library:
+        def __getattr__(self, name):
+            return lambda dims, rule, *rest: seen.append(rule._obj.bias) or 0
+
+    monkeypatch.setattr(layer, "_load", Library)
+    monkeypatch.setattr(layer, "_on_gpu", lambda *a, **k: None)
+    rule = ms.RouterRule(ms.SCORE_SIGMOID, bias=torch.zeros(8))
+    first, other = rule.bias, torch.ones(8)
+    call(**dict(args, rule=rule), stream=Stream())
+    rule.bias = other
+    call(**dict(args, rule=rule), stream=Stream())
+    moved = torch.ones(8)
+    other.data = moved
+    call(**dict(args, rule=rule), stream=Stream())
+    rule.bias = None
+    call(**dict(args, rule=rule), stream=Stream())
+    assert seen == [first.data_ptr(), seen[1], moved.data_ptr(), None] and seen[1] not in (seen[0], seen[2])
+    if which != "back":
+        for bias in (torch.zeros(8, dtype=torch.float64), torch.zeros(8, 1), torch.zeros(9)):
+            rule.bias = bias
+            with pytest.raises(ms.MoeShuffleError):
+                call(**dict(args, rule=rule), stream=Stream())
+
+
 # ---- the tests' own definition ----
 
 @pytest.mark.parametrize("sigmoid", [False, True])

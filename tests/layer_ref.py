@@ -15,6 +15,25 @@ def logits(x, w):
     return x.double() @ w.double().T
 
 
+def logit_bound(x, w, T=None):
+    """How far the router's fp32 logits may be off, of each row and expert: 4 2^-23 sqrt(sum c_i x_i^2) sqrt(sum c_i w_i^2),
+    with c_i the tiles of 64 k from i on in its part of H and (8 + parts) / 4 more.  The parts are those of a batch of T rows
+    (x's own where not given): as many, a power of two up to 16, as fill the card with blocks and leave four tiles each."""
+    (rows, H), E = x.shape, w.shape[0]
+    T = rows if T is None else T
+    tokens, blocks = (128, 256) if T >= 2048 else (64, 512)
+    tiles, parts = -(-T // tokens) * -(-E // 256), 1
+    while parts < 16 and tiles * parts * 2 <= blocks and H >= parts * 2 * 4 * 64:
+        parts *= 2
+    each = -(-(-(-H // parts)) // 64) * 64
+    parts = -(-H // each)
+    i = torch.arange(H, device=x.device)
+    k0 = i // each * each
+    c = (-(-(H - k0).clamp(max=each) // 64) - (i - k0) // 64).double() + (8 + parts) / 4
+    norm = lambda v: (c * v.double() ** 2).sum(1).sqrt()  # noqa: E731
+    return 4 * 2.0 ** -23 * norm(x)[:, None] * norm(w)[None, :]
+
+
 def scores(l, sigmoid: bool):
     if sigmoid:
         return 1 / (1 + torch.exp(-l))

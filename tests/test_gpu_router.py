@@ -143,6 +143,39 @@ def test_large_batch(rule):
         c.check(slice(lo, lo + 1024))
 
 
+@pytest.mark.parametrize("rule", RULES, ids=NAMES)
+@pytest.mark.parametrize("shape", [(8192, 7168, 256, 8), (2100, 7168, 300, 8), (300, 7168, 256, 8), (1, 7168, 8, 2), (63, 4096, 40, 6),
+                                   (257, 1544, 64, 8), (1000, 264, 130, 3)], ids=lambda s: "-".join(map(str, s)))
+def test_logits_within_their_bound(shape, rule):
+    """What the choice of experts takes a logit to be off by at most is what it is off by at most; and gates are off by what that
+    makes of them: twice a logit's of a normalized gate, or one of a softmax's, once of a plain sigmoid (e^(2 b) - 1 < 2.01 b)."""
+    c = Router(*shape, seed=sum(shape) + 1, **rule).forward()
+    for lo in range(0, c.T, 1024):
+        r = slice(lo, lo + 1024)
+        l = c.x[r].double() @ c.w.double().T
+        bound = ref.logit_bound(c.x[r], c.w, c.T)
+        far = (c.logits[r].double() - l).abs()
+        assert bool((far <= bound).all()), f"{float((far / bound).max()):.3g} of the bound"
+        gates, rel = ref.gates(l, c.idx[r].long(), c.sigmoid, c.norm, c.scale)
+        rel = rel + 2.01 * bound.amax(1, keepdim=True)
+        off = (c.gates[r].double() - gates).abs()
+        assert bool((off <= rel * gates.abs() + 1e-37).all()), f"gates: {float((off / (rel * gates.abs() + 1e-37)).max())}"
+
+
+@pytest.mark.parametrize("shape", [(8192, 7168, 256, 8), (2100, 7168, 300, 8), (300, 7168, 256, 8), (1, 7168, 8, 2), (63, 4096, 40, 6),
+                                   (257, 1544, 64, 8), (65, 7176, 17, 3)], ids=lambda s: "-".join(map(str, s)))
+def test_logits_of_whole_numbers(shape):
+    """Products up to 64 of whole numbers, whose sums are exact in fp32 in any order (7176 64 < 2^24): every bit of the
+    logits, so each product once, in the tail of H and at the borders of its parts too; ids with their ties."""
+    c = Router(*shape, seed=sum(shape) + 2)
+    c.x[:] = torch.randint(-8, 9, c.x.shape, device="cuda", generator=c.gen)
+    c.w[:] = torch.randint(-8, 9, c.w.shape, device="cuda", generator=c.gen) / 64
+    c.forward()
+    l = c.x.double() @ c.w.double().T
+    assert torch.equal(c.logits.double(), l)
+    assert torch.equal(c.idx.long(), ref.choose(l, c.k, False))
+
+
 @pytest.mark.parametrize("rule", RULES[1:3], ids=NAMES[1:3])
 @pytest.mark.parametrize("shape", [(1024, 520, 200, 8), (1041, 1544, 256, 4), (1055, 8, 129, 2), (8200, 4104, 40, 2),
                                    (8207, 4104, 72, 3)], ids=lambda s: "-".join(map(str, s)))

@@ -305,3 +305,18 @@ def test_a_planted_mistake_exceeds_the_bounds():
     dropped[:, -1] = 0
     less, _ = ref.layer(x, idx, dropped, rel.expand_as(gates), *args, 0)
     assert float(((out - less).abs() > bound).double().mean()) > 0.8
+
+
+@pytest.mark.parametrize("T,H", [(300, 7168), (8192, 7168), (64, 1544)])
+def test_a_lost_product_exceeds_the_bound_of_a_logit(T, H):
+    """Four products in five are more than a logit may be off (at H = 7168 it may by 0.06 of their usual size, which the product of
+    two normal numbers is under once in six); sums in fp32, element after element and split alike, are not."""
+    gen = torch.Generator().manual_seed(5)
+    x, w = torch.randn(5, H, generator=gen).to(torch.bfloat16), (torch.randn(3, H, generator=gen) / H ** 0.5).to(torch.bfloat16)
+    bound = ref.logit_bound(x, w, T)
+    products = x.double()[:, None] * w.double()
+    assert float((products.abs() > bound[..., None]).double().mean()) > 0.8
+    in32 = torch.zeros(5, 3)
+    for i in range(H):
+        in32 = in32 + products[..., i].float()
+    assert bool(((in32.double() - products.sum(2)).abs() < bound * 4).all())

@@ -26,7 +26,7 @@ using namespace stream;
 __device__ __forceinline__ double as_double(unsigned bits) { return (double)__uint_as_float(bits); }
 
 // Experts [Experts blockIdx.x, ...) and Tokens tokens a block; its waves share H.  What a number costs is its way
-// to 64 bits, so with many tokens four experts share it (48 tokens, 256 experts, H = 7168: 18 us).
+// to 64 bits, so with many tokens four experts share it (48 tokens, 256 experts, H = 7168: 17 us).
 template <int Tokens, int Experts, int Threads>
 __global__ __launch_bounds__(Threads) void layer_scores_kernel(LayerShape S, Rule rule, const u32x4* x,
                                                                      const u32x4* w, int columns)
@@ -95,9 +95,9 @@ struct LayerSplit {
 constexpr int kMaxExperts = 1024;
 
 // Where there is a wave for each token and expert, and their sums are short, a block of the projections makes the scores
-// itself: one launch less.  Us a call in a graph, with and without: one token, 8 experts, H = 128 13.5 / 15.4, 1024 32.8
-// / 34.6, 4096 30.4 / 31.2; four tokens, 8 experts, H = 1024 36.7 / 36.1, 4096 41.4 / 33.1; one token, 64 experts, H = 512
-// 26.4 / 23.8.
+// itself: one launch less.  Us a call in a graph, with and without (bf16 experts half as wide): one token, 8 experts, H = 128
+// 11.9 / 13.4, 512 13.4 / 15.0, 1024 16.4 / 17.5, 2048 22.7 / 23.1, 4096 37.0 / 35.9; four tokens, 8 experts, H = 1024 20.7 /
+// 18.7, 4096 83 / 70; one token, 64 experts, H = 512 18.1 / 15.1.
 constexpr int kOwnPairs = kWaves;
 constexpr int64_t kOwnProducts = 1 << 15;
 
@@ -531,11 +531,15 @@ hipError_t launch_down(const LayerShape& S, const Rule&, const LayerCall& C, hip
     return hipGetLastError();
 }
 
-// All eight waves share a sum of bf16 weights, whatever its length: us a call with eight ways and with two, one token,
-// 64 experts of 2048 x 1024 28.0 / 58.6, 16 tokens 161 / 177, 64 tokens 184 / 200; one token, 8 of 7168 x 2048 144.7 /
-// 143.7.  Of 4-bit weights, where k is short, two do, unless that leaves half of the card without work: groups of 128,
-// one token, 8 experts of 1024 x 512 13.3 / 18.7, 64 experts of 7168 x 2048 45.5 / 42.7, 16 tokens 316 / 304, 64 tokens,
-// 64 of 2048 x 1024 82.8 / 76.4.  The scales of the features have to fit LDS, or come from memory.
+// A block's eight waves are the ways of a sum of bf16 weights, whatever its length.  They are dealt chunks of 128 k four at
+// a time, so a short sum keeps some of them only: one wave of eight with k up to 512, two up to 1024, four up to 2048; all
+// from 4096 on.  Us a call with eight ways and with two, which are dealt alike: one token, 64 experts of 2048 x 1024 28.0 /
+// 58.6, 16 tokens 161 / 177, 64 tokens 184 / 200; one token, 8 of 7168 x 2048 144.7 / 143.7.  Of 4-bit weights, dealt chunk
+// by chunk, two ways share a sum where k is short, unless that leaves half of the card without work: groups of 128, one
+// token, 8 experts of 1024 x 512 15.2 / 19.8, 64 experts of 7168 x 2048 54.4 / 53.0, 256 of them 53.2 / 50.9, 16 tokens, 64
+// of them 310 / 299, 64 tokens, 64 of 2048 x 1024 82.1 / 75.1; groups of 64 15.3 / 19.9, 56.3 / 55.3, 54.2 / 51.4, 312 / 305,
+// 83.1 / 74.6; groups of 32 15.6 / 20.9, 59.1 / 59.1, 57.4 / 55.6, 332 / 321, 84.8 / 77.5.  (There, as it is, the projections
+// of 7168 k have eight, and the down projection two.)  The scales of the features have to fit LDS, or come from memory.
 constexpr int kFewItems = 128;
 
 template <int Group, int Rows, bool Up>
@@ -567,7 +571,7 @@ hipError_t launch_both(const LayerShape& S, const Rule& rule, const LayerCall& C
 }
 
 // Rows an expert has on average, up to which tiles have 16 of them: two blocks fit a CU then, but an expert with more
-// has its weights read again.  Us a call with 16 and with 32, for 64 experts of 2048 x 1024, 8 of 4096 x 4096 and 16 of
+// has its weights read again.  Where few large bf16 experts have a long sum that is 5 % slower.  Us a call with 16 and with 32, for 64 experts of 2048 x 1024, 8 of 4096 x 4096 and 16 of
 // 2048 x 2048: bf16, 4 rows 172 / 179, 184 / 175, 92 / 94; 10 rows -, 194 / 183, 103 / 105; 12 rows -, 218 / 187, 118 / 106;
 // groups of 128, 4 rows 62 / 73, 55 / 65, 44 / 45; 10 rows -, 65 / 76, 58 / 59; 12 rows -, 80 / 82, 72 / 65.
 constexpr int kRowsOf16 = 10;

@@ -16,8 +16,8 @@
 //
 //   4 2^-23 sqrt(sum_i c_i x_i^2) sqrt(sum_i c_i w_i^2),    c_i = the tiles from k = i on + (8 + splits) / 4
 //
-// The weighted squares come out of the same product for nothing (the fragments are in registers: one of four waves
-// squares a tile of k).  One large product before thousands of 2^-27 of it reaches nine tenths of it.  Of
+// The weighted squares come out of the same product (the fragments are in registers: one of four waves squares a tile of
+// k) for 3 us of the logits' 44 (8192 rows, H = 7168, 256 experts).  One large product before thousands of 2^-27 of it reaches nine tenths of it.  Of
 // the k + 1 largest keys those whose order that bound leaves open are summed again, in 64 bits, by the whole block.
 #include <math.h>
 
@@ -281,7 +281,8 @@ struct Own {
 
 constexpr int kAgain = 16;  // candidates of a row that are summed again, at most; with more, all its experts are
 
-// A wave a row; Each logits a lane.
+// A wave a row; Each logits a lane.  Eight waves a SIMD, so that all blocks of 8192 rows are on the card at once: 30 us
+// (256 experts, H = 7168), and 35 without that bound, though it costs some spills.
 template <int Each>
 __global__ __launch_bounds__(kChooseWaves * kWave, Each <= 4 ? 8 : 1) void router_choose_kernel(RouterShape S, Rule rule, Cut cut, Partial P,
                                                                              ChooseArgs A, GridSpan span)
@@ -862,9 +863,10 @@ __global__ __launch_bounds__(256) void router_join_kernel(const f32x4* parts, in
 
 constexpr int kMaxSplits = 16;
 
-// Whether grad_x is made in stripes.  dlogits and grad_x, us, in stripes and by tiles: H = 7168, 256 experts, 1024 rows 21 /
-// 23, 2048 31 / 36, 8192 81 / 108; H = 4096, 128 experts, 4096 rows 31 / 28, 8192 47 / 52; 8 experts, 4096 rows 25 / 24,
-// 8192 40 / 41; H = 2048, 64 experts, 8192 rows 29 / 25, 32768 84 / 91.
+// Whether grad_x is made in stripes.  dlogits and grad_x, us, in stripes and by tiles: 256 experts, H = 7168, 1024 rows 20 /
+// 21, 2048 26 / 34, 8192 61 / 99; H = 4096 17 / 15, 23 / 21, 56 / 62; H = 2048 14 / 15, 17 / 15, 36 / 37; H = 1024 13 / 16, 14 /
+// 16, 24 / 25; 160 experts, 8192 rows, H = 7168 56 / 88, 4096 48 / 55, 1024 22 / 23; H = 4096, 128 experts, 4096 rows 31 / 28,
+// 8192 47 / 52; 8 experts, 4096 rows 25 / 24, 8192 40 / 41; H = 2048, 64 experts, 8192 rows 29 / 25, 32768 84 / 91.
 bool in_stripes(const RouterShape& S)
 {
     if (S.E > 256) return false;

@@ -79,7 +79,8 @@ class AdamwTensors:
       m_out, v_out  values of 8-bit states, for moe_adamw_pack and moe_adamw_unpack
 
     Shapes are free: a tensor is its elements in memory order, and they must be contiguous.  All tensors of a kind
-    have one type.  The list holds its tensors; a program keeps it as long as their memory stays the same.
+    have one type.  The list holds its tensors; a program keeps it as long as their memory stays the same.  Making it
+    takes the host 6 to 10 us a tensor, which a program whose gradients are new tensors in each step pays each time.
     """
 
     def __init__(self, tensors):

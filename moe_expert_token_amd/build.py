@@ -25,6 +25,7 @@ HIPCC_FLAGS = [
     "-ffp-contract=off", "-fno-gpu-flush-denormals-to-zero",
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-Wall", "-Wno-unused-result",
+    "-Werror=pass-failed",  # a kernel that misses the occupancy its launch bounds ask for
 ]
 
 

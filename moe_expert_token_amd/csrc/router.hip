@@ -91,6 +91,7 @@ __global__ __launch_bounds__(kGemmThreads, MF <= 2 ? 4 : 2) void router_logits_k
     constexpr bool kSmall = MF <= 2;
     constexpr int kTokens = 32 * MF;
     __shared__ __align__(1024) char lds[Lds<kSmall>::kBytes];
+    static_assert((4 * kTokens + 2 * kTileFeatures + 16) * 4 <= sizeof(lds), "room for the squares");
     // the parts of H vary fastest: with 1, 2, 4 or 8 of them an XCD's L2 holds one part of the weights, not all
     const int b = span_block(span), part = b % cut.splits, at = b / cut.splits, tile = at % tiles;
     const int t0 = tile * kTokens, e0 = at / tiles * kTileFeatures, k0 = part * cut.each;
@@ -147,7 +148,14 @@ __global__ __launch_bounds__(kGemmThreads, MF <= 2 ? 4 : 2) void router_logits_k
             const u32x4 a = *(const u32x4*)(w + ((int64_t)(e0 + v / V) * S.H + k0 + v % V * 8) * 2);
             any |= (a[0] | a[1] | a[2] | a[3]) & 0x7fff7fffu;
         }
-        if (__syncthreads_or(any != 0)) top = 1e-30f;
+        // joined here: a block-wide vote of the library's takes 256 bytes of LDS, with which no two small tiles fit a CU
+        int* const some = (int*)lds + 4 * kTokens + 2 * kTileFeatures + 8;
+        const bool its = __ballot(any != 0) != 0;
+        if (lane == 0) some[wave] = its;
+        __syncthreads();
+#pragma unroll
+        for (int v = 0; v < kGemmThreads / kWave; ++v)
+            if (some[v]) top = 1e-30f;
     }
     if (i == 0) P.w2[part * across + e0 / kTileFeatures] = top;
 }
@@ -878,8 +886,9 @@ int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 Cut cut_of(const RouterShape& S)
 {
     Cut c;
-    // tiles of 128 rows against 64, both kernels, us: H = 7168, 256 experts: 1024 rows 49 / 48, 2048 51 / 54, 8192 73 / 79;
-    // H = 4096, 128 experts: 2048 rows 37 / 37, 4096 34 / 35, 16384 69 / 75
+    // tiles of 128 rows against 64, both kernels, us: H = 7168, 256 experts: 512 rows 29 / 25, 1024 35 / 32, 2048 35 / 36,
+    // 8192 63 / 68, 16384 108 / 123; 1000 experts: 1024 rows 52 / 50, 2048 60 / 63, 16384 335 / 366; H = 4096, 128 experts:
+    // 1024 rows 23 / 21, 2048 28 / 27, 4096 31 / 30, 16384 66 / 65
     c.tokens = S.T >= 2048 ? 128 : 64;
     const int64_t tiles = up(S.T, c.tokens) * up(S.E, kTileFeatures);
     const int kBlocks = c.tokens > 64 ? 256 : 512;

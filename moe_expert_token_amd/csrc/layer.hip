@@ -571,9 +571,10 @@ hipError_t launch_both(const LayerShape& S, const Rule& rule, const LayerCall& C
 }
 
 // Rows an expert has on average, up to which tiles have 16 of them: two blocks fit a CU then, but an expert with more
-// has its weights read again.  Where few large bf16 experts have a long sum that is 5 % slower.  Us a call with 16 and with 32, for 64 experts of 2048 x 1024, 8 of 4096 x 4096 and 16 of
-// 2048 x 2048: bf16, 4 rows 172 / 179, 184 / 175, 92 / 94; 10 rows -, 194 / 183, 103 / 105; 12 rows -, 218 / 187, 118 / 106;
-// groups of 128, 4 rows 62 / 73, 55 / 65, 44 / 45; 10 rows -, 65 / 76, 58 / 59; 12 rows -, 80 / 82, 72 / 65.
+// has its weights read again.  Us a call with 16 and with 32, for 64 experts of 2048 x 1024, 8 of 4096 x 4096 (where the
+// rule loses 5 % in bf16) and 16 of 2048 x 2048: bf16, 4 rows 172 / 179, 184 / 175, 92 / 94; 10 rows -, 194 / 183, 103 / 105;
+// 12 rows -, 218 / 187, 118 / 106; groups of 128, 4 rows 62 / 73, 55 / 65, 44 / 45; 10 rows -, 65 / 76, 58 / 59; 12 rows -, 80 /
+// 82, 72 / 65.
 constexpr int kRowsOf16 = 10;
 
 template <int Group>
